@@ -220,6 +220,98 @@ int lrhead_factor(const void* W, int64_t V, int64_t d, int r, int q,
                   size_t workspace_bytes, void* stream);
 
 /*
+ * Distillation of a low-rank head from a teacher's top logits: the loss, and
+ * what its gradients need. For N rows Z (N x r) of the student and its head
+ * P (V x r), both in `dtype`, and the k teacher places of each row (idx and
+ * logits: N x k, as fullhead_topk writes them):
+ *   s_n[v] = P[v,:] . z_n,  q_n = softmax(s_n / T) over all V,
+ *   p_n    = softmax(logits_n / T) over the row's places,
+ *   loss[n] = sum_j p_nj (log p_nj - s_n[idx_nj] / T) + lse[n],
+ *   lse[n]  = log sum_v exp(s_n[v] / T),
+ *   grad[n] = dloss[n]/dz_n = (sum_v q_n[v] P[v,:] - sum_j p_nj P[idx_nj,:]) / T.
+ * A place whose id lies outside [0, V), or whose logit is NaN or -inf, is
+ * empty; a row of empty places has loss 0 and gradient 0. An id that occurs
+ * twice in a row counts twice. Ids need no order. The scores are never
+ * stored; they, the sums and the statistics are fp32 (bf16: the weights q
+ * of the gradients are rounded to bf16, products and sums are fp32). With
+ * grad == NULL the call computes loss and lse alone, at half the work.
+ * loss, lse: N fp32; grad: N x r fp32. T = temperature > 0.
+ *
+ * lrhead_distill_grad: with the rows' weights w (N fp32: the gradient that
+ * arrives at loss; NULL: 1), the lse and grad of lrhead_distill on the same
+ * inputs, and c_n = w[n] / T,
+ *   dZ[n,:] = w[n] grad[n,:],
+ *   dP[v,:] = sum_n c_n (q_n[v] - sum_{j: idx_nj = v} p_nj) z_n,
+ * both written whole, in `dtype`. Either may be NULL (grad too, without dZ).
+ * A row of weight 0 contributes nothing, whatever its Z holds. The results
+ * do not vary from call to call.
+ *
+ * Requirements: 1 <= V < 2^31, r as for lrhead_create, 0 <= N <= 2^20,
+ * 1 <= k <= 64, and a workspace of lrhead_distill_workspace_bytes bytes (0:
+ * invalid sizes), whose contents need not survive between the calls. N == 0
+ * writes no row, but dP (zeros).
+ */
+size_t lrhead_distill_workspace_bytes(int dtype, int64_t V, int64_t r, int64_t N, int k);
+int lrhead_distill(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N,
+                   const int32_t* idx, const float* logits, int k, float temperature,
+                   float* loss, float* lse, float* grad, void* workspace,
+                   size_t workspace_bytes, void* stream);
+int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N,
+                        const int32_t* idx, const float* logits, int k, float temperature,
+                        const float* lse, const float* grad, const float* weight, void* dZ,
+                        void* dP, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Beam search's selection ("EAGLE-4 Triples Qwen3 Inference Speed by Adapting
+ * to Serving Load", section "Runtime-sized speculation": several branches per
+ * node draft a tree; here the nb best paths of all of a sequence's nodes).
+ * For B sequences of m beams with path scores `score` (B x m fp32, log
+ * probabilities; -inf: no beam) and logits (B x m rows of n columns in
+ * `dtype`, `ld` elements from row to row): the nb largest of
+ *   score[b, i] + logits[b, i, v] - log sum_u exp(logits[b, i, u])
+ * over beams i and columns v, larger first, ties to the lower beam, then the
+ * lower column. out_score[b, j] is that total, out_beam[b, j] the beam i, and
+ * out_token[b, j] the column v, or with idx (B x m x n int32, the ids of
+ * candidate lists) idx[b, i, v]. A logit that is NaN or -inf, or has a
+ * negative id, is no candidate and has no share of the sum. With `ended`
+ * (B x m bytes), a beam whose byte is not 0 has one continuation: end_id,
+ * at its score. Slots past the last candidate hold -inf, -1 and -1. Totals
+ * are formed in fp64 (the sum of exponentials to about 1e-7). A logit or
+ * score of +inf gives undefined ids.
+ * Requirements: 1 <= m, nb <= 64, 1 <= n < 2^31, ld >= n, B >= 0. `logits`
+ * need only be aligned to its elements; the workspace has at least
+ * lrhead_beam_workspace_bytes bytes (0: invalid sizes).
+ */
+size_t lrhead_beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb);
+int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t* idx,
+                       const float* score, const uint8_t* ended, int end_id, int64_t B, int m,
+                       int64_t n, int nb, float* out_score, int32_t* out_beam, int32_t* out_token,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves the beams' states behind a selection: for each of n_states states
+ * (`states` is a HOST array), dst[b, j] = src[b, parent[b, j]]. A state holds,
+ * per beam, segs x positions x position_bytes contiguous bytes; src has m
+ * beams per sequence, dst has nb. With `length` (B int32), only the first
+ * length[b] positions of each segment are moved (clamped to [0, positions]);
+ * the others keep what dst held, and so do slots whose parent lies outside
+ * [0, m). Requirements: m, nb >= 1; B, n_states, segs, positions,
+ * position_bytes >= 0; no dst may overlap another dst or any src
+ * (LRHEAD_EINVAL). src and dst may have any alignment; 16 bytes in
+ * addresses and sizes are fastest. n_states <= LRHEAD_STATES_MAX.
+ */
+#define LRHEAD_STATES_MAX 1024
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t segs;
+  int64_t positions;
+  int64_t position_bytes;
+} lrhead_state_t;
+int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* parent,
+                   const int32_t* length, int64_t B, int m, int nb, void* stream);
+
+/*
  * Profiling aid: hipEvent_t handles (passed as void*) that later calls on
  * this handle attach to the dispatch of the vocabulary score pass
  * (lrhead_candidates, lrhead_draft, fullhead_topk; for row batches its main

@@ -16,6 +16,14 @@ FP32 = 1
 OK, EINVAL, ERANGE, EDTYPE, EALIGN, EWORKSPACE, EHIP, EDEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 K_MAX, R_MAX, D_MAX = 64, 512, 65536
 STATIC_SCRATCH_BYTES = 64 << 20   # LRHEAD_STATIC_SCRATCH_MB
+STATES_MAX = 1024
+
+
+class State(ctypes.Structure):
+    """lrhead_state_t"""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("segs", ctypes.c_int64),
+                ("positions", ctypes.c_int64), ("position_bytes", ctypes.c_int64)]
+
 
 _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -35,6 +43,15 @@ SIGNATURES = {
     "lrhead_factor_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, ctypes.c_int]),
     "lrhead_factor": (ctypes.c_int, [_vp, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
                                      ctypes.c_size_t, _vp]),
+    "lrhead_distill_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64, ctypes.c_int]),
+    "lrhead_distill": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp, _vp, ctypes.c_int,
+                                      ctypes.c_float, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lrhead_distill_grad": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp, _vp, ctypes.c_int,
+                                           ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lrhead_beam_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, ctypes.c_int, _c_i64, ctypes.c_int]),
+    "lrhead_beam_select": (ctypes.c_int, [ctypes.c_int, _vp, _c_i64, _vp, _vp, _vp, ctypes.c_int, _c_i64, ctypes.c_int,
+                                          _c_i64, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lrhead_reorder": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _c_i64, ctypes.c_int, ctypes.c_int, _vp]),
     "lrhead_set_stage_events": (ctypes.c_int, [_vp, _vp, _vp]),
     "lrhead_destroy": (None, [_vp]),
     "lrhead_strerror": (ctypes.c_char_p, [ctypes.c_int]),

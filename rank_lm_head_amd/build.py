@@ -23,7 +23,7 @@ PROBE_LIB = os.path.join(PKG, "libprobe.so")   # measurement only, not the head'
 PROBE_SOURCE = "probe_read.hip"
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["kernels_small.hip", "kernels_mfma.hip", "kernels_gemm.hip", "kernels_merge.hip", "kernels_branch.hip",
-           "kernels_factor.hip", "kernels_b1.hip", "lrhead.hip"]
+           "kernels_factor.hip", "kernels_b1.hip", "kernels_distill.hip", "kernels_beam.hip", "lrhead.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,1005 @@
+// kernels_distill.hip — distillation of the low-rank head from a teacher's
+// top logits: the loss and its gradients.
+//
+// For N rows z_n of the student (length r) and its head P (V x r), with a
+// temperature T and the k teacher places (id, t) of each row:
+//   q_n = softmax(P . z_n / T) over the whole vocabulary,
+//   p_n = softmax(t / T) over the row's places that are not empty,
+//   loss_n   = sum_j p_nj (log p_nj - s_nj / T) + lse_n,   s_nj = P[id_j] . z_n
+//   dloss_n/dz_n = (sum_v q_nv P_v - sum_j p_nj P[id_j]) / T
+//   dP       = sum_n w_n / T (q_n - p_n) z_n^T             (w: the rows' weights)
+//
+// The scores (N x V; 2.5 GB in fp32 at 4096 rows of a 151936-token
+// vocabulary) are never stored: both passes keep one side in registers,
+// stream the other through LDS and use each tile of scores where it is
+// made. With X the side at rest and Y the streamed one, both compute
+//   S = Y . X^T,   E = exp2(S log2(e)/T - c),   A += Y^T . E
+//   rows pass    (X = Z, Y = P): c = the running maximum of the row of Z; A is
+//                the unnormalised sum_v q_v P_v, an attention over the
+//                vocabulary whose keys and values are both P;
+//   columns pass (X = P, Y = Z): c = lse_n - log(|w_n|/T), so E is already
+//                |w_n| q_nv / T and A the dense part of dP.
+// The matrix cores leave S with its X row in the lane and its Y rows in the
+// lane's registers, which is (up to an order of the contracted index that
+// the other operand follows) the layout in which E is the right operand of
+// the second product: E never leaves the registers.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "device.h"
+#include "launch.h"
+#include "topk.h"
+
+namespace lrh {
+
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kRawBufferFlags = 0x00020000;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum of a row moves only when a score passes it by more
+// than 2^kSlack: E stays below 2^kSlack, sums keep their relative precision
+// (fp32 and bf16 have range to spare) and most tiles need no rescaling.
+constexpr float kSlack = 8.f;
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Two fp32 as packed bf16, each rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x2 v;
+  v[0] = (__bf16)lo;
+  v[1] = (__bf16)hi;
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+struct StreamArgs {
+  const void* X;        // nx x r, at rest in registers
+  const void* Y;        // ny x ldy (r columns used), streamed
+  int64_t nx, ny;
+  int r, ldy;
+  float scale;          // log2(e) / T
+  int splits;           // shares of Y, one block each
+  // rows pass: a share's maximum (log2 domain), sum and weighted sum of P
+  float* pm;            // [share][nx]
+  float* pl;
+  float* po;            // [share][nx][RP]
+  // columns pass
+  const float* beta;    // [ny]: c, +inf for rows without weight
+  const float* sgn;     // [ny]: the weight's sign
+  const uint32_t* list_start;   // [groups + 1]: a group of columns' teacher places in `list`
+  const uint2* list;    // (row | local column << kRowBits, bits of w p / T), by row within a group
+  const void* Z;        // N x r, for the teacher places
+  void* dP;             // V x r, with one share
+  float* part;          // [share][nx][RP], with more
+};
+constexpr int kRowBits = 20;   // N <= 2^20
+constexpr uint32_t kRowMask = (1u << kRowBits) - 1;
+
+// 16-byte chunk c of row y of an LDS tile sits at chunk c ^ swz_row(y). A wave
+// reads the tile as the left operand of S (32 rows, one chunk each) and,
+// transposed, of A (4 rows, 4 neighbouring chunks each); the two low row
+// bits go to the high chunk bits so that both spread over all banks.
+template <int RP>
+__device__ __forceinline__ int swz_row(int y) {
+  if constexpr (RP >= 128) return ((y & 3) << 2) | ((y >> 2) & 3);
+  else if constexpr (RP == 64) return (((y >> 1) & 1) << 2) | ((y >> 2) & 3);
+  else return (y >> 2) & 3;
+}
+
+// Rows of a tile: 32 for each of the waves that share one out, and at least
+// 16 KiB.
+template <int RP, int WX>
+constexpr int bf16_tile_rows() {
+  const int rows = 32 * (kWaves / WX);
+  return rows < (RP <= 128 ? 64 : 32) ? (RP <= 128 ? 64 : 32) : rows;
+}
+// LDS of a block: two tiles and, for the columns pass, two sets of row values.
+template <int RP, int WX>
+constexpr int bf16_lds_bytes() { return 2 * bf16_tile_rows<RP, WX>() * (RP * 2 + 8); }
+
+// Streams rows [tile * TY, ...) of Y into an LDS tile, zeros past the matrix
+// and past r columns.
+template <int RP, int TY>
+struct TileCopy {
+  static constexpr int kChunks = RP / 8;
+  static constexpr int kLoads = TY * kChunks / (kWaves * kWave);
+  uint32_t off[kLoads];
+  const char* base;
+  int64_t rows;
+  uint32_t row_bytes;
+
+  __device__ __forceinline__ void init(const void* Y, int64_t ny, int r, int ldy) {
+    const int wave = wave_id(), lane = threadIdx.x & 63;
+    base = static_cast<const char*>(Y);
+    rows = ny;
+    row_bytes = (uint32_t)ldy * 2u;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int p = (i * kWaves + wave) * kWave + lane;
+      const int row = p / kChunks, c = (p % kChunks) ^ swz_row<RP>(row);
+      off[i] = c * 8 < r ? (uint32_t)row * row_bytes + (uint32_t)c * 16u : 0x7ffffff0u;
+    }
+  }
+  __device__ __forceinline__ void issue(uint16_t* tile, int64_t t) const {
+    const int wave = wave_id();
+    const int64_t row0 = t * TY;
+    const uint32_t bytes = (uint32_t)min(rows - row0, (int64_t)TY) * row_bytes;
+    const uint64_t addr = reinterpret_cast<uint64_t>(base) + (uint64_t)row0 * row_bytes;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)addr);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(addr >> 32));
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), (short)0,
+                                          __builtin_amdgcn_readfirstlane((int)bytes), kRawBufferFlags);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(tile + (i * kWaves + wave) * kWave * 8), 16,
+                                               (int)off[i], 0, 0, 0);
+  }
+};
+
+// bf16. RP: r rounded up to a tile size; a wave owns XT * 32 rows of X, WX of
+// the block's four waves sit side by side on X and 4 / WX share out a
+// tile's rows of Y.
+template <int RP, int XT, int WX, bool ACC, bool COLS>
+__global__ void __launch_bounds__(kWaves* kWave, 1) stream_bf16_kernel(StreamArgs a) {
+  constexpr int TY = bf16_tile_rows<RP, WX>();
+  constexpr int KS = RP / 16, RT = RP / 32, WY = kWaves / WX;
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  float* const rows = reinterpret_cast<float*>(lds + 2 * TY * RP);   // [buffer][offset, sign][TY]
+  const int lane = threadIdx.x & 63, h = lane >> 5, wave = wave_id();
+  const int wx = wave % WX, wy = wave / WX;
+  const int64_t xtile = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits;
+  const int64_t x0 = (xtile * WX + wx) * (32 * XT);
+
+  bf16x8 X[XT][KS];
+#pragma unroll
+  for (int xt = 0; xt < XT; ++xt) {
+    const int64_t x = x0 + xt * 32 + (lane & 31);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = ks * 16 + h * 8;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (x < a.nx && c < a.r) v = load16(static_cast<const uint16_t*>(a.X) + x * a.r + c);
+      X[xt][ks] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+
+  f32x16 acc[XT][ACC ? RT : 1] = {};
+  float m[XT], l[XT];
+#pragma unroll
+  for (int xt = 0; xt < XT; ++xt) {
+    m[xt] = neg_inf();
+    l[xt] = 0.f;
+  }
+
+  const int64_t nt = (a.ny + TY - 1) / TY;
+  const int64_t t_begin = nt * split / a.splits, t_end = nt * (split + 1) / a.splits;
+  TileCopy<RP, TY> copy;
+  copy.init(a.Y, a.ny, a.r, a.ldy);
+
+  const auto stage_rows = [&](int buf, int64_t t) {
+    if constexpr (COLS) {
+      if ((int)threadIdx.x < TY) {
+        const int64_t y = t * TY + threadIdx.x;
+        rows[buf * 2 * TY + threadIdx.x] = y < a.ny ? a.beta[y] : __builtin_inff();
+        rows[buf * 2 * TY + TY + threadIdx.x] = y < a.ny ? a.sgn[y] : 1.f;
+      }
+    }
+  };
+  if (t_begin < t_end) {
+    copy.issue(lds, t_begin);
+    stage_rows(0, t_begin);
+  }
+  for (int64_t t = t_begin; t < t_end; ++t) {
+    const int buf = (int)(t - t_begin) & 1;
+    __builtin_amdgcn_s_waitcnt(0xF70);   // vmcnt(0): this wave's share of tile t has landed
+    __syncthreads();                      // everyone's has, and every wave is done with the other buffer
+    if (t + 1 < t_end) {
+      copy.issue(lds + (buf ^ 1) * TY * RP, t + 1);
+      stage_rows(buf ^ 1, t + 1);
+    }
+    const uint16_t* tile = lds + buf * TY * RP;
+    const float* row_c = rows + buf * 2 * TY;
+    const float* row_s = row_c + TY;
+#pragma unroll 1
+    for (int sub = wy; sub < TY / 32; sub += WY) {
+      const int64_t y0 = t * TY + sub * 32;
+      if (y0 >= a.ny) break;
+      f32x16 S[XT] = {};
+      {
+        const int row = sub * 32 + (lane & 31);
+        const int f = swz_row<RP>(row);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const bf16x8 A = __builtin_bit_cast(bf16x8, load16(tile + row * RP + ((ks * 2 + h) ^ f) * 8));
+#pragma unroll
+          for (int xt = 0; xt < XT; ++xt)
+            S[xt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, X[xt][ks], S[xt], 0, 0, 0);
+        }
+      }
+      if constexpr (COLS) {
+        f32x4 c[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) c[g] = *reinterpret_cast<const f32x4*>(&row_c[sub * 32 + g * 8 + h * 4]);
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) S[xt][i] = exp2_hw(fmaf(S[xt][i], a.scale, -c[i >> 2][i & 3]));
+        if (__ballot(row_s[sub * 32 + (lane & 31)] < 0.f)) {   // rare: rows with a negative weight
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 s = *reinterpret_cast<const f32x4*>(&row_s[sub * 32 + g * 8 + h * 4]);
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) S[xt][g * 4 + i] *= s[i];
+          }
+        }
+      } else {
+        if (y0 + 32 > a.ny) {   // the vocabulary ends inside this tile
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (y0 + (i >> 2) * 8 + h * 4 + (i & 3) >= a.ny)
+#pragma unroll
+              for (int xt = 0; xt < XT; ++xt) S[xt][i] = neg_inf();
+        }
+        float top[XT];
+        bool move = false;
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+          float v = S[xt][0];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) v = fmaxf(v, S[xt][i]);
+          top[xt] = v * a.scale;
+          move |= top[xt] > m[xt] + kSlack;
+        }
+        if (__ballot(move)) {
+#pragma unroll
+          for (int xt = 0; xt < XT; ++xt) {
+            const float mn = fmaxf(m[xt], fmaxf(top[xt], __shfl_xor(top[xt], 32)));
+            const float s = mn == m[xt] ? 1.f : exp2_hw(m[xt] - mn);
+            m[xt] = mn;
+            l[xt] *= s;
+            if constexpr (ACC) {
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) acc[xt][rt] *= s;
+            }
+          }
+        }
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            S[xt][i] = exp2_hw(fmaf(S[xt][i], a.scale, -m[xt]));
+            part[i & 3] += S[xt][i];
+          }
+          l[xt] += (part[0] + part[1]) + (part[2] + part[3]);
+        }
+      }
+      if constexpr (ACC) {
+        // E as the right operand. It is rounded to bf16 here (off by at most
+        // 2^-9 of itself, nearest even); products and sums stay in fp32.
+        bf16x8 E[XT][2];
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+          for (int s2 = 0; s2 < 2; ++s2) {
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = pack_bf16(S[xt][s2 * 8 + i * 2], S[xt][s2 * 8 + i * 2 + 1]);
+            E[xt][s2] = __builtin_bit_cast(bf16x8, v);
+          }
+        // Y^T by transposing LDS reads: 16 lanes read 4 rows of 16 columns
+        // (lane i row i / 4, columns 4 (i % 4)..) and each receives a column.
+        const int q = (lane & 15) >> 2;
+        const int cl = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // the lane's chunk within 4
+        const int half = (lane & 1) * 4;
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+          const int ra = sub * 32 + s2 * 16 + h * 4 + q, rb = ra + 8;
+          const int fa = swz_row<RP>(ra), fb = swz_row<RP>(rb);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const uint16_t* pa = tile + ra * RP + ((rt * 4 + cl) ^ fa) * 8 + half;
+            const uint16_t* pb = tile + rb * RP + ((rt * 4 + cl) ^ fb) * 8 + half;
+            const s16x4 va = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)pa);
+            const s16x4 vb = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)pb);
+            typedef short s16x8 __attribute__((ext_vector_type(8)));
+            const s16x8 v = {va[0], va[1], va[2], va[3], vb[0], vb[1], vb[2], vb[3]};
+            const bf16x8 A = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt)
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, E[xt][s2], acc[xt][rt], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+
+  if constexpr (COLS) {
+    if (split == 0 && x0 < a.nx) {
+      // The teacher's part of this wave's columns: -w p / T z_n for every
+      // place. Eight places make one step of the contraction: the left
+      // operand gathers their rows of Z, the right one holds their weight in
+      // their column, as the sum of two bf16 (one per half of the wave's
+      // k slots), within 2^-17 of it.
+      const int64_t g = x0 / (32 * XT);
+      const uint32_t e1 = a.list_start[g + 1];
+      const uint16_t* Z = static_cast<const uint16_t*>(a.Z);
+      for (uint32_t e0 = a.list_start[g]; e0 < e1; e0 += 8) {
+        bf16x8 B[XT];
+        int64_t zrow[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint2 en = a.list[min(e0 + e, e1 - 1)];
+          const float w = e0 + e < e1 ? -__uint_as_float(en.y) : 0.f;
+          const float hi = bf16_to_f32(f32_to_bf16(w));
+          const float v = h ? w - hi : hi;
+          zrow[e] = (int64_t)(en.x & kRowMask) * a.r;
+#pragma unroll
+          for (int xt = 0; xt < XT; ++xt)
+            B[xt][e] = (__bf16)((int)(en.x >> kRowBits) == xt * 32 + (lane & 31) ? v : 0.f);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int c = rt * 32 + (lane & 31);
+          typedef short s16x8 __attribute__((ext_vector_type(8)));
+          s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+          if (c < a.r) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (short)Z[zrow[e] + c];
+          }
+          const bf16x8 A = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+          for (int xt = 0; xt < XT; ++xt)
+            acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, B[xt], acc[xt][rt], 0, 0, 0);
+        }
+      }
+    }
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) {
+      const int64_t x = x0 + xt * 32 + (lane & 31);
+      if (x >= a.nx) continue;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = rt * 32 + g * 8 + h * 4;
+          const f32x4 v = {acc[xt][rt][g * 4], acc[xt][rt][g * 4 + 1], acc[xt][rt][g * 4 + 2],
+                           acc[xt][rt][g * 4 + 3]};
+          if (a.splits > 1) {
+            *reinterpret_cast<f32x4*>(a.part + ((int64_t)split * a.nx + x) * RP + c) = v;
+          } else if (c < a.r) {
+            const uint2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dP) + x * a.r + c) = b;
+          }
+        }
+    }
+  } else {
+    const int64_t share = (int64_t)split * WY + wy;
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) {
+      const int64_t x = x0 + xt * 32 + (lane & 31);
+      const float lt = l[xt] + __shfl_xor(l[xt], 32);
+      if (x >= a.nx) continue;
+      if (h == 0) {
+        a.pm[share * a.nx + x] = m[xt];
+        a.pl[share * a.nx + x] = lt;
+      }
+      if constexpr (ACC) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 v = {acc[xt][rt][g * 4], acc[xt][rt][g * 4 + 1], acc[xt][rt][g * 4 + 2],
+                             acc[xt][rt][g * 4 + 3]};
+            *reinterpret_cast<f32x4*>(a.po + (share * a.nx + x) * RP + rt * 32 + g * 8 + h * 4) = v;
+          }
+      }
+    }
+  }
+}
+
+// fp32, on v_mfma_f32_16x16x4_f32: a wave owns 16 rows of X, the block 64.
+// A tile holds 16 rows of Y, each padded by 4 words so that both reads of
+// it (rows as the left operand of S, columns as that of A) spread over the
+// banks.
+template <int RP, bool ACC, bool COLS>
+__global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs a) {
+  constexpr int TY = 16, LD = RP + 4, KC = RP / 16, RT = RP / 16;
+  __shared__ __attribute__((aligned(16))) float tile[TY * LD];
+  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15, wave = wave_id();
+  const int64_t xtile = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits;
+  const int64_t x0 = (xtile * kWaves + wave) * 16;
+  const int64_t x = x0 + col;
+  const float* Yp = static_cast<const float*>(a.Y);
+
+  f32x4 X[KC];
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const int kk = c * 16 + g * 4;
+    X[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (x < a.nx && kk < a.r) X[c] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.X) + x * a.r + kk);
+  }
+  f32x4 acc[ACC ? RT : 1] = {};
+  float m = neg_inf(), l = 0.f;
+
+  const int64_t nt = (a.ny + TY - 1) / TY;
+  const int64_t t_begin = nt * split / a.splits, t_end = nt * (split + 1) / a.splits;
+  for (int64_t t = t_begin; t < t_end; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TY * RP / 4; i += kWaves * kWave) {
+      const int p = i + threadIdx.x;
+      const int row = p / (RP / 4), c = (p % (RP / 4)) * 4;
+      const int64_t y = t * TY + row;
+      if (p < TY * RP / 4) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (y < a.ny && c < a.r) v = *reinterpret_cast<const f32x4*>(Yp + y * a.ldy + c);
+        *reinterpret_cast<f32x4*>(tile + row * LD + c) = v;
+      }
+    }
+    __syncthreads();
+    const int64_t y0 = t * TY;
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const f32x4 A = *reinterpret_cast<const f32x4*>(tile + col * LD + c * 16 + g * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S = __builtin_amdgcn_mfma_f32_16x16x4f32(A[j], X[c][j], S, 0, 0, 0);
+    }
+    if constexpr (COLS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t y = y0 + g * 4 + i;
+        S[i] = y < a.ny ? a.sgn[y] * exp2_hw(fmaf(S[i], a.scale, -a.beta[y])) : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (y0 + g * 4 + i >= a.ny) S[i] = neg_inf();
+      const float top = fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3])) * a.scale;
+      if (__ballot(top > m + kSlack)) {
+        float mn = fmaxf(top, __shfl_xor(top, 16));
+        mn = fmaxf(m, fmaxf(mn, __shfl_xor(mn, 32)));
+        const float s = mn == m ? 1.f : exp2_hw(m - mn);
+        m = mn;
+        l *= s;
+        if constexpr (ACC) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) acc[rt] *= s;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[i] = exp2_hw(fmaf(S[i], a.scale, -m));
+      l += (S[0] + S[1]) + (S[2] + S[3]);
+    }
+    if constexpr (ACC) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(tile[(g * 4 + i) * LD + rt * 16 + col], S[i], acc[rt], 0, 0, 0);
+    }
+  }
+
+  if constexpr (COLS) {
+    if (split == 0 && x0 < a.nx) {
+      const uint32_t e1 = a.list_start[x0 / 16 + 1];
+      const float* Z = static_cast<const float*>(a.Z);
+      for (uint32_t e0 = a.list_start[x0 / 16]; e0 < e1; e0 += 4) {   // four places a step
+        const uint2 en = a.list[min(e0 + g, e1 - 1)];
+        const bool mine = e0 + g < e1 && (int)(en.x >> kRowBits) == col;
+        const float B = mine ? -__uint_as_float(en.y) : 0.f;
+        const float* z = Z + (int64_t)(en.x & kRowMask) * a.r;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int c = rt * 16 + col;
+          acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(c < a.r ? z[c] : 0.f, B, acc[rt], 0, 0, 0);
+        }
+      }
+    }
+    if (x >= a.nx) return;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int c = rt * 16 + g * 4;
+      if (a.splits > 1) *reinterpret_cast<f32x4*>(a.part + ((int64_t)split * a.nx + x) * RP + c) = acc[rt];
+      else if (c < a.r) *reinterpret_cast<f32x4*>(static_cast<float*>(a.dP) + x * a.r + c) = acc[rt];
+    }
+  } else {
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (x >= a.nx) return;
+    if (g == 0) {
+      a.pm[(int64_t)split * a.nx + x] = m;
+      a.pl[(int64_t)split * a.nx + x] = l;
+    }
+    if constexpr (ACC) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        *reinterpret_cast<f32x4*>(a.po + ((int64_t)split * a.nx + x) * RP + rt * 16 + g * 4) = acc[rt];
+    }
+  }
+}
+
+// ----------------------------------------------------------- teacher places
+
+template <typename T> __device__ __forceinline__ float widen(T x);
+template <> __device__ __forceinline__ float widen<uint16_t>(uint16_t x) { return bf16_to_f32(x); }
+template <> __device__ __forceinline__ float widen<float>(float x) { return x; }
+
+// The teacher's distribution over a row's places, lane j holding place j: a
+// place is empty (p = 0, id = INT_MAX) when its id lies outside [0, V) or its
+// logit is NaN or -inf. logp is log p where p > 0. Returns whether the row
+// has a place at all.
+__device__ __forceinline__ bool teacher(const int32_t* idx, const float* t, int64_t row, int k, int64_t V, float inv_t,
+                                        int& id, float& p, float& logp) {
+  const int lane = threadIdx.x & 63;
+  id = lane < k ? idx[row * k + lane] : -1;
+  const float x = lane < k ? t[row * k + lane] * inv_t : 0.f;
+  const bool real = id >= 0 && id < V && x > neg_inf();
+  const uint32_t mk = wave_max_u32(real ? order_key(x) : 0u);
+  if (!real) id = INT_MAX;
+  p = 0.f;
+  logp = 0.f;
+  if (!mk) return false;
+  const float d = x - __uint_as_float(order_key_inv(mk));
+  const float e = real ? expf(d) : 0.f;
+  const float s = group_sum<kWave>(e);
+  p = e / s;
+  if (p > 0.f) logp = d - logf(s);
+  return true;
+}
+
+// Joins the shares of the rows pass: loss, lse and, with G, dloss/dz. One
+// block per row.
+template <typename T>
+__global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
+    const T* __restrict__ Z, const T* __restrict__ P, const int32_t* __restrict__ idx, const float* __restrict__ t,
+    int64_t N, int64_t V, int r, int RP, int k, float inv_t, int shares, const float* __restrict__ pm,
+    const float* __restrict__ pl, const float* __restrict__ po, float* __restrict__ loss, float* __restrict__ lse,
+    float* __restrict__ G) {
+  __shared__ float sp[kWave], sdot[kWave], red[kWaves * 2];
+  __shared__ int sid[kWave];
+  const int64_t n = blockIdx.x;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  int id;
+  float p, logp;
+  const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);   // every wave: the same values
+  if (wave == 0) {
+    sid[lane] = id;
+    sp[lane] = p;
+  }
+  // maximum and sum over the shares, by the whole block
+  float m = neg_inf();
+  for (int s = threadIdx.x; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if (lane == 0) red[wave] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float l = 0.f;
+  for (int s = threadIdx.x; s < shares; s += kWaves * kWave) {
+    const float ps = pl[(int64_t)s * N + n];
+    if (ps != 0.f) l += ps * exp2_hw(pm[(int64_t)s * N + n] - m);   // a share without rows has sum 0
+  }
+  l = group_sum<kWave>(l);
+  if (lane == 0) red[kWaves + wave] = l;
+  // the places' scores
+  for (int j = wave; j < k; j += kWaves) {
+    const int v = sid[j];
+    float d = 0.f;
+    if (v != INT_MAX)
+      for (int c = lane; c < r; c += kWave) d = fmaf(widen<T>(P[(int64_t)v * r + c]), widen<T>(Z[n * r + c]), d);
+    d = group_sum<kWave>(d);
+    if (lane == 0) sdot[j] = d;
+  }
+  __syncthreads();
+  l = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
+  const float ls = (m + log2f(l)) * kLn2;
+  if (wave == 0) {
+    const float s = lane < k && p > 0.f ? sdot[lane] * inv_t : 0.f;
+    const float e = group_sum<kWave>(p > 0.f ? p * (logp - s + ls) : 0.f);
+    if (lane == 0) {
+      lse[n] = ls;
+      loss[n] = any ? e : 0.f;
+    }
+  }
+  if (!G) return;
+  const float il = 1.f / l;
+  for (int c = threadIdx.x; c < r; c += kWaves * kWave) {
+    float o = 0.f;
+    for (int s = 0; s < shares; ++s) {
+      if (pl[(int64_t)s * N + n] != 0.f)
+        o = fmaf(po[((int64_t)s * N + n) * RP + c], exp2_hw(pm[(int64_t)s * N + n] - m), o);
+    }
+    o *= il;
+    float q = 0.f;
+    for (int j = 0; j < k; ++j)
+      if (sid[j] != INT_MAX) q = fmaf(sp[j], widen<T>(P[(int64_t)sid[j] * r + c]), q);
+    G[n * r + c] = any ? (o - q) * inv_t : 0.f;
+  }
+}
+
+// Per row, before the columns pass: the exponent's offset and the sign of the
+// weight, the row of Z (zeros without weight, so that what a masked row holds,
+// NaN included, cannot reach dP), the places in ascending order of their ids
+// with w p / T, and dZ = w G. One wave per row.
+template <typename T>
+__global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
+    const T* __restrict__ Z, const int32_t* __restrict__ idx, const float* __restrict__ t,
+    const float* __restrict__ lse, const float* __restrict__ G, const float* __restrict__ weight, int64_t N,
+    int64_t V, int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ beta,
+    float* __restrict__ sgn, int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
+  const int64_t n = (int64_t)blockIdx.x * kWaves + wave_id();
+  const int lane = threadIdx.x & 63;
+  if (n >= N) return;
+  int id;
+  float p, logp;
+  const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);
+  const float w = weight ? weight[n] : 1.f;
+  const bool live = any && w != 0.f;
+  const float c = w * inv_t;
+  if (dZ)
+    for (int i = lane; i < r; i += kWave) dZ[n * r + i] = store_cast<T>(live ? w * G[n * r + i] : 0.f);
+  if (!zc) return;
+  if (lane == 0) {
+    beta[n] = live ? lse[n] * kLog2e - log2f(fabsf(c)) : __builtin_inff();
+    sgn[n] = live && c < 0.f ? -1.f : 1.f;
+  }
+  for (int i = lane; i < RP; i += kWave) zc[n * RP + i] = live && i < r ? Z[n * r + i] : T(0);
+  if (!live) id = INT_MAX;
+  int rank = 0;
+  for (int j = 0; j < k; ++j) {
+    const int o = __builtin_amdgcn_readlane(id, j);
+    rank += o < id || (o == id && j < lane);
+  }
+  if (lane < k) {
+    srt_id[n * k + rank] = id;
+    srt_w[n * k + rank] = p * c;
+  }
+}
+
+// table[g][n] = how many of row n's places have an id below g * GC: one lane
+// per row, walking up its sorted places over a range of column groups.
+constexpr int kTableGroups = 64;   // groups per wave
+__global__ void __launch_bounds__(kWave) distill_table_kernel(const int* __restrict__ srt_id, int64_t N, int64_t npad,
+                                                              int k, int GC, int64_t groups,
+                                                              uint8_t* __restrict__ table) {
+  const int64_t ranges = (groups + kTableGroups) / kTableGroups;   // of the groups + 1 boundaries
+  const int64_t n = blockIdx.x / ranges * kWave + threadIdx.x;
+  const int64_t g0 = blockIdx.x % ranges * kTableGroups, g1 = min(g0 + kTableGroups, groups + 1);
+  const int* id = srt_id + n * k;
+  int j = 0;
+  if (n < N) {   // first place at or above the range
+    int hi = k;
+    while (j < hi) {
+      const int mid = (j + hi) >> 1;
+      if (id[mid] < g0 * GC && id[mid] != INT_MAX) j = mid + 1;
+      else hi = mid;
+    }
+  }
+  int64_t next = n < N && j < k ? id[j] : INT_MAX;
+  for (int64_t g = g0; g < g1; ++g) {
+    while (next < g * GC && next != INT_MAX) {
+      ++j;
+      next = j < k ? id[j] : INT_MAX;
+    }
+    table[g * npad + n] = (uint8_t)j;
+  }
+}
+
+// The places of each group of GC columns, ascending by row. The number of
+// places below a group, summed over the rows, is where its list starts.
+__global__ void __launch_bounds__(256) distill_list_kernel(const uint8_t* __restrict__ table,
+                                                           const int* __restrict__ srt_id,
+                                                           const float* __restrict__ srt_w, int64_t npad, int k,
+                                                           int GC, uint32_t* __restrict__ start,
+                                                           uint2* __restrict__ list) {
+  __shared__ uint32_t red[4], scan[4];
+  const int64_t g = blockIdx.x;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const uint8_t* lo = table + g * npad;
+  const uint8_t* hi = lo + npad;
+  uint32_t below = 0;
+  for (int64_t n = threadIdx.x * 16; n < npad; n += 256 * 16) {
+    const u32x4 v = load16(lo + n);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) below += (v[q] & 255) + ((v[q] >> 8) & 255) + ((v[q] >> 16) & 255) + (v[q] >> 24);
+  }
+  for (int o = 32; o; o >>= 1) below += __shfl_xor(below, o);
+  if (lane == 0) red[wave] = below;
+  __syncthreads();
+  uint32_t at = (red[0] + red[1]) + (red[2] + red[3]);
+  if (threadIdx.x == 0) start[g] = at;
+  for (int64_t n0 = 0; n0 < npad; n0 += 256 * 16) {
+    const int64_t n = n0 + threadIdx.x * 16;
+    u32x4 a = {0u, 0u, 0u, 0u}, b = a;
+    if (n < npad) {
+      a = load16(lo + n);
+      b = load16(hi + n);
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int s = 0; s < 32; s += 8) mine += ((b[q] >> s) & 255) - ((a[q] >> s) & 255);
+    const uint32_t incl = wave_incl_scan_u32(mine);
+    __syncthreads();
+    if (lane == 63) scan[wave] = incl;
+    __syncthreads();
+    uint32_t o = at + incl - mine;
+    for (int w = 0; w < wave; ++w) o += scan[w];
+    at += (scan[0] + scan[1]) + (scan[2] + scan[3]);
+    if (!mine) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int s = 0; s < 32; s += 8) {
+        const int64_t row = n + q * 4 + s / 8;
+        for (uint32_t j = (a[q] >> s) & 255; j < ((b[q] >> s) & 255); ++j)
+          list[o++] = uint2{(uint32_t)row | (uint32_t)(srt_id[row * k + j] - g * GC) << kRowBits,
+                            __float_as_uint(srt_w[row * k + j])};
+      }
+  }
+  if (g == (int64_t)gridDim.x - 1 && threadIdx.x == 0) start[g + 1] = at;
+}
+
+// dP = the sum of the columns pass's shares, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) distill_join_kernel(const float* __restrict__ part, int splits, int64_t V,
+                                                           int r, int RP, T* __restrict__ dP) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= V * r) return;
+  const int64_t v = i / r;
+  const int c = (int)(i % r);
+  float s = 0.f;
+  for (int p = 0; p < splits; ++p) s += part[((int64_t)p * V + v) * RP + c];
+  dP[i] = store_cast<T>(s);
+}
+
+__global__ void __launch_bounds__(256) distill_zero_kernel(uint32_t* __restrict__ p, int64_t words) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+// ---------------------------------------------------------------- host side
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int round_rank(int r) { return r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 ? 128 : r <= 256 ? 256 : 512; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int kMaxShares = 512;
+constexpr int kTargetBlocks = 512;   // two blocks per compute unit
+
+struct Plan {
+  int RP;
+  int XT, WX;        // rows pass
+  int row_splits;    // blocks along Y
+  int shares;        // shares per row of Z
+  int cXT;           // columns pass: 32-column tiles per wave
+  int GC;            // columns of a group (a wave)
+  int64_t groups;
+  int col_splits;
+  int64_t npad;
+  // workspace offsets
+  size_t pm, pl, po, fwd_total;
+  size_t zc, beta, sgn, srt_id, srt_w, table, start, list, part, bwd_total;
+};
+
+Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
+  Plan p{};
+  const size_t es = dtype == 0 ? 2 : 4;
+  p.RP = round_rank(r);
+  int64_t xblocks, ytiles, cblocks;
+  if (dtype == 0) {
+    p.XT = p.RP <= 256 ? 2 : 1;
+    p.WX = N <= 32 * p.XT && p.RP < 512 ? 1 : N <= 64 * p.XT ? 2 : 4;
+    xblocks = ceil_div(N, p.WX * 32 * p.XT);
+    ytiles = ceil_div(V, std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX)));
+    p.cXT = p.XT;
+    p.GC = 32 * p.cXT;
+  } else {
+    p.XT = 1;
+    p.WX = 4;
+    xblocks = ceil_div(N, 64);
+    ytiles = ceil_div(V, 16);
+    p.GC = 16;
+  }
+  const int wy = kWaves / p.WX;
+  p.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>({kTargetBlocks / xblocks, ytiles, kMaxShares / wy}));
+  p.shares = p.row_splits * wy;
+  p.groups = ceil_div(V, p.GC);
+  cblocks = ceil_div(p.groups, kWaves);
+  const int64_t ntiles = ceil_div(N, dtype == 0 ? (p.RP <= 128 ? 64 : 32) : 16);
+  p.col_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTargetBlocks / cblocks, ntiles));
+  p.npad = ceil_div(N, 64) * 64;
+  size_t o = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  p.pm = take(size_t(p.shares) * N * 4);
+  p.pl = take(size_t(p.shares) * N * 4);
+  p.po = take(size_t(p.shares) * N * p.RP * 4);
+  p.fwd_total = o;
+  o = 0;
+  p.zc = take(size_t(N) * p.RP * es);
+  p.beta = take(size_t(N) * 4);
+  p.sgn = take(size_t(N) * 4);
+  p.srt_id = take(size_t(N) * k * 4);
+  p.srt_w = take(size_t(N) * k * 4);
+  p.table = take(size_t(p.groups + 1) * p.npad);
+  p.start = take(size_t(p.groups + 1) * 4);
+  p.list = take(size_t(N) * k * 8);
+  p.part = take(p.col_splits > 1 ? size_t(p.col_splits) * V * p.RP * 4 : 0);
+  p.bwd_total = o;
+  return p;
+}
+
+template <int RP, int XT, int WX, bool ACC, bool COLS>
+hipError_t go_bf16(const StreamArgs& a, hipStream_t s) {
+  const int64_t xb = ceil_div(a.nx, WX * 32 * XT);
+  const auto kernel = stream_bf16_kernel<RP, XT, WX, ACC, COLS>;
+  constexpr int bytes = bf16_lds_bytes<RP, WX>();
+  if constexpr (bytes > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(xb * a.splits)), dim3(kWaves * kWave), bytes, s, a);
+  return hipGetLastError();
+}
+
+template <int RP, int XT, bool ACC>
+hipError_t go_rows(const StreamArgs& a, int WX, hipStream_t s) {
+  if constexpr (RP < 512) {
+    if (WX == 1) return go_bf16<RP, XT, 1, ACC, false>(a, s);
+  }
+  if (WX == 2) return go_bf16<RP, XT, 2, ACC, false>(a, s);
+  return go_bf16<RP, XT, 4, ACC, false>(a, s);
+}
+
+template <bool ACC, bool COLS>
+hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) {
+  if (dtype == 0) {
+    if constexpr (COLS) {
+      switch (p.RP) {
+        case 32: return go_bf16<32, 2, 4, true, true>(a, s);
+        case 64: return go_bf16<64, 2, 4, true, true>(a, s);
+        case 128: return go_bf16<128, 2, 4, true, true>(a, s);
+        case 256: return go_bf16<256, 2, 4, true, true>(a, s);
+        default: return go_bf16<512, 1, 4, true, true>(a, s);
+      }
+    } else {
+      switch (p.RP) {
+        case 32: return go_rows<32, 2, ACC>(a, p.WX, s);
+        case 64: return go_rows<64, 2, ACC>(a, p.WX, s);
+        case 128: return go_rows<128, 2, ACC>(a, p.WX, s);
+        case 256: return go_rows<256, 2, ACC>(a, p.WX, s);
+        default: return go_rows<512, 1, ACC>(a, p.WX, s);
+      }
+    }
+  }
+  const dim3 grid((unsigned)(ceil_div(a.nx, 64) * a.splits)), block(kWaves * kWave);
+  switch (p.RP) {
+    case 32: hipLaunchKernelGGL((stream_f32_kernel<32, ACC, COLS>), grid, block, 0, s, a); break;
+    case 64: hipLaunchKernelGGL((stream_f32_kernel<64, ACC, COLS>), grid, block, 0, s, a); break;
+    case 128: hipLaunchKernelGGL((stream_f32_kernel<128, ACC, COLS>), grid, block, 0, s, a); break;
+    case 256: hipLaunchKernelGGL((stream_f32_kernel<256, ACC, COLS>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((stream_f32_kernel<512, ACC, COLS>), grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
+  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)d.N), dim3(kWaves * kWave), 0, s,
+                     static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t, d.N, d.V, d.r, p.RP, d.k,
+                     d.inv_t, p.shares, reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
+                     reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
+}
+
+template <typename T>
+void prep(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
+  hipLaunchKernelGGL(distill_prep_kernel<T>, dim3((unsigned)ceil_div(d.N, kWaves)), dim3(kWaves * kWave), 0, s,
+                     static_cast<const T*>(d.Z), d.idx, d.t, d.lse, d.G, d.weight, d.N, d.V, d.r, p.RP, d.k, d.inv_t,
+                     d.dP ? reinterpret_cast<T*>(ws + p.zc) : nullptr, reinterpret_cast<float*>(ws + p.beta),
+                     reinterpret_cast<float*>(ws + p.sgn), reinterpret_cast<int*>(ws + p.srt_id),
+                     reinterpret_cast<float*>(ws + p.srt_w), static_cast<T*>(d.dZ));
+}
+
+}  // namespace
+
+size_t distill_workspace_bytes(int dtype, int64_t V, int r, int64_t N, int k) {
+  const Plan p = plan(dtype, V, r, N, k);
+  return std::max(p.fwd_total, p.bwd_total);
+}
+
+hipError_t launch_distill(const DistillArgs& d, void* workspace, hipStream_t s) {
+  const Plan p = plan(d.dtype, d.V, d.r, d.N, d.k);
+  char* ws = static_cast<char*>(workspace);
+  StreamArgs a{};
+  a.X = d.Z;
+  a.nx = d.N;
+  a.Y = d.P;
+  a.ny = d.V;
+  a.r = d.r;
+  a.ldy = d.r;
+  a.scale = d.scale;
+  a.splits = p.row_splits;
+  a.pm = reinterpret_cast<float*>(ws + p.pm);
+  a.pl = reinterpret_cast<float*>(ws + p.pl);
+  a.po = reinterpret_cast<float*>(ws + p.po);
+  const hipError_t e = d.G ? stream<true, false>(d.dtype, p, a, s) : stream<false, false>(d.dtype, p, a, s);
+  if (e != hipSuccess) return e;
+  if (d.dtype == 0) finish<uint16_t>(p, d, ws, s);
+  else finish<float>(p, d, ws, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_t s) {
+  if (d.N == 0) {   // no rows: dP is zero (r is a multiple of 8, so bf16 rows are whole words)
+    if (!d.dP) return hipSuccess;
+    const int64_t words = d.V * d.r / (d.dtype == 0 ? 2 : 1);
+    hipLaunchKernelGGL(distill_zero_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(words, 256), 4096)), dim3(256),
+                       0, s, static_cast<uint32_t*>(d.dP), words);
+    return hipGetLastError();
+  }
+  const Plan p = plan(d.dtype, d.V, d.r, d.N, d.k);
+  char* ws = static_cast<char*>(workspace);
+  if (d.dtype == 0) prep<uint16_t>(p, d, ws, s);
+  else prep<float>(p, d, ws, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !d.dP) return e;
+  const int* srt_id = reinterpret_cast<int*>(ws + p.srt_id);
+  const float* srt_w = reinterpret_cast<float*>(ws + p.srt_w);
+  uint8_t* table = reinterpret_cast<uint8_t*>(ws + p.table);
+  uint32_t* start = reinterpret_cast<uint32_t*>(ws + p.start);
+  uint2* list = reinterpret_cast<uint2*>(ws + p.list);
+  hipLaunchKernelGGL(distill_table_kernel,
+                     dim3((unsigned)(p.npad / kWave * ceil_div(p.groups + 1, kTableGroups))), dim3(kWave), 0, s, srt_id, d.N, p.npad, d.k, p.GC, p.groups, table);
+  hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(256), 0, s, table, srt_id, srt_w, p.npad,
+                     d.k, p.GC, start, list);
+  StreamArgs a{};
+  a.X = d.P;
+  a.nx = d.V;
+  a.Y = ws + p.zc;
+  a.ny = d.N;
+  a.r = d.r;
+  a.ldy = p.RP;
+  a.scale = d.scale;
+  a.splits = p.col_splits;
+  a.beta = reinterpret_cast<float*>(ws + p.beta);
+  a.sgn = reinterpret_cast<float*>(ws + p.sgn);
+  a.list_start = start;
+  a.list = list;
+  a.Z = d.Z;
+  a.dP = d.dP;
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  e = stream<true, true>(d.dtype, p, a, s);
+  if (e != hipSuccess) return e;
+  if (p.col_splits > 1) {
+    const dim3 grid((unsigned)ceil_div(d.V * d.r, 256));
+    if (d.dtype == 0)
+      hipLaunchKernelGGL(distill_join_kernel<uint16_t>, grid, dim3(256), 0, s, a.part, p.col_splits, d.V, d.r, p.RP,
+                         static_cast<uint16_t*>(d.dP));
+    else
+      hipLaunchKernelGGL(distill_join_kernel<float>, grid, dim3(256), 0, s, a.part, p.col_splits, d.V, d.r, p.RP,
+                         static_cast<float*>(d.dP));
+  }
+  return hipGetLastError();
+}
+
+}  // namespace lrh

@@ -202,6 +202,50 @@ size_t factor_workspace_bytes(int64_t V, int64_t d, int r);
 hipError_t launch_factor(const void* W, int64_t V, int64_t d, int r, int q, const float* omega, void* P, void* Q,
                          void* workspace, hipStream_t stream);
 
+// ------------------------------------------------------ kernels_beam.hip
+// The nb best (beam, column) of each of B sequences, see lrhead_beam_select.
+// beam_fits: whether the launch fits a grid.
+bool beam_fits(int dtype, int64_t B, int m, int64_t n);
+size_t beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb);
+hipError_t launch_beam_select(int dtype, const void* x, int64_t ld, const int32_t* idx, const float* score,
+                              const uint8_t* ended, int end_id, int64_t B, int m, int64_t n, int nb, float* out_score,
+                              int32_t* out_beam, int32_t* out_token, void* workspace, hipStream_t stream);
+// dst[b, j] = src[b, parent[b, j]] for each state (host array): segs segments
+// of `positions` positions of pos_bytes each per beam; with `length` only the
+// first length[b] positions of each segment.
+struct BeamState {
+  const void* src;
+  void* dst;
+  int64_t segs, positions, pos_bytes;
+};
+hipError_t launch_beam_move(const BeamState* states, int n_states, const int32_t* parent, const int32_t* length,
+                            int64_t B, int m, int nb, hipStream_t stream);
+
+// --------------------------------------------------- kernels_distill.hip
+// Distillation of (Z: N x r, P: V x r) from the teacher places idx / t
+// (N x k), see lrhead_distill. launch_distill writes loss, lse and, unless G
+// is NULL, G; launch_distill_grad reads lse and G (needed for dZ only) and
+// writes dZ and dP, either of which may be NULL.
+struct DistillArgs {
+  int dtype;
+  int64_t V, N;
+  int r, k;
+  float inv_t, scale;    // 1 / T, log2(e) / T
+  const void* P;
+  const void* Z;
+  const int32_t* idx;
+  const float* t;
+  const float* weight;   // N, or NULL: 1
+  float* loss;
+  float* lse;
+  float* G;              // N x r
+  void* dZ;
+  void* dP;
+};
+size_t distill_workspace_bytes(int dtype, int64_t V, int r, int64_t N, int k);
+hipError_t launch_distill(const DistillArgs& d, void* workspace, hipStream_t stream);
+hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_t stream);
+
 // logits[b, j] = W[idx[b, j], :] . h_b (NaN for ids outside [0, V)).
 hipError_t launch_rescore(int dtype, const void* W, const void* H, const int32_t* idx, int64_t B,
                           int k, int64_t V, int d, float* logits, hipStream_t stream);

@@ -8,6 +8,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -298,6 +299,49 @@ void fill_handle(lrhead_s* h, int dtype, int64_t V, int64_t d, int64_t r, const 
   h->ev_after = nullptr;
 }
 
+// ------------------------------------------------------- training, beams
+int check_distill(int dtype, int64_t V, int64_t r, int64_t N, int k) {
+  if (dtype != LRHEAD_BF16 && dtype != LRHEAD_FP32) return fail(LRHEAD_EDTYPE, "unknown dtype %d", dtype);
+  if (V < 1 || V > INT32_MAX) return fail(LRHEAD_ERANGE, "V = %lld outside [1, 2^31)", (long long)V);
+  if (r < 8 || r > LRHEAD_R_MAX || r % 8) return fail(LRHEAD_ERANGE, "r = %lld: need a multiple of 8 in [8, %d]", (long long)r, LRHEAD_R_MAX);
+  if (N < 0 || N > kBMaxLimit) return fail(LRHEAD_ERANGE, "N = %lld outside [0, 2^20]", (long long)N);
+  if (k < 1 || k > LRHEAD_K_MAX) return fail(LRHEAD_ERANGE, "k = %d outside [1, %d]", k, LRHEAD_K_MAX);
+  return LRHEAD_OK;
+}
+
+int check_temperature(float t) {
+  // also its reciprocal has to be a normal number
+  if (!(t >= 1e-30f && t <= 1e30f)) return fail(LRHEAD_ERANGE, "temperature = %g outside [1e-30, 1e30]", (double)t);
+  return LRHEAD_OK;
+}
+
+lrh::DistillArgs distill_args(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N,
+                              const int32_t* idx, const float* logits, int k, float temperature) {
+  lrh::DistillArgs d{};
+  d.dtype = dtype;
+  d.V = V;
+  d.N = N;
+  d.r = (int)r;
+  d.k = k;
+  d.inv_t = (float)(1.0 / (double)temperature);
+  d.scale = (float)(1.4426950408889634 / (double)temperature);
+  d.P = P;
+  d.Z = Z;
+  d.idx = idx;
+  d.t = logits;
+  return d;
+}
+
+int check_beam(int dtype, int64_t B, int m, int64_t n, int nb) {
+  if (dtype != LRHEAD_BF16 && dtype != LRHEAD_FP32) return fail(LRHEAD_EDTYPE, "unknown dtype %d", dtype);
+  if (m < 1 || m > LRHEAD_K_MAX) return fail(LRHEAD_ERANGE, "m = %d outside [1, %d]", m, LRHEAD_K_MAX);
+  if (nb < 1 || nb > LRHEAD_K_MAX) return fail(LRHEAD_ERANGE, "nb = %d outside [1, %d]", nb, LRHEAD_K_MAX);
+  if (n < 1 || n > INT32_MAX) return fail(LRHEAD_ERANGE, "n = %lld outside [1, 2^31)", (long long)n);
+  if (B < 0 || B > kBMaxLimit || !lrh::beam_fits(dtype, B > 0 ? B : 1, m, n))
+    return fail(LRHEAD_ERANGE, "B = %lld outside [0, 2^20], or B m n too large for one call", (long long)B);
+  return LRHEAD_OK;
+}
+
 // ------------------------------------------------- allocation-free variant
 // The workspace of lrhead_draft_static is `scratch` (file scope, below the
 // namespace): one copy per GPU, resident until the process ends. In host
@@ -493,6 +537,129 @@ int lrhead_factor(const void* W, int64_t V, int64_t d, int r, int q, const float
   LRH_HIP(lrh::batch_init(), "GEMM kernel set-up");   // the W-sized products run on the GEMM kernel
   LRH_HIP(lrh::launch_factor(W, V, d, r, q, omega, P, Q, workspace, static_cast<hipStream_t>(stream)),
           "factor launch");
+  return LRHEAD_OK;
+}
+
+size_t lrhead_distill_workspace_bytes(int dtype, int64_t V, int64_t r, int64_t N, int k) {
+  if (check_distill(dtype, V, r, N, k) != LRHEAD_OK) return 0;
+  return lrh::distill_workspace_bytes(dtype, V, (int)r, N > 0 ? N : 1, k);
+}
+
+int lrhead_distill(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N, const int32_t* idx,
+                   const float* logits, int k, float temperature, float* loss, float* lse, float* grad,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  LRH_TRY(check_distill(dtype, V, r, N, k));
+  LRH_TRY(check_temperature(temperature));
+  if (N == 0) return LRHEAD_OK;
+  if (!P || !Z || !idx || !logits || !loss || !lse || !workspace)
+    return fail(LRHEAD_EINVAL, "P, Z, idx, logits, loss, lse and workspace must be non-NULL");
+  if (!aligned16(P) || !aligned16(Z) || !aligned16(idx) || !aligned16(logits) || !aligned16(loss) ||
+      !aligned16(lse) || !aligned16(grad) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "P, Z, idx, logits, loss, lse, grad and workspace must be 16-byte aligned");
+  const size_t need = lrh::distill_workspace_bytes(dtype, V, (int)r, N, k);
+  if (workspace_bytes < need) return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  lrh::DistillArgs d = distill_args(dtype, V, r, P, Z, N, idx, logits, k, temperature);
+  d.loss = loss;
+  d.lse = lse;
+  d.G = grad;
+  LRH_HIP(lrh::launch_distill(d, workspace, static_cast<hipStream_t>(stream)), "distillation launch");
+  return LRHEAD_OK;
+}
+
+int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N, const int32_t* idx,
+                        const float* logits, int k, float temperature, const float* lse, const float* grad,
+                        const float* weight, void* dZ, void* dP, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  LRH_TRY(check_distill(dtype, V, r, N, k));
+  LRH_TRY(check_temperature(temperature));
+  if (N > 0 && (!P || !Z || !idx || !logits || !lse || !workspace))
+    return fail(LRHEAD_EINVAL, "P, Z, idx, logits, lse and workspace must be non-NULL");
+  if (N > 0 && dZ && !grad) return fail(LRHEAD_EINVAL, "dZ needs grad");
+  if (!aligned16(P) || !aligned16(Z) || !aligned16(idx) || !aligned16(logits) || !aligned16(lse) ||
+      !aligned16(grad) || !aligned16(weight) || !aligned16(dZ) || !aligned16(dP) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "a pointer is not 16-byte aligned");
+  lrh::DistillArgs d = distill_args(dtype, V, r, P, Z, N, idx, logits, k, temperature);
+  if (N > 0) {
+    const size_t need = lrh::distill_workspace_bytes(dtype, V, (int)r, N, k);
+    if (workspace_bytes < need)
+      return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  }
+  d.lse = const_cast<float*>(lse);
+  d.G = const_cast<float*>(grad);
+  d.weight = weight;
+  d.dZ = dZ;
+  d.dP = dP;
+  LRH_HIP(lrh::launch_distill_grad(d, workspace, static_cast<hipStream_t>(stream)), "distillation gradient launch");
+  return LRHEAD_OK;
+}
+
+size_t lrhead_beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb) {
+  if (check_beam(dtype, B, m, n, nb) != LRHEAD_OK) return 0;
+  return lrh::beam_workspace_bytes(dtype, B > 0 ? B : 1, m, n, nb);
+}
+
+int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t* idx, const float* score,
+                       const uint8_t* ended, int end_id, int64_t B, int m, int64_t n, int nb, float* out_score,
+                       int32_t* out_beam, int32_t* out_token, void* workspace, size_t workspace_bytes, void* stream) {
+  LRH_TRY(check_beam(dtype, B, m, n, nb));
+  if (ld < n) return fail(LRHEAD_ERANGE, "ld = %lld below n = %lld", (long long)ld, (long long)n);
+  if (B == 0) return LRHEAD_OK;
+  if (!logits || !score || !workspace) return fail(LRHEAD_EINVAL, "logits, score and workspace must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(logits) % elem_bytes(dtype))
+    return fail(LRHEAD_EALIGN, "logits are not aligned to their elements");
+  if (!aligned16(idx) || !aligned16(score) || !aligned16(ended) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "idx, score, ended and workspace must be 16-byte aligned");
+  LRH_TRY(check_out(out_score, "out_score", true));
+  LRH_TRY(check_out(out_beam, "out_beam", true));
+  LRH_TRY(check_out(out_token, "out_token", true));
+  const size_t need = lrh::beam_workspace_bytes(dtype, B, m, n, nb);
+  if (workspace_bytes < need) return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  LRH_HIP(lrh::launch_beam_select(dtype, logits, ld, idx, score, ended, end_id, B, m, n, nb, out_score, out_beam,
+                                  out_token, workspace, static_cast<hipStream_t>(stream)),
+          "beam selection launch");
+  return LRHEAD_OK;
+}
+
+int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* parent, const int32_t* length,
+                   int64_t B, int m, int nb, void* stream) {
+  if (n_states < 0 || n_states > LRHEAD_STATES_MAX)
+    return fail(LRHEAD_ERANGE, "n_states = %d outside [0, %d]", n_states, LRHEAD_STATES_MAX);
+  if (B < 0 || m < 1 || nb < 1) return fail(LRHEAD_ERANGE, "need B >= 0 and m, nb >= 1");
+  if (B == 0 || n_states == 0) return LRHEAD_OK;
+  if (!states || !parent) return fail(LRHEAD_EINVAL, "states and parent must be non-NULL");
+  struct Range {   // half-open
+    uintptr_t lo, hi;
+    bool dst;
+  };
+  static thread_local Range ranges[2 * LRHEAD_STATES_MAX];
+  static thread_local lrh::BeamState moves[LRHEAD_STATES_MAX];
+  int n = 0, n_moves = 0;
+  for (int i = 0; i < n_states; ++i) {
+    const lrhead_state_t& s = states[i];
+    if (s.segs < 0 || s.positions < 0 || s.position_bytes < 0)
+      return fail(LRHEAD_ERANGE, "state %d has a negative size", i);
+    int64_t beam = 0, src = 0, dst = 0;
+    if (__builtin_mul_overflow(s.segs, s.positions, &beam) || __builtin_mul_overflow(beam, s.position_bytes, &beam) ||
+        __builtin_mul_overflow(beam, B, &beam) || __builtin_mul_overflow(beam, (int64_t)m, &src) ||
+        __builtin_mul_overflow(beam, (int64_t)nb, &dst))
+      return fail(LRHEAD_ERANGE, "state %d: its size passes 64 bits", i);
+    if (beam == 0) continue;
+    if (!s.src || !s.dst) return fail(LRHEAD_EINVAL, "state %d: src and dst must be non-NULL", i);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s.src), b = reinterpret_cast<uintptr_t>(s.dst);
+    ranges[n++] = {a, a + (uintptr_t)src, false};
+    ranges[n++] = {b, b + (uintptr_t)dst, true};
+    moves[n_moves++] = {s.src, s.dst, s.segs, s.positions, s.position_bytes};
+  }
+  std::sort(ranges, ranges + n, [](const Range& x, const Range& y) { return x.lo < y.lo; });
+  uintptr_t any_end = 0, dst_end = 0;   // how far the ranges, and the destinations, before this one reach
+  for (int i = 0; i < n; ++i) {
+    if (ranges[i].lo < dst_end || (ranges[i].dst && ranges[i].lo < any_end))
+      return fail(LRHEAD_EINVAL, "a destination overlaps another state");
+    any_end = std::max(any_end, ranges[i].hi);
+    if (ranges[i].dst) dst_end = std::max(dst_end, ranges[i].hi);
+  }
+  LRH_HIP(lrh::launch_beam_move(moves, n_moves, parent, length, B, m, nb, static_cast<hipStream_t>(stream)),
+          "state reordering launch");
   return LRHEAD_OK;
 }
 

@@ -25,6 +25,24 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
+class _on:
+    """Makes a device current and gives its current HIP stream."""
+
+    def __init__(self, device: torch.device):
+        self.index = device.index
+        self.before = -1
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.before = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+        return ctypes.c_void_p(torch.cuda.current_stream(self.index).cuda_stream)
+
+    def __exit__(self, *_):
+        if self.before >= 0:
+            torch.cuda.set_device(self.before)
+
+
 class Head:
     """A low-rank head (Q: r x d, P: V x r) with its full-rank head W (V x d).
 
