@@ -14,8 +14,8 @@
 // stream the other through LDS and use each tile of scores where it is
 // made. With X the side at rest and Y the streamed one, both compute
 //   S = Y . X^T,   E = exp2(S log2(e)/T - c),   A += Y^T . E
-//   rows pass    (X = Z, Y = P): c = the running maximum of the row of Z; A is
-//                the unnormalised sum_v q_v P_v, an attention over the
+//   rows pass    (X = Z, Y = P): c = a score near the row's largest; A is the
+//                unnormalised sum_v q_v P_v, an attention over the
 //                vocabulary whose keys and values are both P;
 //   columns pass (X = P, Y = Z): c = lse_n - log(|w_n|/T), so E is already
 //                |w_n| q_nv / T and A the dense part of dP.
@@ -26,6 +26,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "launch.h"
@@ -43,10 +44,12 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kRawBufferFlags = 0x00020000;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum of a row moves only when a score passes it by more
-// than 2^kSlack: E stays below 2^kSlack, sums keep their relative precision
-// (fp32 and bf16 have range to spare) and most tiles need no rescaling.
-constexpr float kSlack = 8.f;
+// The exponents of the rows pass are taken from the largest of a share's
+// first scores, not from a running maximum: fp32 and bf16 have range to
+// spare, so a score may pass the reference by 2^60 before a sum or a product
+// could leave it, and neither the sums nor the accumulators (which would have
+// to leave the matrix cores' registers for it) are ever rescaled.
+constexpr float kMostSum = 0x1p60f;
 constexpr int kWaves = 4;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -72,16 +75,22 @@ struct StreamArgs {
   float* pl;
   float* po;            // [share][nx][RP]
   // columns pass
-  const float* beta;    // [ny]: c, +inf for rows without weight
-  const float* sgn;     // [ny]: the weight's sign
+  // [tile] of the rows of Z: RB times c (+inf for rows without weight), RB
+  // times the weight's sign as bit 15 of 16 bits, padding to 2 RB words
+  const float* row_c;
   const uint32_t* list_start;   // [groups + 1]: a group of columns' teacher places in `list`
   const uint2* list;    // (row | local column << kRowBits, bits of w p / T), by row within a group
-  const void* Z;        // N x r, for the teacher places
   void* dP;             // V x r, with one share
   float* part;          // [share][nx][RP], with more
 };
 constexpr int kRowBits = 20;   // N <= 2^20
 constexpr uint32_t kRowMask = (1u << kRowBits) - 1;
+
+constexpr int kRowBlock = 64;   // RB of the fp32 kernel
+__device__ __forceinline__ float* row_c_at(float* row_c, int64_t n, int RB) { return row_c + n / RB * (2 * RB) + n % RB; }
+__device__ __forceinline__ uint16_t* row_sign_at(float* row_c, int64_t n, int RB) {
+  return reinterpret_cast<uint16_t*>(row_c + n / RB * (2 * RB) + RB) + n % RB;
+}
 
 // 16-byte chunk c of row y of an LDS tile sits at chunk c ^ swz_row(y). A wave
 // reads the tile as the left operand of S (32 rows, one chunk each) and,
@@ -145,11 +154,72 @@ struct TileCopy {
   }
 };
 
+// The lane's places in a tile, in elements from its first row. The swizzle
+// depends on the row within 16 only and touches the low 4 chunk bits, so a
+// few registers hold all of them; subtiles, steps of 16 rows and chunks past
+// 16 are constants added to a place.
+template <int RP>
+struct Places {
+  static constexpr int kRow = RP >= 128 ? 8 : RP / 16;   // steps of 16 columns within 16 chunks
+  static constexpr int kCol = RP >= 128 ? 4 : RP / 32;   // steps of 32 columns
+  int row[kRow];       // left operand of S: row (lane & 31), 8 columns
+  int col[2][kCol];    // left operand of A: rows 4 h + (lane & 15) / 4 and 8 more
+  __device__ __forceinline__ void init() {
+    const int lane = threadIdx.x & 63, h = lane >> 5, y = lane & 31;
+#pragma unroll
+    for (int i = 0; i < kRow; ++i) row[i] = y * RP + ((i * 2 + h) ^ swz_row<RP>(y)) * 8;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int v = b * 8 + h * 4 + ((lane & 15) >> 2);
+#pragma unroll
+      for (int i = 0; i < kCol; ++i) {
+        const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        col[b][i] = v * RP + (c ^ swz_row<RP>(v)) * 8 + (lane & 1) * 4;
+      }
+    }
+  }
+};
+
+// S of one 32-row subtile: its rows as the left operand.
+template <int RP, int XT>
+__device__ __forceinline__ void scores(const uint16_t* subtile, const Places<RP>& at, const bf16x8 (&X)[XT][RP / 16],
+                                       f32x16 (&S)[XT]) {
+#pragma unroll
+  for (int xt = 0; xt < XT; ++xt) S[xt] = f32x16{};
+#pragma unroll
+  for (int ks = 0; ks < RP / 16; ++ks) {
+    const bf16x8 A = __builtin_bit_cast(bf16x8, load16(subtile + at.row[ks % at.kRow] + ks / at.kRow * 128));
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) S[xt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, X[xt][ks], S[xt], 0, 0, 0);
+  }
+}
+
+// 16 rows of a tile, transposed, as the left operand of A (32 columns from
+// 32 rt): 16 lanes read 4 rows of 16 columns (lane i row i / 4, columns
+// 4 (i % 4)..) and each receives a column. The 8 rows of a half wave come
+// in the order in which the matrix cores leave S: 4 h + 0..3, 8 + 4 h + 0..3.
+template <int RP>
+__device__ __forceinline__ bf16x8 columns(const uint16_t* rows16, const Places<RP>& at, int rt) {
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const uint16_t* p = rows16 + rt / at.kCol * 128;
+  const s16x4 va = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(p + at.col[0][rt % at.kCol]));
+  const s16x4 vb = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(p + at.col[1][rt % at.kCol]));
+  const s16x8 v = {va[0], va[1], va[2], va[3], vb[0], vb[1], vb[2], vb[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Tiles of 32 rows of X that a wave owns. Two halve the LDS reads of each
+// product, but from r = 128 on they take more than half of the registers, and
+// the one wave that is left to a SIMD cannot hide its exponentials behind
+// another's products: rows and columns pass at 4096 rows, r = 128, took 308
+// and 334 us with one tile and two waves, 377 and 411 us with two and one.
+constexpr int x_tiles(int RP) { return RP <= 64 ? 2 : 1; }
+
 // bf16. RP: r rounded up to a tile size; a wave owns XT * 32 rows of X, WX of
 // the block's four waves sit side by side on X and 4 / WX share out a
 // tile's rows of Y.
 template <int RP, int XT, int WX, bool ACC, bool COLS>
-__global__ void __launch_bounds__(kWaves* kWave, 1) stream_bf16_kernel(StreamArgs a) {
+__global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_kernel(StreamArgs a) {
   constexpr int TY = bf16_tile_rows<RP, WX>();
   constexpr int KS = RP / 16, RT = RP / 32, WY = kWaves / WX;
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
@@ -185,96 +255,102 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_bf16_kernel(StreamArg
   const int64_t t_begin = nt * split / a.splits, t_end = nt * (split + 1) / a.splits;
   TileCopy<RP, TY> copy;
   copy.init(a.Y, a.ny, a.r, a.ldy);
-
-  const auto stage_rows = [&](int buf, int64_t t) {
-    if constexpr (COLS) {
-      if ((int)threadIdx.x < TY) {
-        const int64_t y = t * TY + threadIdx.x;
-        rows[buf * 2 * TY + threadIdx.x] = y < a.ny ? a.beta[y] : __builtin_inff();
-        rows[buf * 2 * TY + TY + threadIdx.x] = y < a.ny ? a.sgn[y] : 1.f;
-      }
+  const auto stage = [&](int buf, int64_t t) {
+    copy.issue(lds + buf * TY * RP, t);
+    if constexpr (COLS) {   // the rows' offsets and signs, kept tile by tile
+      if (wave < TY / 32)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(a.row_c + (t * 2 * TY + wave * kWave + lane)),
+            (lds_ptr_t)(rows + buf * 2 * TY + wave * kWave), 4, 0, 0);
     }
   };
-  if (t_begin < t_end) {
-    copy.issue(lds, t_begin);
-    stage_rows(0, t_begin);
-  }
-  for (int64_t t = t_begin; t < t_end; ++t) {
-    const int buf = (int)(t - t_begin) & 1;
-    __builtin_amdgcn_s_waitcnt(0xF70);   // vmcnt(0): this wave's share of tile t has landed
-    __syncthreads();                      // everyone's has, and every wave is done with the other buffer
-    if (t + 1 < t_end) {
-      copy.issue(lds + (buf ^ 1) * TY * RP, t + 1);
-      stage_rows(buf ^ 1, t + 1);
-    }
-    const uint16_t* tile = lds + buf * TY * RP;
-    const float* row_c = rows + buf * 2 * TY;
-    const float* row_s = row_c + TY;
-#pragma unroll 1
-    for (int sub = wy; sub < TY / 32; sub += WY) {
-      const int64_t y0 = t * TY + sub * 32;
-      if (y0 >= a.ny) break;
-      f32x16 S[XT] = {};
-      {
-        const int row = sub * 32 + (lane & 31);
-        const int f = swz_row<RP>(row);
+  Places<RP> at;
+  at.init();
+  // Calls f(subtile, row values, rows left) for this wave's subtiles of the
+  // share. Rows left is a constant 32 but for the rows pass's last tile,
+  // where the vocabulary may end (the columns pass pads its rows).
+  const int64_t t_full = COLS ? t_end : min(t_end, a.ny / TY);
+  const auto each_subtile = [&](auto&& f) {
+    const auto one_tile = [&](int buf, int64_t t, auto last) {
+      __builtin_amdgcn_s_waitcnt(0xF70);   // vmcnt(0): this wave's share of tile t has landed
+      __syncthreads();                      // everyone's has, and every wave is done with the other buffer
+      if (t + 1 < t_end) stage(buf ^ 1, t + 1);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const bf16x8 A = __builtin_bit_cast(bf16x8, load16(tile + row * RP + ((ks * 2 + h) ^ f) * 8));
-#pragma unroll
-          for (int xt = 0; xt < XT; ++xt)
-            S[xt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, X[xt][ks], S[xt], 0, 0, 0);
-        }
+      for (int i = 0; i < TY / 32 / WY; ++i) {
+        const int sub = i * WY + wy;
+        const uint16_t* subtile = lds + (buf * TY + sub * 32) * RP;
+        const float* row_c = rows + buf * 2 * TY + sub * 32;
+        if constexpr (last) f(subtile, row_c, rows + buf * 2 * TY + TY + sub * 16, (int)(a.ny - t * TY - sub * 32));
+        else f(subtile, row_c, rows + buf * 2 * TY + TY + sub * 16, std::integral_constant<int, 32>());
       }
+    };
+    if (t_begin < t_end) stage(0, t_begin);
+    for (int64_t t = t_begin; t < t_full; t += 2) {
+      one_tile(0, t, std::false_type());
+      if (t + 1 < t_full) one_tile(1, t + 1, std::false_type());
+    }
+    if constexpr (!COLS) {
+      if (t_full < t_end) one_tile((int)(t_full - t_begin) & 1, t_full, std::true_type());
+    }
+    __syncthreads();   // the tiles may be filled again
+  };
+  const auto mask = [&](f32x16 (&S)[XT], int left) {   // the rows past the vocabulary's end
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i >> 2) * 8 + h * 4 + (i & 3) >= left)
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) S[xt][i] = neg_inf();
+  };
+  const auto largest = [&](const f32x16 (&S)[XT]) {
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) {
+      float v = S[xt][0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) v = fmaxf(v, S[xt][i]);
+      m[xt] = fmaxf(m[xt], fmaxf(v, __shfl_xor(v, 32)) * a.scale);
+    }
+  };
+
+  if constexpr (!COLS) {
+    // The exponents' reference: the largest of the share's first 32 scores.
+    if (t_begin < t_end) {
+      stage(0, t_begin);
+      __builtin_amdgcn_s_waitcnt(0xF70);
+      __syncthreads();
+      f32x16 S[XT];
+      scores<RP, XT>(lds, at, X, S);
+      mask(S, (int)min(a.ny - t_begin * TY, (int64_t)32));
+      largest(S);
+      __syncthreads();
+    }
+  }
+  for (int attempt = 0;; ++attempt) {
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) {
+      l[xt] = 0.f;
+#pragma unroll
+      for (int rt = 0; rt < (ACC ? RT : 1); ++rt) acc[xt][rt] = f32x16{};
+    }
+    each_subtile([&](const uint16_t* tile, const float* row_c, const float* row_s, auto left) {
+      f32x16 S[XT];
+      scores<RP, XT>(tile, at, X, S);
+      uint32_t sign[8];
       if constexpr (COLS) {
         f32x4 c[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) c[g] = *reinterpret_cast<const f32x4*>(&row_c[sub * 32 + g * 8 + h * 4]);
+        for (int g = 0; g < 4; ++g) c[g] = *reinterpret_cast<const f32x4*>(&row_c[g * 8 + h * 4]);
 #pragma unroll
         for (int xt = 0; xt < XT; ++xt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) S[xt][i] = exp2_hw(fmaf(S[xt][i], a.scale, -c[i >> 2][i & 3]));
-        if (__ballot(row_s[sub * 32 + (lane & 31)] < 0.f)) {   // rare: rows with a negative weight
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 s = *reinterpret_cast<const f32x4*>(&row_s[sub * 32 + g * 8 + h * 4]);
-#pragma unroll
-            for (int xt = 0; xt < XT; ++xt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) S[xt][g * 4 + i] *= s[i];
-          }
+        for (int g = 0; g < 4; ++g) {
+          const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row_s) + g * 8 + h * 4);
+          sign[g * 2] = w.x;
+          sign[g * 2 + 1] = w.y;
         }
       } else {
-        if (y0 + 32 > a.ny) {   // the vocabulary ends inside this tile
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (y0 + (i >> 2) * 8 + h * 4 + (i & 3) >= a.ny)
-#pragma unroll
-              for (int xt = 0; xt < XT; ++xt) S[xt][i] = neg_inf();
-        }
-        float top[XT];
-        bool move = false;
-#pragma unroll
-        for (int xt = 0; xt < XT; ++xt) {
-          float v = S[xt][0];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) v = fmaxf(v, S[xt][i]);
-          top[xt] = v * a.scale;
-          move |= top[xt] > m[xt] + kSlack;
-        }
-        if (__ballot(move)) {
-#pragma unroll
-          for (int xt = 0; xt < XT; ++xt) {
-            const float mn = fmaxf(m[xt], fmaxf(top[xt], __shfl_xor(top[xt], 32)));
-            const float s = mn == m[xt] ? 1.f : exp2_hw(m[xt] - mn);
-            m[xt] = mn;
-            l[xt] *= s;
-            if constexpr (ACC) {
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) acc[xt][rt] *= s;
-            }
-          }
-        }
+        if constexpr (!std::is_same_v<decltype(left), std::integral_constant<int, 32>>) mask(S, left);
 #pragma unroll
         for (int xt = 0; xt < XT; ++xt) {
           float part[4] = {0.f, 0.f, 0.f, 0.f};
@@ -289,81 +365,103 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_bf16_kernel(StreamArg
       if constexpr (ACC) {
         // E as the right operand. It is rounded to bf16 here (off by at most
         // 2^-9 of itself, nearest even); products and sums stay in fp32.
-        bf16x8 E[XT][2];
-#pragma unroll
-        for (int xt = 0; xt < XT; ++xt)
-#pragma unroll
-          for (int s2 = 0; s2 < 2; ++s2) {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = pack_bf16(S[xt][s2 * 8 + i * 2], S[xt][s2 * 8 + i * 2 + 1]);
-            E[xt][s2] = __builtin_bit_cast(bf16x8, v);
-          }
-        // Y^T by transposing LDS reads: 16 lanes read 4 rows of 16 columns
-        // (lane i row i / 4, columns 4 (i % 4)..) and each receives a column.
-        const int q = (lane & 15) >> 2;
-        const int cl = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // the lane's chunk within 4
-        const int half = (lane & 1) * 4;
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
-          const int ra = sub * 32 + s2 * 16 + h * 4 + q, rb = ra + 8;
-          const int fa = swz_row<RP>(ra), fb = swz_row<RP>(rb);
+          bf16x8 E[XT];
+#pragma unroll
+          for (int xt = 0; xt < XT; ++xt) {
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = pack_bf16(S[xt][s2 * 8 + i * 2], S[xt][s2 * 8 + i * 2 + 1]);
+              if constexpr (COLS) v[i] ^= sign[s2 * 4 + i];
+            }
+            E[xt] = __builtin_bit_cast(bf16x8, v);
+          }
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const uint16_t* pa = tile + ra * RP + ((rt * 4 + cl) ^ fa) * 8 + half;
-            const uint16_t* pb = tile + rb * RP + ((rt * 4 + cl) ^ fb) * 8 + half;
-            const s16x4 va = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)pa);
-            const s16x4 vb = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)pb);
-            typedef short s16x8 __attribute__((ext_vector_type(8)));
-            const s16x8 v = {va[0], va[1], va[2], va[3], vb[0], vb[1], vb[2], vb[3]};
-            const bf16x8 A = __builtin_bit_cast(bf16x8, v);
+            const bf16x8 A = columns<RP>(tile + s2 * 16 * RP, at, rt);
 #pragma unroll
             for (int xt = 0; xt < XT; ++xt)
-              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, E[xt][s2], acc[xt][rt], 0, 0, 0);
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, E[xt], acc[xt][rt], 0, 0, 0);
           }
         }
       }
-    }
+    });
+    if constexpr (COLS) break;
+    // A sum within its limit shows that no exponential passed it (they are
+    // all positive). Past it, the share is done once more, from its largest
+    // score.
+    bool over = false;
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt) over |= !(l[xt] <= kMostSum);
+    if (attempt || !__syncthreads_or(over)) break;
+    each_subtile([&](const uint16_t* tile, const float*, const float*, auto left) {
+      f32x16 S[XT];
+      scores<RP, XT>(tile, at, X, S);
+      mask(S, left);
+      largest(S);
+    });
   }
 
   if constexpr (COLS) {
-    if (split == 0 && x0 < a.nx) {
-      // The teacher's part of this wave's columns: -w p / T z_n for every
-      // place. Eight places make one step of the contraction: the left
-      // operand gathers their rows of Z, the right one holds their weight in
-      // their column, as the sum of two bf16 (one per half of the wave's
-      // k slots), within 2^-17 of it.
-      const int64_t g = x0 / (32 * XT);
-      const uint32_t e1 = a.list_start[g + 1];
-      const uint16_t* Z = static_cast<const uint16_t*>(a.Z);
-      for (uint32_t e0 = a.list_start[g]; e0 < e1; e0 += 8) {
-        bf16x8 B[XT];
-        int64_t zrow[8];
+    if (split == 0) {
+      // The teacher's part of this wave's columns, -w p / T z_n for every
+      // place: their rows of Z are gathered into the wave's quarter of the
+      // tiles' LDS and go through the same product, with the places' weights
+      // as the right operand, as the sum of two bf16 (within 2^-17 of them).
+      constexpr int R = TY / 2;
+      uint16_t* tile = lds + wave * R * RP;
+      const uint32_t e_end = x0 < a.nx ? a.list_start[x0 / (32 * XT) + 1] : 0;
+      uint32_t e = x0 < a.nx ? a.list_start[x0 / (32 * XT)] : 0;
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
+      const auto entry = [&](uint32_t e0) {
+        const uint32_t i = e0 + lane % R;
+        return i < e_end ? a.list[i] : uint2{kRowMask, 0u};
+      };
+      uint2 en = entry(e);
+      for (; e < e_end; e += R) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint2 en = a.list[min(e0 + e, e1 - 1)];
-          const float w = e0 + e < e1 ? -__uint_as_float(en.y) : 0.f;
-          const float hi = bf16_to_f32(f32_to_bf16(w));
-          const float v = h ? w - hi : hi;
-          zrow[e] = (int64_t)(en.x & kRowMask) * a.r;
-#pragma unroll
-          for (int xt = 0; xt < XT; ++xt)
-            B[xt][e] = (__bf16)((int)(en.x >> kRowBits) == xt * 32 + (lane & 31) ? v : 0.f);
+        for (int i = 0; i < R * RP / 8 / kWave; ++i) {
+          const int p = i * kWave + lane;
+          const int row = p / (RP / 8), c = (p % (RP / 8)) ^ swz_row<RP>(row);
+          const uint32_t n = (uint32_t)__shfl((int)en.x, row) & kRowMask;
+          const uint32_t off = e + row < e_end ? n * (uint32_t)(RP * 2) + (uint32_t)c * 16u : 0xfffffff0u;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(tile + i * kWave * 8), 16, (int)off, 0, 0, 0);
         }
+        const uint2 next = entry(e + R);
+        __builtin_amdgcn_s_waitcnt(0xF70);
+        asm volatile("" ::: "memory");
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const int c = rt * 32 + (lane & 31);
-          typedef short s16x8 __attribute__((ext_vector_type(8)));
-          s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-          if (c < a.r) {
+        for (int s2 = 0; s2 < R / 16; ++s2) {
+          bf16x8 hi[XT], lo[XT];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (short)Z[zrow[e] + c];
+          for (int k = 0; k < 8; ++k) {
+            const int y = s2 * 16 + (k >> 2) * 8 + h * 4 + (k & 3);
+            const int col = (int)((uint32_t)__shfl((int)en.x, y) >> kRowBits);
+            const float w = -__int_as_float(__shfl((int)en.y, y));
+            const float wh = bf16_to_f32(f32_to_bf16(w));
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt) {
+              const bool mine = col == xt * 32 + (lane & 31);
+              hi[xt][k] = (__bf16)(mine ? wh : 0.f);
+              lo[xt][k] = (__bf16)(mine ? w - wh : 0.f);
+            }
           }
-          const bf16x8 A = __builtin_bit_cast(bf16x8, v);
 #pragma unroll
-          for (int xt = 0; xt < XT; ++xt)
-            acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, B[xt], acc[xt][rt], 0, 0, 0);
+          for (int rt = 0; rt < RT; ++rt) {
+            const bf16x8 A = columns<RP>(tile + s2 * 16 * RP, at, rt);
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt) {
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi[xt], acc[xt][rt], 0, 0, 0);
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[xt], acc[xt][rt], 0, 0, 0);
+            }
+          }
         }
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the tile has been read before it is filled again
+        asm volatile("" ::: "memory");
+        en = next;
       }
     }
 #pragma unroll
@@ -462,15 +560,16 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
     if constexpr (COLS) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t y = y0 + g * 4 + i;
-        S[i] = y < a.ny ? a.sgn[y] * exp2_hw(fmaf(S[i], a.scale, -a.beta[y])) : 0.f;
+        float* rc = const_cast<float*>(a.row_c);   // padded past ny
+        const float e = exp2_hw(fmaf(S[i], a.scale, -*row_c_at(rc, y0 + g * 4 + i, kRowBlock)));
+        S[i] = *row_sign_at(rc, y0 + g * 4 + i, kRowBlock) ? -e : e;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (y0 + g * 4 + i >= a.ny) S[i] = neg_inf();
       const float top = fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3])) * a.scale;
-      if (__ballot(top > m + kSlack)) {
+      if (__ballot(top > m)) {
         float mn = fmaxf(top, __shfl_xor(top, 16));
         mn = fmaxf(m, fmaxf(mn, __shfl_xor(mn, 32)));
         const float s = mn == m ? 1.f : exp2_hw(m - mn);
@@ -497,16 +596,15 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
   if constexpr (COLS) {
     if (split == 0 && x0 < a.nx) {
       const uint32_t e1 = a.list_start[x0 / 16 + 1];
-      const float* Z = static_cast<const float*>(a.Z);
       for (uint32_t e0 = a.list_start[x0 / 16]; e0 < e1; e0 += 4) {   // four places a step
         const uint2 en = a.list[min(e0 + g, e1 - 1)];
         const bool mine = e0 + g < e1 && (int)(en.x >> kRowBits) == col;
         const float B = mine ? -__uint_as_float(en.y) : 0.f;
-        const float* z = Z + (int64_t)(en.x & kRowMask) * a.r;
+        const float* z = Yp + (int64_t)(en.x & kRowMask) * a.ldy;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           const int c = rt * 16 + col;
-          acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(c < a.r ? z[c] : 0.f, B, acc[rt], 0, 0, 0);
+          acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(z[c], B, acc[rt], 0, 0, 0);
         }
       }
     }
@@ -640,11 +738,17 @@ template <typename T>
 __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     const T* __restrict__ Z, const int32_t* __restrict__ idx, const float* __restrict__ t,
     const float* __restrict__ lse, const float* __restrict__ G, const float* __restrict__ weight, int64_t N,
-    int64_t V, int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ beta,
-    float* __restrict__ sgn, int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
+    int64_t V, int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ row_c,
+    int RB, int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
   const int64_t n = (int64_t)blockIdx.x * kWaves + wave_id();
   const int lane = threadIdx.x & 63;
-  if (n >= N) return;
+  if (n >= N) {   // the last tile's rows past N
+    if (zc && n < (N + 63) / 64 * 64 && lane == 0) {
+      *row_c_at(row_c, n, RB) = __builtin_inff();
+      *row_sign_at(row_c, n, RB) = 0;
+    }
+    return;
+  }
   int id;
   float p, logp;
   const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);
@@ -655,8 +759,8 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     for (int i = lane; i < r; i += kWave) dZ[n * r + i] = store_cast<T>(live ? w * G[n * r + i] : 0.f);
   if (!zc) return;
   if (lane == 0) {
-    beta[n] = live ? lse[n] * kLog2e - log2f(fabsf(c)) : __builtin_inff();
-    sgn[n] = live && c < 0.f ? -1.f : 1.f;
+    *row_c_at(row_c, n, RB) = live ? lse[n] * kLog2e - log2f(fabsf(c)) : __builtin_inff();
+    *row_sign_at(row_c, n, RB) = live && c < 0.f ? 0x8000 : 0;
   }
   for (int i = lane; i < RP; i += kWave) zc[n * RP + i] = live && i < r ? Z[n * r + i] : T(0);
   if (!live) id = INT_MAX;
@@ -791,10 +895,11 @@ struct Plan {
   int GC;            // columns of a group (a wave)
   int64_t groups;
   int col_splits;
+  int RB;            // rows of a tile of the columns pass
   int64_t npad;
   // workspace offsets
   size_t pm, pl, po, fwd_total;
-  size_t zc, beta, sgn, srt_id, srt_w, table, start, list, part, bwd_total;
+  size_t zc, row_c, srt_id, srt_w, table, start, list, part, bwd_total;
 };
 
 Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
@@ -803,7 +908,7 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   p.RP = round_rank(r);
   int64_t xblocks, ytiles, cblocks;
   if (dtype == 0) {
-    p.XT = p.RP <= 256 ? 2 : 1;
+    p.XT = x_tiles(p.RP);
     p.WX = N <= 32 * p.XT && p.RP < 512 ? 1 : N <= 64 * p.XT ? 2 : 4;
     xblocks = ceil_div(N, p.WX * 32 * p.XT);
     ytiles = ceil_div(V, std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX)));
@@ -823,6 +928,7 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   cblocks = ceil_div(p.groups, kWaves);
   const int64_t ntiles = ceil_div(N, dtype == 0 ? (p.RP <= 128 ? 64 : 32) : 16);
   p.col_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTargetBlocks / cblocks, ntiles));
+  p.RB = dtype == 0 && p.RP > 128 ? 32 : 64;
   p.npad = ceil_div(N, 64) * 64;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
@@ -836,8 +942,7 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   p.fwd_total = o;
   o = 0;
   p.zc = take(size_t(N) * p.RP * es);
-  p.beta = take(size_t(N) * 4);
-  p.sgn = take(size_t(N) * 4);
+  p.row_c = take(size_t(p.npad) * 8);
   p.srt_id = take(size_t(N) * k * 4);
   p.srt_w = take(size_t(N) * k * 4);
   p.table = take(size_t(p.groups + 1) * p.npad);
@@ -876,19 +981,19 @@ hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) 
   if (dtype == 0) {
     if constexpr (COLS) {
       switch (p.RP) {
-        case 32: return go_bf16<32, 2, 4, true, true>(a, s);
-        case 64: return go_bf16<64, 2, 4, true, true>(a, s);
-        case 128: return go_bf16<128, 2, 4, true, true>(a, s);
-        case 256: return go_bf16<256, 2, 4, true, true>(a, s);
-        default: return go_bf16<512, 1, 4, true, true>(a, s);
+        case 32: return go_bf16<32, x_tiles(32), 4, true, true>(a, s);
+        case 64: return go_bf16<64, x_tiles(64), 4, true, true>(a, s);
+        case 128: return go_bf16<128, x_tiles(128), 4, true, true>(a, s);
+        case 256: return go_bf16<256, x_tiles(256), 4, true, true>(a, s);
+        default: return go_bf16<512, x_tiles(512), 4, true, true>(a, s);
       }
     } else {
       switch (p.RP) {
-        case 32: return go_rows<32, 2, ACC>(a, p.WX, s);
-        case 64: return go_rows<64, 2, ACC>(a, p.WX, s);
-        case 128: return go_rows<128, 2, ACC>(a, p.WX, s);
-        case 256: return go_rows<256, 2, ACC>(a, p.WX, s);
-        default: return go_rows<512, 1, ACC>(a, p.WX, s);
+        case 32: return go_rows<32, x_tiles(32), ACC>(a, p.WX, s);
+        case 64: return go_rows<64, x_tiles(64), ACC>(a, p.WX, s);
+        case 128: return go_rows<128, x_tiles(128), ACC>(a, p.WX, s);
+        case 256: return go_rows<256, x_tiles(256), ACC>(a, p.WX, s);
+        default: return go_rows<512, x_tiles(512), ACC>(a, p.WX, s);
       }
     }
   }
@@ -913,10 +1018,10 @@ void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
 
 template <typename T>
 void prep(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
-  hipLaunchKernelGGL(distill_prep_kernel<T>, dim3((unsigned)ceil_div(d.N, kWaves)), dim3(kWaves * kWave), 0, s,
+  hipLaunchKernelGGL(distill_prep_kernel<T>, dim3((unsigned)(p.npad / kWaves)), dim3(kWaves * kWave), 0, s,
                      static_cast<const T*>(d.Z), d.idx, d.t, d.lse, d.G, d.weight, d.N, d.V, d.r, p.RP, d.k, d.inv_t,
-                     d.dP ? reinterpret_cast<T*>(ws + p.zc) : nullptr, reinterpret_cast<float*>(ws + p.beta),
-                     reinterpret_cast<float*>(ws + p.sgn), reinterpret_cast<int*>(ws + p.srt_id),
+                     d.dP ? reinterpret_cast<T*>(ws + p.zc) : nullptr, reinterpret_cast<float*>(ws + p.row_c),
+                     p.RB, reinterpret_cast<int*>(ws + p.srt_id),
                      reinterpret_cast<float*>(ws + p.srt_w), static_cast<T*>(d.dZ));
 }
 
@@ -981,11 +1086,9 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   a.ldy = p.RP;
   a.scale = d.scale;
   a.splits = p.col_splits;
-  a.beta = reinterpret_cast<float*>(ws + p.beta);
-  a.sgn = reinterpret_cast<float*>(ws + p.sgn);
+  a.row_c = reinterpret_cast<float*>(ws + p.row_c);
   a.list_start = start;
   a.list = list;
-  a.Z = d.Z;
   a.dP = d.dP;
   a.part = reinterpret_cast<float*>(ws + p.part);
   e = stream<true, true>(d.dtype, p, a, s);
