@@ -51,6 +51,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // to leave the matrix cores' registers for it) are ever rescaled.
 constexpr float kMostSum = 0x1p60f;
 constexpr int kWaves = 4;
+constexpr int kMaxShares = 512;   // of a row of Z
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -637,6 +638,15 @@ template <typename T> __device__ __forceinline__ float widen(T x);
 template <> __device__ __forceinline__ float widen<uint16_t>(uint16_t x) { return bf16_to_f32(x); }
 template <> __device__ __forceinline__ float widen<float>(float x) { return x; }
 
+__device__ __forceinline__ float dot8(const uint16_t* a, const uint16_t* b, float acc) {
+  return dot8_bf16(load16(a), load16(b), acc);
+}
+__device__ __forceinline__ float dot8(const float* a, const float* b, float acc) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc = fmaf(a[i], b[i], acc);
+  return acc;
+}
+
 // The teacher's distribution over a row's places, lane j holding place j: a
 // place is empty (p = 0, id = INT_MAX) when its id lies outside [0, V) or its
 // logit is NaN or -inf. logp is log p where p > 0. Returns whether the row
@@ -660,18 +670,24 @@ __device__ __forceinline__ bool teacher(const int32_t* idx, const float* t, int6
   return true;
 }
 
-// Joins the shares of the rows pass: loss, lse and, with G, dloss/dz. One
-// block per row.
+// Joins the shares of the rows pass. A block takes one row and 64 of its
+// columns: 16 lanes hold 4 columns each, and 16 such groups share out the
+// shares of the weighted sum and the teacher's places. The first block of a
+// row also writes its lse and loss.
+constexpr int kJoinCols = 64;
 template <typename T>
 __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
     const T* __restrict__ Z, const T* __restrict__ P, const int32_t* __restrict__ idx, const float* __restrict__ t,
     int64_t N, int64_t V, int r, int RP, int k, float inv_t, int shares, const float* __restrict__ pm,
     const float* __restrict__ pl, const float* __restrict__ po, float* __restrict__ loss, float* __restrict__ lse,
     float* __restrict__ G) {
-  __shared__ float sp[kWave], sdot[kWave], red[kWaves * 2];
+  __shared__ float sp[kWave], sdot[kWave], red[kWaves * 2], share_w[kMaxShares];
   __shared__ int sid[kWave];
-  const int64_t n = blockIdx.x;
-  const int wave = wave_id(), lane = threadIdx.x & 63;
+  __shared__ f32x4 part[kWaves * 4][16];
+  const int chunks = G ? (r + kJoinCols - 1) / kJoinCols : 1;
+  const int64_t n = blockIdx.x / chunks;
+  const int chunk = blockIdx.x % chunks;
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   int id;
   float p, logp;
   const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);   // every wave: the same values
@@ -679,34 +695,37 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
     sid[lane] = id;
     sp[lane] = p;
   }
-  // maximum and sum over the shares, by the whole block
   float m = neg_inf();
-  for (int s = threadIdx.x; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
+  for (int s = tid; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
 #pragma unroll
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   if (lane == 0) red[wave] = m;
   __syncthreads();
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   float l = 0.f;
-  for (int s = threadIdx.x; s < shares; s += kWaves * kWave) {
+  for (int s = tid; s < shares; s += kWaves * kWave) {
     const float ps = pl[(int64_t)s * N + n];
-    if (ps != 0.f) l += ps * exp2_hw(pm[(int64_t)s * N + n] - m);   // a share without rows has sum 0
+    const float w = ps != 0.f ? exp2_hw(pm[(int64_t)s * N + n] - m) : 0.f;   // a share without rows has sum 0
+    share_w[s] = w;
+    l = fmaf(ps, w, l);
   }
   l = group_sum<kWave>(l);
   if (lane == 0) red[kWaves + wave] = l;
-  // the places' scores
-  for (int j = wave; j < k; j += kWaves) {
-    const int v = sid[j];
-    float d = 0.f;
-    if (v != INT_MAX)
-      for (int c = lane; c < r; c += kWave) d = fmaf(widen<T>(P[(int64_t)v * r + c]), widen<T>(Z[n * r + c]), d);
-    d = group_sum<kWave>(d);
-    if (lane == 0) sdot[j] = d;
+  const int group = tid >> 4, sub = tid & 15;
+  if (chunk == 0) {   // the places' scores: 16 lanes per place
+    for (int j = group; j < k; j += kWaves * 4) {
+      const int v = sid[j];
+      float d = 0.f;
+      if (v != INT_MAX)
+        for (int c = sub * 8; c < r; c += 128) d = dot8(P + (int64_t)v * r + c, Z + n * r + c, d);
+      d = group_sum<16>(d);
+      if (sub == 0) sdot[j] = d;
+    }
   }
   __syncthreads();
   l = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
-  const float ls = (m + log2f(l)) * kLn2;
-  if (wave == 0) {
+  if (chunk == 0 && wave == 0) {
+    const float ls = (m + log2f(l)) * kLn2;
     const float s = lane < k && p > 0.f ? sdot[lane] * inv_t : 0.f;
     const float e = group_sum<kWave>(p > 0.f ? p * (logp - s + ls) : 0.f);
     if (lane == 0) {
@@ -716,17 +735,32 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   }
   if (!G) return;
   const float il = 1.f / l;
-  for (int c = threadIdx.x; c < r; c += kWaves * kWave) {
-    float o = 0.f;
-    for (int s = 0; s < shares; ++s) {
-      if (pl[(int64_t)s * N + n] != 0.f)
-        o = fmaf(po[((int64_t)s * N + n) * RP + c], exp2_hw(pm[(int64_t)s * N + n] - m), o);
+  const int c = chunk * kJoinCols + sub * 4;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  if (c < r) {
+#pragma unroll 4
+    for (int s = group; s < shares; s += kWaves * 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(po + ((int64_t)s * N + n) * RP + c);
+      const float w = share_w[s];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], w, o[i]);
     }
     o *= il;
-    float q = 0.f;
-    for (int j = 0; j < k; ++j)
-      if (sid[j] != INT_MAX) q = fmaf(sp[j], widen<T>(P[(int64_t)sid[j] * r + c]), q);
-    G[n * r + c] = any ? (o - q) * inv_t : 0.f;
+    for (int j = group; j < k; j += kWaves * 4) {
+      if (sid[j] == INT_MAX) continue;
+      const T* q = P + (int64_t)sid[j] * r + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(-sp[j], widen<T>(q[i]), o[i]);
+    }
+  }
+  part[group][sub] = o;
+  __syncthreads();
+  if (group == 0 && c < r) {
+#pragma unroll
+    for (int g = 1; g < kWaves * 4; ++g) o += part[g][sub];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = any ? o[i] * inv_t : 0.f;
+    *reinterpret_cast<f32x4*>(G + n * r + c) = o;
   }
 }
 
@@ -775,32 +809,36 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
   }
 }
 
-// table[g][n] = how many of row n's places have an id below g * GC: one lane
-// per row, walking up its sorted places over a range of column groups.
-constexpr int kTableGroups = 64;   // groups per wave
-__global__ void __launch_bounds__(kWave) distill_table_kernel(const int* __restrict__ srt_id, int64_t N, int64_t npad,
-                                                              int k, int GC, int64_t groups,
-                                                              uint8_t* __restrict__ table) {
-  const int64_t ranges = (groups + kTableGroups) / kTableGroups;   // of the groups + 1 boundaries
-  const int64_t n = blockIdx.x / ranges * kWave + threadIdx.x;
-  const int64_t g0 = blockIdx.x % ranges * kTableGroups, g1 = min(g0 + kTableGroups, groups + 1);
-  const int* id = srt_id + n * k;
-  int j = 0;
-  if (n < N) {   // first place at or above the range
-    int hi = k;
-    while (j < hi) {
-      const int mid = (j + hi) >> 1;
-      if (id[mid] < g0 * GC && id[mid] != INT_MAX) j = mid + 1;
-      else hi = mid;
-    }
+// table[g][n] = how many of row n's places have an id below g * GC. A block
+// takes 64 rows, their sorted ids in LDS; a wave walks up them, one lane per
+// row, over a range of column groups.
+constexpr int kTableGroups = 32;   // groups per wave
+__global__ void __launch_bounds__(kWaves* kWave) distill_table_kernel(const int* __restrict__ srt_id, int64_t N,
+                                                                      int64_t npad, int k, int GC, int64_t groups,
+                                                                      uint8_t* __restrict__ table) {
+  __shared__ int ids[kWave * (kWave + 1)];
+  const int64_t ranges = (groups + 1 + kTableGroups * kWaves - 1) / (kTableGroups * kWaves);
+  const int64_t n0 = blockIdx.x / ranges * kWave;
+  const int rows = (int)min(N - n0, (int64_t)kWave);
+  for (int i = threadIdx.x; i < rows * k; i += kWaves * kWave) ids[i / k * (kWave + 1) + i % k] = srt_id[n0 * k + i];
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  const int64_t g0 = (blockIdx.x % ranges * kWaves + wave_id()) * kTableGroups, g1 = min(g0 + kTableGroups, groups + 1);
+  const int* id = ids + lane * (kWave + 1);
+  const int have = lane < rows ? k : 0;
+  int j = 0, hi = have;
+  while (j < hi) {   // first place at or above the range
+    const int mid = (j + hi) >> 1;
+    if (id[mid] < g0 * GC && id[mid] != INT_MAX) j = mid + 1;
+    else hi = mid;
   }
-  int64_t next = n < N && j < k ? id[j] : INT_MAX;
+  int next = j < have ? id[j] : INT_MAX;
   for (int64_t g = g0; g < g1; ++g) {
     while (next < g * GC && next != INT_MAX) {
       ++j;
-      next = j < k ? id[j] : INT_MAX;
+      next = j < have ? id[j] : INT_MAX;
     }
-    table[g * npad + n] = (uint8_t)j;
+    table[g * npad + n0 + lane] = (uint8_t)j;
   }
 }
 
@@ -883,7 +921,6 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int round_rank(int r) { return r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 ? 128 : r <= 256 ? 256 : 512; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kMaxShares = 512;
 constexpr int kTargetBlocks = 512;   // two blocks per compute unit
 
 struct Plan {
@@ -1010,7 +1047,7 @@ hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) 
 
 template <typename T>
 void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
-  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)d.N), dim3(kWaves * kWave), 0, s,
+  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)(d.N * (d.G ? ceil_div(d.r, kJoinCols) : 1))), dim3(kWaves * kWave), 0, s,
                      static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t, d.N, d.V, d.r, p.RP, d.k,
                      d.inv_t, p.shares, reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
                      reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
@@ -1074,7 +1111,8 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   uint32_t* start = reinterpret_cast<uint32_t*>(ws + p.start);
   uint2* list = reinterpret_cast<uint2*>(ws + p.list);
   hipLaunchKernelGGL(distill_table_kernel,
-                     dim3((unsigned)(p.npad / kWave * ceil_div(p.groups + 1, kTableGroups))), dim3(kWave), 0, s, srt_id, d.N, p.npad, d.k, p.GC, p.groups, table);
+                     dim3((unsigned)(p.npad / kWave * ceil_div(p.groups + 1, kTableGroups * kWaves))),
+                     dim3(kWaves * kWave), 0, s, srt_id, d.N, p.npad, d.k, p.GC, p.groups, table);
   hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(256), 0, s, table, srt_id, srt_w, p.npad,
                      d.k, p.GC, start, list);
   StreamArgs a{};
