@@ -43,6 +43,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kRawBufferFlags = 0x00020000;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLo = 1.92596299e-8f;   // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 // The exponents of the rows pass are taken from the largest of a share's
 // first scores, not from a running maximum: fp32 and bf16 have range to
@@ -54,6 +55,7 @@ constexpr int kWaves = 4;
 constexpr int kMaxShares = 512;   // of a row of Z
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }   // of normal numbers
 
 // Two fp32 as packed bf16, each rounded to nearest even.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -70,7 +72,8 @@ struct StreamArgs {
   int64_t nx, ny;
   int r, ldy;
   float scale;          // log2(e) / T
-  int splits;           // shares of Y, one block each
+  int64_t whole;        // blocks of X that stream all of Y (the first ones)
+  int splits;           // shares of Y of the others, one block each
   // rows pass: a share's maximum (log2 domain), sum and weighted sum of P
   float* pm;            // [share][nx]
   float* pl;
@@ -79,18 +82,20 @@ struct StreamArgs {
   // [tile] of the rows of Z: RB times c (+inf for rows without weight), RB
   // times the weight's sign as bit 15 of 16 bits, padding to 2 RB words
   const float* row_c;
-  const uint32_t* list_start;   // [groups + 1]: a group of columns' teacher places in `list`
-  const uint2* list;    // (row | local column << kRowBits, bits of w p / T), by row within a group
-  void* dP;             // V x r, with one share
-  float* part;          // [share][nx][RP], with more
+  const uint32_t* list_start;   // [groups + 1]: the teacher places of a group of columns in `list`
+  const uint2* list;    // (row | local column << kRowBits, -w p / T), by row within a group
+  void* dP;             // V x r, from whole blocks
+  float* part;          // [share][row of X past the whole blocks'][RP], from the others
 };
-constexpr int kRowBits = 20;   // N <= 2^20
+constexpr int kRowBits = 20;   // N <= 2^20, groups of at most 2^12 columns
 constexpr uint32_t kRowMask = (1u << kRowBits) - 1;
 
 constexpr int kRowBlock = 64;   // RB of the fp32 kernel
-__device__ __forceinline__ float* row_c_at(float* row_c, int64_t n, int RB) { return row_c + n / RB * (2 * RB) + n % RB; }
-__device__ __forceinline__ uint16_t* row_sign_at(float* row_c, int64_t n, int RB) {
-  return reinterpret_cast<uint16_t*>(row_c + n / RB * (2 * RB) + RB) + n % RB;
+__device__ __forceinline__ float* row_c_at(float* row_c, uint32_t n, uint32_t RB) {   // RB a power of two
+  return row_c + n + (n & ~(RB - 1));
+}
+__device__ __forceinline__ uint16_t* row_sign_at(float* row_c, uint32_t n, uint32_t RB) {
+  return reinterpret_cast<uint16_t*>(row_c + 2 * (n & ~(RB - 1)) + RB) + (n & (RB - 1));
 }
 
 // 16-byte chunk c of row y of an LDS tile sits at chunk c ^ swz_row(y). A wave
@@ -209,6 +214,11 @@ __device__ __forceinline__ bf16x8 columns(const uint16_t* rows16, const Places<R
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Rows 8 g + 4 h .. + 3 of the lane's column of a result.
+__device__ __forceinline__ f32x4 quad(const f32x16& v, int g) {
+  return f32x4{v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]};
+}
+
 // Tiles of 32 rows of X that a wave owns. Two halve the LDS reads of each
 // product, but from r = 128 on they take more than half of the registers, and
 // the one wave that is left to a SIMD cannot hide its exponentials behind
@@ -227,22 +237,11 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   float* const rows = reinterpret_cast<float*>(lds + 2 * TY * RP);   // [buffer][offset, sign][TY]
   const int lane = threadIdx.x & 63, h = lane >> 5, wave = wave_id();
   const int wx = wave % WX, wy = wave / WX;
-  const int64_t xtile = blockIdx.x / a.splits;
-  const int split = blockIdx.x % a.splits;
+  const bool whole = blockIdx.x < a.whole;
+  const int splits = whole ? 1 : a.splits;
+  const int64_t xtile = whole ? blockIdx.x : a.whole + (blockIdx.x - a.whole) / splits;
+  const int split = whole ? 0 : (int)((blockIdx.x - a.whole) % splits);
   const int64_t x0 = (xtile * WX + wx) * (32 * XT);
-
-  bf16x8 X[XT][KS];
-#pragma unroll
-  for (int xt = 0; xt < XT; ++xt) {
-    const int64_t x = x0 + xt * 32 + (lane & 31);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int c = ks * 16 + h * 8;
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (x < a.nx && c < a.r) v = load16(static_cast<const uint16_t*>(a.X) + x * a.r + c);
-      X[xt][ks] = __builtin_bit_cast(bf16x8, v);
-    }
-  }
 
   f32x16 acc[XT][ACC ? RT : 1] = {};
   float m[XT], l[XT];
@@ -253,7 +252,9 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   }
 
   const int64_t nt = (a.ny + TY - 1) / TY;
-  const int64_t t_begin = nt * split / a.splits, t_end = nt * (split + 1) / a.splits;
+  const int64_t t_begin = nt * split / splits, t_end = nt * (split + 1) / splits;
+  Places<RP> at;
+  at.init();
   TileCopy<RP, TY> copy;
   copy.init(a.Y, a.ny, a.r, a.ldy);
   const auto stage = [&](int buf, int64_t t) {
@@ -265,8 +266,83 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
             (lds_ptr_t)(rows + buf * 2 * TY + wave * kWave), 4, 0, 0);
     }
   };
-  Places<RP> at;
-  at.init();
+  if constexpr (COLS) {
+    if (split == 0) {
+      // First the teacher's part of the block's columns, -w p / T z_n for every
+      // place: the places' rows of Z are gathered into the tiles' LDS and go
+      // through the same product, with the places' weights as the right
+      // operand, each the sum of two bf16 (within 2^-17 of it; in one word).
+      const uint32_t e_end = a.list_start[xtile + 1];
+      uint32_t e = a.list_start[xtile];
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
+      const auto gather = [&](int buf, uint32_t e0) {   // returns the lane's place (of TY)
+        const uint32_t i = e0 + lane % TY;
+        const uint2 en = i < e_end ? a.list[i] : uint2{0u, 0u};
+#pragma unroll
+        for (int j = 0; j < copy.kLoads; ++j) {
+          const int p = (j * kWaves + wave) * kWave + lane;
+          const int row = p / (RP / 8), c = (p % (RP / 8)) ^ swz_row<RP>(row);
+          const uint32_t n = (uint32_t)__shfl((int)en.x, row) & kRowMask;
+          const uint32_t off = e0 + row < e_end ? n * (uint32_t)(RP * 2) + (uint32_t)c * 16u : 0xfffffff0u;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(lds + buf * TY * RP + (j * kWaves + wave) * kWave * 8),
+                                                   16, (int)off, 0, 0, 0);
+        }
+        return en;
+      };
+      uint2 en = {0u, 0u};
+      if (e < e_end) en = gather(0, e);
+      for (int buf = 0; e < e_end; e += TY, buf ^= 1) {
+        __builtin_amdgcn_s_waitcnt(0xF70);
+        __syncthreads();
+        uint2 next = {0u, 0u};
+        if (e + TY < e_end) next = gather(buf ^ 1, e + TY);
+        const uint16_t* tile = lds + buf * TY * RP;
+#pragma unroll 1
+        for (int s = 0; s < TY / 16; ++s) {
+          if (e + s * 16 >= e_end) break;
+          bf16x8 hi[XT], lo[XT];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int y = s * 16 + (k >> 2) * 8 + h * 4 + (k & 3);
+            const int col = (int)((uint32_t)__shfl((int)en.x, y) >> kRowBits) - wx * (32 * XT);
+            const uint32_t w = (uint32_t)__shfl((int)en.y, y);
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt) {
+              const uint32_t v = col == xt * 32 + (lane & 31) ? w : 0u;
+              hi[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)v);
+              lo[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)(v >> 16));
+            }
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const bf16x8 A = columns<RP>(tile + s * 16 * RP, at, rt);
+#pragma unroll
+            for (int xt = 0; xt < XT; ++xt) {
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi[xt], acc[xt][rt], 0, 0, 0);
+              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[xt], acc[xt][rt], 0, 0, 0);
+            }
+          }
+        }
+        en = next;
+      }
+      __syncthreads();   // the tiles may be filled again
+    }
+  }
+  bf16x8 X[XT][KS];
+#pragma unroll
+  for (int xt = 0; xt < XT; ++xt) {
+    const int64_t x = x0 + xt * 32 + (lane & 31);
+    const uint16_t* row = static_cast<const uint16_t*>(a.X) + min(x, a.nx - 1) * a.r;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = ks * 16 + h * 8;
+      const bool ok = x < a.nx && c < a.r;
+      const u32x4 v = load16(row + (ok ? c : 0));
+      X[xt][ks] = __builtin_bit_cast(bf16x8, ok ? v : u32x4{0u, 0u, 0u, 0u});
+    }
+  }
+
   // Calls f(subtile, row values, rows left) for this wave's subtiles of the
   // share. Rows left is a constant 32 but for the rows pass's last tile,
   // where the vocabulary may end (the columns pass pads its rows).
@@ -329,8 +405,10 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
       l[xt] = 0.f;
+      if constexpr (!COLS) {
 #pragma unroll
-      for (int rt = 0; rt < (ACC ? RT : 1); ++rt) acc[xt][rt] = f32x16{};
+        for (int rt = 0; rt < (ACC ? RT : 1); ++rt) acc[xt][rt] = f32x16{};
+      }
     }
     each_subtile([&](const uint16_t* tile, const float* row_c, const float* row_s, auto left) {
       f32x16 S[XT];
@@ -346,9 +424,10 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
           for (int i = 0; i < 16; ++i) S[xt][i] = exp2_hw(fmaf(S[xt][i], a.scale, -c[i >> 2][i & 3]));
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(row_s) + g * 8 + h * 4);
-          sign[g * 2] = w.x;
-          sign[g * 2 + 1] = w.y;
+          typedef float f32x2 __attribute__((ext_vector_type(2)));
+          const f32x2 w = *reinterpret_cast<const f32x2*>(row_s + g * 4 + h * 2);
+          sign[g * 2] = __float_as_uint(w[0]);
+          sign[g * 2 + 1] = __float_as_uint(w[1]);
         }
       } else {
         if constexpr (!std::is_same_v<decltype(left), std::integral_constant<int, 32>>) mask(S, left);
@@ -406,83 +485,25 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   }
 
   if constexpr (COLS) {
-    if (split == 0) {
-      // The teacher's part of this wave's columns, -w p / T z_n for every
-      // place: their rows of Z are gathered into the wave's quarter of the
-      // tiles' LDS and go through the same product, with the places' weights
-      // as the right operand, as the sum of two bf16 (within 2^-17 of them).
-      constexpr int R = TY / 2;
-      uint16_t* tile = lds + wave * R * RP;
-      const uint32_t e_end = x0 < a.nx ? a.list_start[x0 / (32 * XT) + 1] : 0;
-      uint32_t e = x0 < a.nx ? a.list_start[x0 / (32 * XT)] : 0;
-      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
-      const auto entry = [&](uint32_t e0) {
-        const uint32_t i = e0 + lane % R;
-        return i < e_end ? a.list[i] : uint2{kRowMask, 0u};
-      };
-      uint2 en = entry(e);
-      for (; e < e_end; e += R) {
-#pragma unroll
-        for (int i = 0; i < R * RP / 8 / kWave; ++i) {
-          const int p = i * kWave + lane;
-          const int row = p / (RP / 8), c = (p % (RP / 8)) ^ swz_row<RP>(row);
-          const uint32_t n = (uint32_t)__shfl((int)en.x, row) & kRowMask;
-          const uint32_t off = e + row < e_end ? n * (uint32_t)(RP * 2) + (uint32_t)c * 16u : 0xfffffff0u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(tile + i * kWave * 8), 16, (int)off, 0, 0, 0);
-        }
-        const uint2 next = entry(e + R);
-        __builtin_amdgcn_s_waitcnt(0xF70);
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int s2 = 0; s2 < R / 16; ++s2) {
-          bf16x8 hi[XT], lo[XT];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int y = s2 * 16 + (k >> 2) * 8 + h * 4 + (k & 3);
-            const int col = (int)((uint32_t)__shfl((int)en.x, y) >> kRowBits);
-            const float w = -__int_as_float(__shfl((int)en.y, y));
-            const float wh = bf16_to_f32(f32_to_bf16(w));
-#pragma unroll
-            for (int xt = 0; xt < XT; ++xt) {
-              const bool mine = col == xt * 32 + (lane & 31);
-              hi[xt][k] = (__bf16)(mine ? wh : 0.f);
-              lo[xt][k] = (__bf16)(mine ? w - wh : 0.f);
-            }
-          }
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const bf16x8 A = columns<RP>(tile + s2 * 16 * RP, at, rt);
-#pragma unroll
-            for (int xt = 0; xt < XT; ++xt) {
-              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi[xt], acc[xt][rt], 0, 0, 0);
-              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[xt], acc[xt][rt], 0, 0, 0);
-            }
-          }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the tile has been read before it is filled again
-        asm volatile("" ::: "memory");
-        en = next;
-      }
-    }
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
       const int64_t x = x0 + xt * 32 + (lane & 31);
       if (x >= a.nx) continue;
+      if (splits > 1) {
+        const int64_t first = a.whole * (WX * 32 * XT);
+        float* row = a.part + ((int64_t)split * (a.nx - first) + x - first) * RP + h * 4;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+        for (int i = 0; i < RT * 4; ++i) *reinterpret_cast<f32x4*>(row + i * 8) = quad(acc[xt][i >> 2], i & 3);
+      } else {
+        uint16_t* row = static_cast<uint16_t*>(a.dP) + x * a.r + h * 4;
+        const int have = (a.r - h * 4 + 7) / 8;   // quads of this lane that exist: r is a multiple of 8
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = rt * 32 + g * 8 + h * 4;
-          const f32x4 v = {acc[xt][rt][g * 4], acc[xt][rt][g * 4 + 1], acc[xt][rt][g * 4 + 2],
-                           acc[xt][rt][g * 4 + 3]};
-          if (a.splits > 1) {
-            *reinterpret_cast<f32x4*>(a.part + ((int64_t)split * a.nx + x) * RP + c) = v;
-          } else if (c < a.r) {
-            const uint2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dP) + x * a.r + c) = b;
-          }
+        for (int i = 0; i < RT * 4; ++i) {
+          const f32x4 v = quad(acc[xt][i >> 2], i & 3);
+          const uint2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+          if (i < have) *reinterpret_cast<uint2*>(row + i * 8) = b;
         }
+      }
     }
   } else {
     const int64_t share = (int64_t)split * WY + wy;
@@ -496,14 +517,9 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
         a.pl[share * a.nx + x] = lt;
       }
       if constexpr (ACC) {
+        float* row = a.po + (share * a.nx + x) * RP + h * 4;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 v = {acc[xt][rt][g * 4], acc[xt][rt][g * 4 + 1], acc[xt][rt][g * 4 + 2],
-                             acc[xt][rt][g * 4 + 3]};
-            *reinterpret_cast<f32x4*>(a.po + (share * a.nx + x) * RP + rt * 32 + g * 8 + h * 4) = v;
-          }
+        for (int i = 0; i < RT * 4; ++i) *reinterpret_cast<f32x4*>(row + i * 8) = quad(acc[xt][i >> 2], i & 3);
       }
     }
   }
@@ -518,8 +534,10 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
   constexpr int TY = 16, LD = RP + 4, KC = RP / 16, RT = RP / 16;
   __shared__ __attribute__((aligned(16))) float tile[TY * LD];
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15, wave = wave_id();
-  const int64_t xtile = blockIdx.x / a.splits;
-  const int split = blockIdx.x % a.splits;
+  const bool whole = blockIdx.x < a.whole;
+  const int splits = whole ? 1 : a.splits;
+  const int64_t xtile = whole ? blockIdx.x : a.whole + (blockIdx.x - a.whole) / splits;
+  const int split = whole ? 0 : (int)((blockIdx.x - a.whole) % splits);
   const int64_t x0 = (xtile * kWaves + wave) * 16;
   const int64_t x = x0 + col;
   const float* Yp = static_cast<const float*>(a.Y);
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
   float m = neg_inf(), l = 0.f;
 
   const int64_t nt = (a.ny + TY - 1) / TY;
-  const int64_t t_begin = nt * split / a.splits, t_end = nt * (split + 1) / a.splits;
+  const int64_t t_begin = nt * split / splits, t_end = nt * (split + 1) / splits;
   for (int64_t t = t_begin; t < t_end; ++t) {
     __syncthreads();
 #pragma unroll
@@ -562,8 +580,8 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float* rc = const_cast<float*>(a.row_c);   // padded past ny
-        const float e = exp2_hw(fmaf(S[i], a.scale, -*row_c_at(rc, y0 + g * 4 + i, kRowBlock)));
-        S[i] = *row_sign_at(rc, y0 + g * 4 + i, kRowBlock) ? -e : e;
+        const float e = exp2_hw(fmaf(S[i], a.scale, -*row_c_at(rc, (uint32_t)(y0 + g * 4 + i), kRowBlock)));
+        S[i] = *row_sign_at(rc, (uint32_t)(y0 + g * 4 + i), kRowBlock) ? -e : e;
       }
     } else {
 #pragma unroll
@@ -600,7 +618,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
       for (uint32_t e0 = a.list_start[x0 / 16]; e0 < e1; e0 += 4) {   // four places a step
         const uint2 en = a.list[min(e0 + g, e1 - 1)];
         const bool mine = e0 + g < e1 && (int)(en.x >> kRowBits) == col;
-        const float B = mine ? -__uint_as_float(en.y) : 0.f;
+        const float B = mine ? __uint_as_float(en.y) : 0.f;
         const float* z = Yp + (int64_t)(en.x & kRowMask) * a.ldy;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -613,7 +631,9 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int c = rt * 16 + g * 4;
-      if (a.splits > 1) *reinterpret_cast<f32x4*>(a.part + ((int64_t)split * a.nx + x) * RP + c) = acc[rt];
+      const int64_t first = a.whole * (kWaves * 16);
+      if (splits > 1)
+        *reinterpret_cast<f32x4*>(a.part + ((int64_t)split * (a.nx - first) + x - first) * RP + c) = acc[rt];
       else if (c < a.r) *reinterpret_cast<f32x4*>(static_cast<float*>(a.dP) + x * a.r + c) = acc[rt];
     }
   } else {
@@ -647,15 +667,13 @@ __device__ __forceinline__ float dot8(const float* a, const float* b, float acc)
   return acc;
 }
 
-// The teacher's distribution over a row's places, lane j holding place j: a
-// place is empty (p = 0, id = INT_MAX) when its id lies outside [0, V) or its
-// logit is NaN or -inf. logp is log p where p > 0. Returns whether the row
-// has a place at all.
-__device__ __forceinline__ bool teacher(const int32_t* idx, const float* t, int64_t row, int k, int64_t V, float inv_t,
-                                        int& id, float& p, float& logp) {
-  const int lane = threadIdx.x & 63;
-  id = lane < k ? idx[row * k + lane] : -1;
-  const float x = lane < k ? t[row * k + lane] * inv_t : 0.f;
+// The teacher's distribution over a row's places, lane j holding place j's id
+// (any, outside [0, V) past k) and logit / T: a place is empty (p = 0, id =
+// INT_MAX) when its id lies outside [0, V) or its logit is NaN or -inf. logp
+// is log p where p > 0. Returns whether the row has a place at all. The
+// exponent is taken in two parts: log2(e) rounded to fp32 alone would be off
+// by 1e-8 of it.
+__device__ __forceinline__ bool teacher(int64_t V, int& id, float x, float& p, float& logp) {
   const bool real = id >= 0 && id < V && x > neg_inf();
   const uint32_t mk = wave_max_u32(real ? order_key(x) : 0u);
   if (!real) id = INT_MAX;
@@ -663,10 +681,10 @@ __device__ __forceinline__ bool teacher(const int32_t* idx, const float* t, int6
   logp = 0.f;
   if (!mk) return false;
   const float d = x - __uint_as_float(order_key_inv(mk));
-  const float e = real ? expf(d) : 0.f;
+  const float e = real ? exp2_hw(fmaf(d, kLog2e, d * kLog2eLo)) : 0.f;
   const float s = group_sum<kWave>(e);
   p = e / s;
-  if (p > 0.f) logp = d - logf(s);
+  if (p > 0.f) logp = d - log2_hw(s) * kLn2;
   return true;
 }
 
@@ -688,9 +706,10 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   const int64_t n = blockIdx.x / chunks;
   const int chunk = blockIdx.x % chunks;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
-  int id;
+  int id = lane < k ? idx[n * k + lane] : -1;
   float p, logp;
-  const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);   // every wave: the same values
+  const float tl = lane < k ? t[n * k + lane] * inv_t : 0.f;
+  const bool any = teacher(V, id, tl, p, logp);   // every wave: the same values
   if (wave == 0) {
     sid[lane] = id;
     sp[lane] = p;
@@ -725,7 +744,7 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   __syncthreads();
   l = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
   if (chunk == 0 && wave == 0) {
-    const float ls = (m + log2f(l)) * kLn2;
+    const float ls = (m + log2_hw(l)) * kLn2;
     const float s = lane < k && p > 0.f ? sdot[lane] * inv_t : 0.f;
     const float e = group_sum<kWave>(p > 0.f ? p * (logp - s + ls) : 0.f);
     if (lane == 0) {
@@ -746,11 +765,15 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
       for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], w, o[i]);
     }
     o *= il;
-    for (int j = group; j < k; j += kWaves * 4) {
-      if (sid[j] == INT_MAX) continue;
-      const T* q = P + (int64_t)sid[j] * r + c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(-sp[j], widen<T>(q[i]), o[i]);
+    for (int i0 = 0; i0 < 4; ++i0) {   // k <= 64
+      const int j = group + i0 * (kWaves * 4);
+      const bool real = sid[j] != INT_MAX;
+      const T* q = P + (real ? (int64_t)sid[j] * r + c : 0);
+      T v[4];
+      __builtin_memcpy(v, __builtin_assume_aligned(q, sizeof(v)), sizeof(v));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = real ? fmaf(-sp[j], widen<T>(v[i]), o[i]) : o[i];
     }
   }
   part[group][sub] = o;
@@ -767,36 +790,57 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
 // Per row, before the columns pass: the exponent's offset and the sign of the
 // weight, the row of Z (zeros without weight, so that what a masked row holds,
 // NaN included, cannot reach dP), the places in ascending order of their ids
-// with w p / T, and dZ = w G. One wave per row.
+// with w p / T, and dZ = w G. One wave per row, all its loads up front.
 template <typename T>
 __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     const T* __restrict__ Z, const int32_t* __restrict__ idx, const float* __restrict__ t,
-    const float* __restrict__ lse, const float* __restrict__ G, const float* __restrict__ weight, int64_t N,
-    int64_t V, int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ row_c,
-    int RB, int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
-  const int64_t n = (int64_t)blockIdx.x * kWaves + wave_id();
+    const float* __restrict__ lse, const float* __restrict__ G, const float* __restrict__ weight, int N, int64_t V,
+    int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ row_c, int RB,
+    int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
+  const int n = blockIdx.x * kWaves + wave_id();
   const int lane = threadIdx.x & 63;
+  const int at = lane * 8;   // 8 columns a lane: r <= 512
   if (n >= N) {   // the last tile's rows past N
-    if (zc && n < (N + 63) / 64 * 64 && lane == 0) {
+    if (zc && lane == 0) {
       *row_c_at(row_c, n, RB) = __builtin_inff();
       *row_sign_at(row_c, n, RB) = 0;
     }
     return;
   }
-  int id;
-  float p, logp;
-  const bool any = teacher(idx, t, n, k, V, inv_t, id, p, logp);
+  const int64_t place = (int64_t)n * k + lane, elem = (int64_t)n * r + at;
+  int id = lane < k ? idx[place] : -1;
+  const float tl = lane < k ? t[place] * inv_t : 0.f;
   const float w = weight ? weight[n] : 1.f;
-  const bool live = any && w != 0.f;
+  const float ls = lse[n];
+  f32x4 g[2] = {};
+  if (dZ && at < r) {
+    g[0] = reinterpret_cast<const f32x4*>(G + elem)[0];
+    g[1] = reinterpret_cast<const f32x4*>(G + elem)[1];
+  }
+  T z[8] = {};
+  if (zc && at < r) __builtin_memcpy(z, __builtin_assume_aligned(Z + elem, 16), sizeof(z));
+
+  float p, logp;
+  const bool live = teacher(V, id, tl, p, logp) && w != 0.f;
   const float c = w * inv_t;
-  if (dZ)
-    for (int i = lane; i < r; i += kWave) dZ[n * r + i] = store_cast<T>(live ? w * G[n * r + i] : 0.f);
+  if (dZ && at < r) {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = store_cast<T>(live ? w * g[i >> 2][i & 3] : 0.f);
+    __builtin_memcpy(__builtin_assume_aligned(dZ + elem, 16), v, sizeof(v));
+  }
   if (!zc) return;
+  if (at < RP) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = live ? z[i] : T(0);
+    __builtin_memcpy(__builtin_assume_aligned(zc + (int64_t)n * RP + at, 16), z, sizeof(z));
+  }
   if (lane == 0) {
-    *row_c_at(row_c, n, RB) = live ? lse[n] * kLog2e - log2f(fabsf(c)) : __builtin_inff();
+    // |c| may be subnormal: log2 of 2^64 |c| is not
+    const float lc = log2_hw(fabsf(c) * 0x1p64f) - 64.f;
+    *row_c_at(row_c, n, RB) = live ? ls * kLog2e - lc : __builtin_inff();
     *row_sign_at(row_c, n, RB) = live && c < 0.f ? 0x8000 : 0;
   }
-  for (int i = lane; i < RP; i += kWave) zc[n * RP + i] = live && i < r ? Z[n * r + i] : T(0);
   if (!live) id = INT_MAX;
   int rank = 0;
   for (int j = 0; j < k; ++j) {
@@ -804,111 +848,151 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     rank += o < id || (o == id && j < lane);
   }
   if (lane < k) {
-    srt_id[n * k + rank] = id;
-    srt_w[n * k + rank] = p * c;
+    srt_id[(int64_t)n * k + rank] = id;
+    srt_w[(int64_t)n * k + rank] = p * c;
   }
 }
 
-// table[g][n] = how many of row n's places have an id below g * GC. A block
-// takes 64 rows, their sorted ids in LDS; a wave walks up them, one lane per
-// row, over a range of column groups.
-constexpr int kTableGroups = 32;   // groups per wave
-__global__ void __launch_bounds__(kWaves* kWave) distill_table_kernel(const int* __restrict__ srt_id, int64_t N,
-                                                                      int64_t npad, int k, int GC, int64_t groups,
-                                                                      uint8_t* __restrict__ table) {
+// Byte g % 4 of table[g / 4][n]: how many of row n's places have an id below
+// g * GC (g = 0 .. groups). A block takes 64 rows, their sorted ids in LDS; a
+// wave walks up them, one lane per row, over a range of column groups.
+constexpr int kTableWords = 4;   // words per wave
+__global__ void __launch_bounds__(kWaves* kWave) distill_table_kernel(const int* __restrict__ srt_id, int N, int npad,
+                                                                      int k, int GC, int64_t words, int row_blocks,
+                                                                      uint32_t* __restrict__ table) {
   __shared__ int ids[kWave * (kWave + 1)];
-  const int64_t ranges = (groups + 1 + kTableGroups * kWaves - 1) / (kTableGroups * kWaves);
-  const int64_t n0 = blockIdx.x / ranges * kWave;
-  const int rows = (int)min(N - n0, (int64_t)kWave);
-  for (int i = threadIdx.x; i < rows * k; i += kWaves * kWave) ids[i / k * (kWave + 1) + i % k] = srt_id[n0 * k + i];
+  const int n0 = (int)(blockIdx.x % row_blocks) * kWave;
+  const int rows = min(N - n0, kWave);
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  for (int i = wave; i < rows; i += kWaves)
+    if (lane < k) ids[i * (kWave + 1) + lane] = srt_id[(int64_t)(n0 + i) * k + lane];
   __syncthreads();
-  const int lane = threadIdx.x & 63;
-  const int64_t g0 = (blockIdx.x % ranges * kWaves + wave_id()) * kTableGroups, g1 = min(g0 + kTableGroups, groups + 1);
+  const int64_t w0 = ((int64_t)(blockIdx.x / row_blocks) * kWaves + wave) * kTableWords;
   const int* id = ids + lane * (kWave + 1);
   const int have = lane < rows ? k : 0;
   int j = 0, hi = have;
   while (j < hi) {   // first place at or above the range
     const int mid = (j + hi) >> 1;
-    if (id[mid] < g0 * GC && id[mid] != INT_MAX) j = mid + 1;
+    if (id[mid] < w0 * 4 * GC && id[mid] != INT_MAX) j = mid + 1;
     else hi = mid;
   }
   int next = j < have ? id[j] : INT_MAX;
-  for (int64_t g = g0; g < g1; ++g) {
-    while (next < g * GC && next != INT_MAX) {
-      ++j;
-      next = j < have ? id[j] : INT_MAX;
+  for (int64_t w = w0; w < min(w0 + kTableWords, words); ++w) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      while (next < (w * 4 + b) * GC && next != INT_MAX) {
+        ++j;
+        next = j < have ? id[j] : INT_MAX;
+      }
+      v |= (uint32_t)j << (8 * b);
     }
-    table[g * npad + n0 + lane] = (uint8_t)j;
+    table[w * npad + n0 + lane] = v;
   }
 }
 
-// The places of each group of GC columns, ascending by row. The number of
-// places below a group, summed over the rows, is where its list starts.
-__global__ void __launch_bounds__(256) distill_list_kernel(const uint8_t* __restrict__ table,
-                                                           const int* __restrict__ srt_id,
-                                                           const float* __restrict__ srt_w, int64_t npad, int k,
-                                                           int GC, uint32_t* __restrict__ start,
-                                                           uint2* __restrict__ list) {
-  __shared__ uint32_t red[4], scan[4];
+// A place's weight as the columns pass takes it: fp32, or two bf16 that add
+// up to it.
+__device__ __forceinline__ uint32_t place_weight(float w, bool pairs) {
+  if (!pairs) return __float_as_uint(w);
+  const uint16_t hi = f32_to_bf16(w);
+  return hi | (uint32_t)f32_to_bf16(w - bf16_to_f32(hi)) << 16;
+}
+
+// The places of each group of GC columns, ascending by row: a block per group,
+// 8 rows a thread. The number of places below a group, summed over the rows,
+// is where its list starts.
+constexpr int kListWaves = 8, kListRows = kListWaves * kWave * 8;
+__global__ void __launch_bounds__(kListWaves* kWave) distill_list_kernel(
+    const uint32_t* __restrict__ table, const int* __restrict__ srt_id, const float* __restrict__ srt_w, int npad,
+    int k, int GC, bool pairs, uint32_t* __restrict__ start, uint2* __restrict__ list) {
+  __shared__ uint32_t below[kListWaves], scan[kListWaves];
   const int64_t g = blockIdx.x;
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  const uint8_t* lo = table + g * npad;
-  const uint8_t* hi = lo + npad;
-  uint32_t below = 0;
-  for (int64_t n = threadIdx.x * 16; n < npad; n += 256 * 16) {
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lo_bit = (int)(g & 3) * 8, hi_bit = (int)((g + 1) & 3) * 8;
+  const uint32_t* lo = table + (g >> 2) * npad;
+  const uint32_t* hi = table + ((g + 1) >> 2) * npad;
+  uint32_t at = 0;
+  for (int n = threadIdx.x * 4; n < npad; n += kListWaves * kWave * 4) {
     const u32x4 v = load16(lo + n);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) below += (v[q] & 255) + ((v[q] >> 8) & 255) + ((v[q] >> 16) & 255) + (v[q] >> 24);
+    for (int q = 0; q < 4; ++q) at += (v[q] >> lo_bit) & 255;
   }
-  for (int o = 32; o; o >>= 1) below += __shfl_xor(below, o);
-  if (lane == 0) red[wave] = below;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) at += (uint32_t)__shfl_xor((int)at, o);
+  if (lane == 0) below[wave] = at;
   __syncthreads();
-  uint32_t at = (red[0] + red[1]) + (red[2] + red[3]);
+  at = 0;
+#pragma unroll
+  for (int w = 0; w < kListWaves; ++w) at += below[w];
   if (threadIdx.x == 0) start[g] = at;
-  for (int64_t n0 = 0; n0 < npad; n0 += 256 * 16) {
-    const int64_t n = n0 + threadIdx.x * 16;
-    u32x4 a = {0u, 0u, 0u, 0u}, b = a;
-    if (n < npad) {
-      a = load16(lo + n);
-      b = load16(hi + n);
-    }
+  for (int n0 = 0; n0 < npad; n0 += kListRows) {
+    const int n = n0 + threadIdx.x * 8;
+    uint32_t first[8], last[8];   // the rows' places in this group
     uint32_t mine = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 8; q += 4) {
+      u32x4 a = {0u, 0u, 0u, 0u}, b = a;
+      if (n < npad) {
+        a = load16(lo + n + q);
+        b = load16(hi + n + q);
+      }
 #pragma unroll
-      for (int s = 0; s < 32; s += 8) mine += ((b[q] >> s) & 255) - ((a[q] >> s) & 255);
+      for (int i = 0; i < 4; ++i) {
+        first[q + i] = (a[i] >> lo_bit) & 255;
+        last[q + i] = (b[i] >> hi_bit) & 255;
+        mine += last[q + i] - first[q + i];
+      }
+    }
     const uint32_t incl = wave_incl_scan_u32(mine);
     __syncthreads();
     if (lane == 63) scan[wave] = incl;
     __syncthreads();
     uint32_t o = at + incl - mine;
-    for (int w = 0; w < wave; ++w) o += scan[w];
-    at += (scan[0] + scan[1]) + (scan[2] + scan[3]);
+#pragma unroll
+    for (int w = 0; w < kListWaves; ++w) {
+      o += w < wave ? scan[w] : 0u;
+      at += scan[w];
+    }
     if (!mine) continue;
+    // most rows have one place here or none: its loads for all 8 rows at once
+    int id[8];
+    float wt[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 8; ++q) {
+      const int64_t i = first[q] < last[q] ? (int64_t)(n + q) * k + first[q] : 0;
+      id[q] = srt_id[i];
+      wt[q] = srt_w[i];
+    }
 #pragma unroll
-      for (int s = 0; s < 32; s += 8) {
-        const int64_t row = n + q * 4 + s / 8;
-        for (uint32_t j = (a[q] >> s) & 255; j < ((b[q] >> s) & 255); ++j)
-          list[o++] = uint2{(uint32_t)row | (uint32_t)(srt_id[row * k + j] - g * GC) << kRowBits,
-                            __float_as_uint(srt_w[row * k + j])};
+    for (int q = 0; q < 8; ++q) {
+      if (first[q] < last[q])
+        list[o++] = uint2{(uint32_t)(n + q) | (uint32_t)(id[q] - g * GC) << kRowBits, place_weight(-wt[q], pairs)};
+      for (uint32_t j = first[q] + 1; j < last[q]; ++j) {
+        const int64_t i = (int64_t)(n + q) * k + j;
+        list[o++] = uint2{(uint32_t)(n + q) | (uint32_t)(srt_id[i] - g * GC) << kRowBits,
+                          place_weight(-srt_w[i], pairs)};
       }
+    }
   }
   if (g == (int64_t)gridDim.x - 1 && threadIdx.x == 0) start[g + 1] = at;
 }
 
-// dP = the sum of the columns pass's shares, in their order.
+// dP of the rows that the columns pass split: the sum of the shares, in their
+// order. rows, dP: from the first such row.
 template <typename T>
-__global__ void __launch_bounds__(256) distill_join_kernel(const float* __restrict__ part, int splits, int64_t V,
+__global__ void __launch_bounds__(256) distill_join_kernel(const float* __restrict__ part, int splits, int rows,
                                                            int r, int RP, T* __restrict__ dP) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= V * r) return;
-  const int64_t v = i / r;
-  const int c = (int)(i % r);
-  float s = 0.f;
-  for (int p = 0; p < splits; ++p) s += part[((int64_t)p * V + v) * RP + c];
-  dP[i] = store_cast<T>(s);
+  const uint32_t i = (blockIdx.x * 256 + threadIdx.x) * 4;   // r is a multiple of 8
+  const uint32_t v = i / (uint32_t)RP, c = i % (uint32_t)RP;
+  if (v >= (uint32_t)rows || c >= (uint32_t)r) return;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < splits; ++p) s += *reinterpret_cast<const f32x4*>(part + ((int64_t)p * rows + v) * RP + c);
+  T o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = store_cast<T>(s[e]);
+  __builtin_memcpy(__builtin_assume_aligned(dP + (int64_t)v * r + c, sizeof(o)), o, sizeof(o));
 }
 
 __global__ void __launch_bounds__(256) distill_zero_kernel(uint32_t* __restrict__ p, int64_t words) {
@@ -928,10 +1012,11 @@ struct Plan {
   int XT, WX;        // rows pass
   int row_splits;    // blocks along Y
   int shares;        // shares per row of Z
-  int cXT;           // columns pass: 32-column tiles per wave
-  int GC;            // columns of a group (a wave)
+  int GC;            // columns pass: columns of a group (bf16: a block, fp32: a wave)
   int64_t groups;
-  int col_splits;
+  int64_t col_whole; // blocks of the columns pass over all rows
+  int col_splits;    // shares of the rows for the others
+  int64_t split_rows;   // their rows of P
   int RB;            // rows of a tile of the columns pass
   int64_t npad;
   // workspace offsets
@@ -949,8 +1034,7 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
     p.WX = N <= 32 * p.XT && p.RP < 512 ? 1 : N <= 64 * p.XT ? 2 : 4;
     xblocks = ceil_div(N, p.WX * 32 * p.XT);
     ytiles = ceil_div(V, std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX)));
-    p.cXT = p.XT;
-    p.GC = 32 * p.cXT;
+    p.GC = kWaves * 32 * p.XT;
   } else {
     p.XT = 1;
     p.WX = 4;
@@ -958,14 +1042,22 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
     ytiles = ceil_div(V, 16);
     p.GC = 16;
   }
+  p.RB = dtype == 0 && p.RP > 128 ? 32 : 64;
   const int wy = kWaves / p.WX;
   p.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>({kTargetBlocks / xblocks, ytiles, kMaxShares / wy}));
   p.shares = p.row_splits * wy;
   p.groups = ceil_div(V, p.GC);
-  cblocks = ceil_div(p.groups, kWaves);
-  const int64_t ntiles = ceil_div(N, dtype == 0 ? (p.RP <= 128 ? 64 : 32) : 16);
-  p.col_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTargetBlocks / cblocks, ntiles));
-  p.RB = dtype == 0 && p.RP > 128 ? 32 : 64;
+  cblocks = dtype == 0 ? p.groups : ceil_div(p.groups, kWaves);
+  // The blocks of P's rows that do not fill the GPU once more share out the
+  // rows of Z between them, down to about two tiles a share. (At 4096 rows,
+  // r = 128, 1187 blocks of which 512 run at a time: 333 us with the last 163
+  // in three shares and 7 for joining them, 345 without.)
+  const int64_t ntiles = ceil_div(N, p.RB), slots = p.RP == 512 ? kTargetBlocks / 2 : kTargetBlocks;
+  p.col_whole = cblocks / slots * slots;
+  const int64_t rest = cblocks - p.col_whole;
+  p.col_splits = rest ? (int)std::max<int64_t>(1, std::min<int64_t>(slots / rest, ntiles / 2)) : 1;
+  if (p.col_splits == 1) p.col_whole = cblocks;
+  p.split_rows = V - std::min(V, p.col_whole * (dtype == 0 ? p.GC : 64));
   p.npad = ceil_div(N, 64) * 64;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
@@ -982,17 +1074,17 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   p.row_c = take(size_t(p.npad) * 8);
   p.srt_id = take(size_t(N) * k * 4);
   p.srt_w = take(size_t(N) * k * 4);
-  p.table = take(size_t(p.groups + 1) * p.npad);
+  p.table = take(size_t(p.groups / 4 + 1) * p.npad * 4);
   p.start = take(size_t(p.groups + 1) * 4);
   p.list = take(size_t(N) * k * 8);
-  p.part = take(p.col_splits > 1 ? size_t(p.col_splits) * V * p.RP * 4 : 0);
+  p.part = take(p.col_splits > 1 ? size_t(p.col_splits) * p.split_rows * p.RP * 4 : 0);
   p.bwd_total = o;
   return p;
 }
 
 template <int RP, int XT, int WX, bool ACC, bool COLS>
 hipError_t go_bf16(const StreamArgs& a, hipStream_t s) {
-  const int64_t xb = ceil_div(a.nx, WX * 32 * XT);
+  const int64_t blocks = a.whole + (ceil_div(a.nx, WX * 32 * XT) - a.whole) * a.splits;
   const auto kernel = stream_bf16_kernel<RP, XT, WX, ACC, COLS>;
   constexpr int bytes = bf16_lds_bytes<RP, WX>();
   if constexpr (bytes > 65536) {
@@ -1000,7 +1092,7 @@ hipError_t go_bf16(const StreamArgs& a, hipStream_t s) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(xb * a.splits)), dim3(kWaves * kWave), bytes, s, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kWaves * kWave), bytes, s, a);
   return hipGetLastError();
 }
 
@@ -1034,7 +1126,7 @@ hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) 
       }
     }
   }
-  const dim3 grid((unsigned)(ceil_div(a.nx, 64) * a.splits)), block(kWaves * kWave);
+  const dim3 grid((unsigned)(a.whole + (ceil_div(a.nx, 64) - a.whole) * a.splits)), block(kWaves * kWave);
   switch (p.RP) {
     case 32: hipLaunchKernelGGL((stream_f32_kernel<32, ACC, COLS>), grid, block, 0, s, a); break;
     case 64: hipLaunchKernelGGL((stream_f32_kernel<64, ACC, COLS>), grid, block, 0, s, a); break;
@@ -1056,7 +1148,7 @@ void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
 template <typename T>
 void prep(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
   hipLaunchKernelGGL(distill_prep_kernel<T>, dim3((unsigned)(p.npad / kWaves)), dim3(kWaves * kWave), 0, s,
-                     static_cast<const T*>(d.Z), d.idx, d.t, d.lse, d.G, d.weight, d.N, d.V, d.r, p.RP, d.k, d.inv_t,
+                     static_cast<const T*>(d.Z), d.idx, d.t, d.lse, d.G, d.weight, (int)d.N, d.V, d.r, p.RP, d.k, d.inv_t,
                      d.dP ? reinterpret_cast<T*>(ws + p.zc) : nullptr, reinterpret_cast<float*>(ws + p.row_c),
                      p.RB, reinterpret_cast<int*>(ws + p.srt_id),
                      reinterpret_cast<float*>(ws + p.srt_w), static_cast<T*>(d.dZ));
@@ -1107,14 +1199,15 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   if (e != hipSuccess || !d.dP) return e;
   const int* srt_id = reinterpret_cast<int*>(ws + p.srt_id);
   const float* srt_w = reinterpret_cast<float*>(ws + p.srt_w);
-  uint8_t* table = reinterpret_cast<uint8_t*>(ws + p.table);
+  uint32_t* table = reinterpret_cast<uint32_t*>(ws + p.table);
   uint32_t* start = reinterpret_cast<uint32_t*>(ws + p.start);
   uint2* list = reinterpret_cast<uint2*>(ws + p.list);
-  hipLaunchKernelGGL(distill_table_kernel,
-                     dim3((unsigned)(p.npad / kWave * ceil_div(p.groups + 1, kTableGroups * kWaves))),
-                     dim3(kWaves * kWave), 0, s, srt_id, d.N, p.npad, d.k, p.GC, p.groups, table);
-  hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(256), 0, s, table, srt_id, srt_w, p.npad,
-                     d.k, p.GC, start, list);
+  const int row_blocks = (int)(p.npad / kWave);
+  const int64_t words = p.groups / 4 + 1;
+  hipLaunchKernelGGL(distill_table_kernel, dim3((unsigned)(row_blocks * ceil_div(words, kTableWords * kWaves))),
+                     dim3(kWaves * kWave), 0, s, srt_id, (int)d.N, (int)p.npad, d.k, p.GC, words, row_blocks, table);
+  hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(kListWaves * kWave), 0, s, table, srt_id,
+                     srt_w, (int)p.npad, d.k, p.GC, d.dtype == 0, start, list);
   StreamArgs a{};
   a.X = d.P;
   a.nx = d.V;
@@ -1123,6 +1216,7 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   a.r = d.r;
   a.ldy = p.RP;
   a.scale = d.scale;
+  a.whole = p.col_whole;
   a.splits = p.col_splits;
   a.row_c = reinterpret_cast<float*>(ws + p.row_c);
   a.list_start = start;
@@ -1131,14 +1225,15 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   a.part = reinterpret_cast<float*>(ws + p.part);
   e = stream<true, true>(d.dtype, p, a, s);
   if (e != hipSuccess) return e;
-  if (p.col_splits > 1) {
-    const dim3 grid((unsigned)ceil_div(d.V * d.r, 256));
+  if (p.col_splits > 1) {   // at most 512 blocks of rows: the index fits 32 bits
+    const dim3 grid((unsigned)ceil_div(p.split_rows * p.RP, 1024));
+    const int64_t first = (d.V - p.split_rows) * d.r;
     if (d.dtype == 0)
-      hipLaunchKernelGGL(distill_join_kernel<uint16_t>, grid, dim3(256), 0, s, a.part, p.col_splits, d.V, d.r, p.RP,
-                         static_cast<uint16_t*>(d.dP));
+      hipLaunchKernelGGL(distill_join_kernel<uint16_t>, grid, dim3(256), 0, s, a.part, p.col_splits,
+                         (int)p.split_rows, d.r, p.RP, static_cast<uint16_t*>(d.dP) + first);
     else
-      hipLaunchKernelGGL(distill_join_kernel<float>, grid, dim3(256), 0, s, a.part, p.col_splits, d.V, d.r, p.RP,
-                         static_cast<float*>(d.dP));
+      hipLaunchKernelGGL(distill_join_kernel<float>, grid, dim3(256), 0, s, a.part, p.col_splits,
+                         (int)p.split_rows, d.r, p.RP, static_cast<float*>(d.dP) + first);
   }
   return hipGetLastError();
 }
