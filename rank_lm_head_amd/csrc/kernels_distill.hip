@@ -82,6 +82,7 @@ struct StreamArgs {
   // [tile] of the rows of Z: RB times c (+inf for rows without weight), RB
   // times the weight's sign as bit 15 of 16 bits, padding to 2 RB words
   const float* row_c;
+  int row_block;        // RB
   const uint32_t* list_start;   // [groups + 1]: the teacher places of a group of columns in `list`
   const uint2* list;    // (row | local column << kRowBits, -w p / T), by row within a group
   void* dP;             // V x r, from whole blocks
@@ -116,16 +117,59 @@ constexpr int bf16_tile_rows() {
   const int rows = 32 * (kWaves / WX);
   return rows < (RP <= 128 ? 64 : 32) ? (RP <= 128 ? 64 : 32) : rows;
 }
-// LDS of a block: two tiles and, for the columns pass, two sets of row values.
+// LDS of a block: two tiles and, for the columns pass, two sets of row values;
+// results leave through it, 32 rows of at least 32 columns a wave.
 template <int RP, int WX>
-constexpr int bf16_lds_bytes() { return 2 * bf16_tile_rows<RP, WX>() * (RP * 2 + 8); }
+constexpr int bf16_lds_bytes() {
+  const int tiles = 2 * bf16_tile_rows<RP, WX>() * (RP * 2 + 8), out = kWaves * 32 * 32 * 4;
+  return tiles < out ? out : tiles;
+}
 
-// Streams rows [tile * TY, ...) of Y into an LDS tile, zeros past the matrix
+// Stores a wave's 32 rows of results, RP columns of which `cols` exist, to
+// rows ld elements apart, `rows` of which exist. In the accumulators a lane
+// holds one row; it goes through the wave's part of the LDS (chunks of 16
+// bytes swizzled by the row), CH columns at a time, so that whole lines leave.
+template <int RP, int CH, typename T>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[RP / 32], uint16_t* scratch, T* dst, int64_t ld, int rows,
+                                           int cols) {
+  constexpr int kPer = 16 / (int)sizeof(T), kChunks = CH / kPer, kMask = kChunks < 16 ? kChunks - 1 : 15;
+  const int lane = threadIdx.x & 63, h = lane >> 5, x = lane & 31;
+  T* mem = reinterpret_cast<T*>(scratch);
+#pragma unroll
+  for (int c0 = 0; c0 < RP; c0 += CH) {
+#pragma unroll
+    for (int rt = 0; rt < CH / 32; ++rt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x16& a = acc[c0 / 32 + rt];
+        const f32x4 v = {a[g * 4], a[g * 4 + 1], a[g * 4 + 2], a[g * 4 + 3]};
+        const int c = rt * 32 + g * 8 + h * 4;
+        T* at = mem + x * CH + (((c / kPer) ^ (x & kMask)) * kPer + c % kPer);
+        if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(at) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        else *reinterpret_cast<f32x4*>(at) = v;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int i = 0; i < 32 * kChunks / kWave; ++i) {
+      const int p = i * kWave + lane, row = p / kChunks, c = p % kChunks;
+      const u32x4 v = load16(mem + row * CH + (c ^ (row & kMask)) * kPer);
+      if (row < rows && c0 + c * kPer < cols) *reinterpret_cast<u32x4*>(dst + row * ld + c0 + c * kPer) = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// Copies rows [row0, row0 + TY) of a matrix into an LDS tile, zeros past its end
 // and past r columns.
 template <int RP, int TY>
 struct TileCopy {
   static constexpr int kChunks = RP / 8;
-  static constexpr int kLoads = TY * kChunks / (kWaves * kWave);
+  static constexpr int kLoads = (TY * kChunks + kWaves * kWave - 1) / (kWaves * kWave);
+  static constexpr bool kPart = TY * kChunks < kWaves * kWave;   // the first waves only
   uint32_t off[kLoads];
   const char* base;
   int64_t rows;
@@ -143,16 +187,16 @@ struct TileCopy {
       off[i] = c * 8 < r ? (uint32_t)row * row_bytes + (uint32_t)c * 16u : 0x7ffffff0u;
     }
   }
-  __device__ __forceinline__ void issue(uint16_t* tile, int64_t t) const {
+  __device__ __forceinline__ void issue(uint16_t* tile, int64_t row0) const {
     const int wave = wave_id();
-    const int64_t row0 = t * TY;
-    const uint32_t bytes = (uint32_t)min(rows - row0, (int64_t)TY) * row_bytes;
+    const uint32_t bytes = (uint32_t)max(min(rows - row0, (int64_t)TY), (int64_t)0) * row_bytes;
     const uint64_t addr = reinterpret_cast<uint64_t>(base) + (uint64_t)row0 * row_bytes;
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)addr);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(addr >> 32));
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), (short)0,
                                           __builtin_amdgcn_readfirstlane((int)bytes), kRawBufferFlags);
+    if (kPart && wave >= TY * kChunks / kWave) return;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(tile + (i * kWaves + wave) * kWave * 8), 16,
@@ -258,7 +302,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   TileCopy<RP, TY> copy;
   copy.init(a.Y, a.ny, a.r, a.ldy);
   const auto stage = [&](int buf, int64_t t) {
-    copy.issue(lds + buf * TY * RP, t);
+    copy.issue(lds + buf * TY * RP, t * TY);
     if constexpr (COLS) {   // the rows' offsets and signs, kept tile by tile
       if (wave < TY / 32)
         __builtin_amdgcn_global_load_lds(
@@ -329,17 +373,29 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
       __syncthreads();   // the tiles may be filled again
     }
   }
+  // X, whole lines at a time, through the tiles' LDS.
   bf16x8 X[XT][KS];
+  {
+    constexpr int kRows = WX * 32 * XT, kUnits = (kRows + TY - 1) / TY;
+    TileCopy<RP, TY> cx;
+    cx.init(a.X, a.nx, a.r, a.r);
 #pragma unroll
-  for (int xt = 0; xt < XT; ++xt) {
-    const int64_t x = x0 + xt * 32 + (lane & 31);
-    const uint16_t* row = static_cast<const uint16_t*>(a.X) + min(x, a.nx - 1) * a.r;
+    for (int u = 0; u < kUnits; u += 2) {
+      cx.issue(lds, xtile * kRows + u * TY);
+      if (u + 1 < kUnits) cx.issue(lds + TY * RP, xtile * kRows + (u + 1) * TY);
+      __builtin_amdgcn_s_waitcnt(0xF70);
+      __syncthreads();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int c = ks * 16 + h * 8;
-      const bool ok = x < a.nx && c < a.r;
-      const u32x4 v = load16(row + (ok ? c : 0));
-      X[xt][ks] = __builtin_bit_cast(bf16x8, ok ? v : u32x4{0u, 0u, 0u, 0u});
+      for (int xt = 0; xt < XT; ++xt) {
+        const int row = (wx * XT + xt) * 32 - u * TY;   // the wave's tile within the two
+        if (kUnits <= 2 || (row >= 0 && row < 2 * TY)) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            X[xt][ks] = __builtin_bit_cast(
+                bf16x8, load16(lds + row * RP + at.row[ks % at.kRow] + ks / at.kRow * 128));
+        }
+      }
+      __syncthreads();
     }
   }
 
@@ -482,46 +538,205 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
       mask(S, left);
       largest(S);
     });
+    if constexpr (WY > 1) {   // the waves of a row keep one reference
+      float* top = reinterpret_cast<float*>(lds);   // [wy][row of the block]
+#pragma unroll
+      for (int xt = 0; xt < XT; ++xt) {
+        const int x = (wx * XT + xt) * 32 + (lane & 31);
+        top[wy * (WX * 32 * XT) + x] = m[xt];   // (both halves of the wave hold it)
+      }
+      __syncthreads();
+#pragma unroll
+      for (int xt = 0; xt < XT; ++xt) {
+        const int x = (wx * XT + xt) * 32 + (lane & 31);
+#pragma unroll
+        for (int y = 0; y < WY; ++y) m[xt] = fmaxf(m[xt], top[y * (WX * 32 * XT) + x]);
+      }
+      __syncthreads();
+    }
   }
 
+  uint16_t* const scratch = lds + wave * (bf16_lds_bytes<RP, WX>() / 2 / kWaves / 16 * 16);
+  constexpr int kFit = bf16_lds_bytes<RP, WX>() / kWaves / 32;   // bytes of a row that fit the scratch
+  constexpr int kOut2 = kFit >= RP * 2 ? RP : kFit >= RP ? RP / 2 : RP / 4;
+  constexpr int kOut4 = kFit >= RP * 4 ? RP : kFit >= RP * 2 ? RP / 2 : RP / 4;
   if constexpr (COLS) {
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
-      const int64_t x = x0 + xt * 32 + (lane & 31);
-      if (x >= a.nx) continue;
-      if (splits > 1) {
-        const int64_t first = a.whole * (WX * 32 * XT);
-        float* row = a.part + ((int64_t)split * (a.nx - first) + x - first) * RP + h * 4;
-#pragma unroll
-        for (int i = 0; i < RT * 4; ++i) *reinterpret_cast<f32x4*>(row + i * 8) = quad(acc[xt][i >> 2], i & 3);
-      } else {
-        uint16_t* row = static_cast<uint16_t*>(a.dP) + x * a.r + h * 4;
-        const int have = (a.r - h * 4 + 7) / 8;   // quads of this lane that exist: r is a multiple of 8
-#pragma unroll
-        for (int i = 0; i < RT * 4; ++i) {
-          const f32x4 v = quad(acc[xt][i >> 2], i & 3);
-          const uint2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          if (i < have) *reinterpret_cast<uint2*>(row + i * 8) = b;
-        }
-      }
+      const int64_t x = x0 + xt * 32;
+      const int have = (int)min(a.nx - x, (int64_t)32);
+      const int64_t first = a.whole * (WX * 32 * XT);
+      if (splits > 1)
+        store_rows<RP, kOut4>(acc[xt], scratch, a.part + ((int64_t)split * (a.nx - first) + x - first) * RP, RP, have, RP);
+      else
+        store_rows<RP, kOut2>(acc[xt], scratch, static_cast<uint16_t*>(a.dP) + x * a.r, a.r, have, a.r);
     }
   } else {
-    const int64_t share = (int64_t)split * WY + wy;
+    if constexpr (WY > 1) {
+      // The first wave of each row adds the others' sums to its own, in their
+      // order, 16 registers at a time.
+      float* sums = reinterpret_cast<float*>(lds);                    // [wy - 1][row]
+      f32x4* parts = reinterpret_cast<f32x4*>(sums + (WY - 1) * WX * 32 * XT);   // [wy - 1][wx][quad][lane]
+#pragma unroll
+      for (int xt = 0; xt < XT; ++xt) {
+        l[xt] += __shfl_xor(l[xt], 32);
+        const int x = (wx * XT + xt) * 32 + (lane & 31);
+        if (wy) sums[(wy - 1) * (WX * 32 * XT) + x] = l[xt];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int xt = 0; xt < XT; ++xt) {
+        const int x = (wx * XT + xt) * 32 + (lane & 31);
+        if (!wy)
+#pragma unroll
+          for (int y = 0; y < WY - 1; ++y) l[xt] += sums[y * (WX * 32 * XT) + x];
+#pragma unroll
+        for (int rt = 0; rt < (ACC ? RT : 0); ++rt) {
+          if (wy)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) parts[(((wy - 1) * WX + wx) * 4 + g) * kWave + lane] = quad(acc[xt][rt], g);
+          __syncthreads();
+          if (!wy)
+#pragma unroll
+            for (int y = 0; y < WY - 1; ++y)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const f32x4 v = parts[((y * WX + wx) * 4 + g) * kWave + lane];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[xt][rt][g * 4 + i] += v[i];
+              }
+          __syncthreads();
+        }
+      }
+      if (wy) return;
+    }
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
-      const int64_t x = x0 + xt * 32 + (lane & 31);
-      const float lt = l[xt] + __shfl_xor(l[xt], 32);
-      if (x >= a.nx) continue;
-      if (h == 0) {
-        a.pm[share * a.nx + x] = m[xt];
-        a.pl[share * a.nx + x] = lt;
+      const int64_t x = x0 + xt * 32;
+      const float lt = WY > 1 ? l[xt] : l[xt] + __shfl_xor(l[xt], 32);
+      if (lane < 32 && x + lane < a.nx) {
+        a.pm[(int64_t)split * a.nx + x + lane] = m[xt];
+        a.pl[(int64_t)split * a.nx + x + lane] = lt;
       }
-      if constexpr (ACC) {
-        float* row = a.po + (share * a.nx + x) * RP + h * 4;
-#pragma unroll
-        for (int i = 0; i < RT * 4; ++i) *reinterpret_cast<f32x4*>(row + i * 8) = quad(acc[xt][i >> 2], i & 3);
-      }
+      if constexpr (ACC)
+        store_rows<RP, kOut4>(acc[xt], scratch, a.po + ((int64_t)split * a.nx + x) * RP, RP,
+                              (int)min(a.nx - x, (int64_t)32), RP);
     }
+  }
+}
+
+// The columns pass for few rows (NS tiles of 32 at most), bf16: bound by the
+// reading of P and the writing of dP, so it is laid out for many waves in
+// flight rather than for reuse. All rows of Z sit in LDS and all weights of a
+// wave's 32 columns in registers; dP then takes shape 32 columns of r at a
+// time, which leaves room for a second block (r = 512: one block and 256
+// accumulators in the general kernel; 64 rows, 151936 tokens: PLACEHOLDER).
+constexpr int kNear = 512;
+template <int RP, int NS>
+__global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArgs a) {
+  constexpr int TY = NS * 32, KS = RP / 16, RT = RP / 32;
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  const int lane = threadIdx.x & 63, h = lane >> 5, wave = wave_id();
+  uint16_t* const scratch = lds + TY * RP + wave * (32 * 32);
+  uint2* const near = reinterpret_cast<uint2*>(lds + TY * RP + kWaves * (32 * 32));   // the first places
+  const int64_t x0 = ((int64_t)blockIdx.x * kWaves + wave) * 32;
+  const uint32_t e0 = a.list_start[blockIdx.x], e1 = a.list_start[blockIdx.x + 1];
+
+  TileCopy<RP, TY> copy;
+  copy.init(a.Y, a.ny, RP, RP);
+  copy.issue(lds, 0);
+  bf16x8 X[KS];
+  {
+    const int64_t x = x0 + (lane & 31);
+    const uint16_t* row = static_cast<const uint16_t*>(a.X) + min(x, a.nx - 1) * a.r;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = ks * 16 + h * 8;
+      const bool ok = x < a.nx && c < a.r;
+      const u32x4 v = load16(row + (ok ? c : 0));
+      X[ks] = __builtin_bit_cast(bf16x8, ok ? v : u32x4{0u, 0u, 0u, 0u});
+    }
+  }
+  // The first places, zeros behind the last. 16 places make a step: their rows
+  // for the left operand (by k slot and by the lane's part in a transposing
+  // read), their weights for the right one.
+  for (uint32_t i = threadIdx.x; i < kNear; i += kWaves * kWave) {
+    near[i] = i < e1 - e0 ? a.list[e0 + i] : uint2{0u, 0u};
+    if (i >= e1 - e0 + 16) break;
+  }
+  const int ya = h * 4 + ((lane & 15) >> 2);
+  int na, nb;
+  bf16x8 hi, lo;
+  const auto take = [&](auto&& entry) __attribute__((always_inline)) {
+    na = (int)(entry(ya).x & kRowMask);
+    nb = (int)(entry(ya + 8).x & kRowMask);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint2 en = entry((k >> 2) * 8 + h * 4 + (k & 3));
+      const uint32_t w = (int)(en.x >> kRowBits) == wave * 32 + (lane & 31) ? en.y : 0u;
+      hi[k] = __builtin_bit_cast(__bf16, (uint16_t)w);
+      lo[k] = __builtin_bit_cast(__bf16, (uint16_t)(w >> 16));
+    }
+  };
+  const auto places = [&](uint32_t i) {   // from place e0 + i on
+    if (i < kNear) take([&](int y) { return near[i + y]; });
+    else take([&](int y) { return i + y < e1 - e0 ? a.list[e0 + i + y] : uint2{0u, 0u}; });
+  };
+  Places<RP> at;
+  at.init();
+  __builtin_amdgcn_s_waitcnt(0xF70);
+  __syncthreads();
+  places(0);
+
+  bf16x8 E[NS][2];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    f32x16 S[1];
+    const bf16x8(&X1)[1][KS] = reinterpret_cast<const bf16x8(&)[1][KS]>(X);
+    scores<RP, 1>(lds + s * 32 * RP, at, X1, S);
+    float e[16];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t n = s * 32 + g * 8 + h * 4 + i;   // row_c is padded to 64 rows
+        float* rc = const_cast<float*>(a.row_c);
+        const float v = exp2_hw(fmaf(S[0][g * 4 + i], a.scale, -*row_c_at(rc, n, a.row_block)));
+        e[g * 4 + i] = *row_sign_at(rc, n, a.row_block) ? -v : v;
+      }
+#pragma unroll
+    for (int s2 = 0; s2 < 2; ++s2) {
+      u32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = pack_bf16(e[s2 * 8 + i * 2], e[s2 * 8 + i * 2 + 1]);
+      E[s][s2] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+  const int have = (int)min(a.nx - x0, (int64_t)32);
+  uint16_t* out = static_cast<uint16_t*>(a.dP) + x0 * a.r;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    if (rt * 32 >= a.r) break;
+    f32x16 acc[1] = {};
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int s2 = 0; s2 < 2; ++s2)
+        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns<RP>(lds + (s * 32 + s2 * 16) * RP, at, rt), E[s][s2],
+                                                         acc[0], 0, 0, 0);
+    for (uint32_t i = 0; i < e1 - e0; i += 16) {
+      if (e1 - e0 > 16) places(i);   // more than one step: made again for each 32 columns
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const int c = rt * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), half = (lane & 1) * 4;
+      const s16x4 va = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4_t)(lds + na * RP + (c ^ swz_row<RP>(na)) * 8 + half));
+      const s16x4 vb = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4_t)(lds + nb * RP + (c ^ swz_row<RP>(nb)) * 8 + half));
+      const bf16x8 A = __builtin_bit_cast(bf16x8, s16x8{va[0], va[1], va[2], va[3], vb[0], vb[1], vb[2], vb[3]});
+      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi, acc[0], 0, 0, 0);
+      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo, acc[0], 0, 0, 0);
+    }
+    store_rows<32, 32>(acc, scratch, out + rt * 32, a.r, have, a.r - rt * 32);
   }
 }
 
@@ -864,8 +1079,14 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_table_kernel(const int*
   const int n0 = (int)(blockIdx.x % row_blocks) * kWave;
   const int rows = min(N - n0, kWave);
   const int lane = threadIdx.x & 63, wave = wave_id();
-  for (int i = wave; i < rows; i += kWaves)
-    if (lane < k) ids[i * (kWave + 1) + lane] = srt_id[(int64_t)(n0 + i) * k + lane];
+  int v[kWave / kWaves];
+#pragma unroll
+  for (int i = 0; i < kWave / kWaves; ++i) {
+    const int row = i * kWaves + wave;
+    v[i] = row < rows && lane < k ? srt_id[(int64_t)(n0 + row) * k + lane] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kWave / kWaves; ++i) ids[(i * kWaves + wave) * (kWave + 1) + lane] = v[i];
   __syncthreads();
   const int64_t w0 = ((int64_t)(blockIdx.x / row_blocks) * kWaves + wave) * kTableWords;
   const int* id = ids + lane * (kWave + 1);
@@ -1009,9 +1230,9 @@ constexpr int kTargetBlocks = 512;   // two blocks per compute unit
 
 struct Plan {
   int RP;
+  bool few;          // the columns pass for few rows
   int XT, WX;        // rows pass
   int row_splits;    // blocks along Y
-  int shares;        // shares per row of Z
   int GC;            // columns pass: columns of a group (bf16: a block, fp32: a wave)
   int64_t groups;
   int64_t col_whole; // blocks of the columns pass over all rows
@@ -1031,10 +1252,11 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   int64_t xblocks, ytiles, cblocks;
   if (dtype == 0) {
     p.XT = x_tiles(p.RP);
-    p.WX = N <= 32 * p.XT && p.RP < 512 ? 1 : N <= 64 * p.XT ? 2 : 4;
+    p.WX = N <= 32 * p.XT && p.RP < 256 ? 1 : N <= 64 * p.XT ? 2 : 4;
     xblocks = ceil_div(N, p.WX * 32 * p.XT);
     ytiles = ceil_div(V, std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX)));
-    p.GC = kWaves * 32 * p.XT;
+    p.few = N <= 64;
+    p.GC = kWaves * 32 * (p.few ? 1 : p.XT);
   } else {
     p.XT = 1;
     p.WX = 4;
@@ -1043,19 +1265,19 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
     p.GC = 16;
   }
   p.RB = dtype == 0 && p.RP > 128 ? 32 : 64;
-  const int wy = kWaves / p.WX;
-  p.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>({kTargetBlocks / xblocks, ytiles, kMaxShares / wy}));
-  p.shares = p.row_splits * wy;
+  const int64_t slots = p.RP == 512 && dtype == 0 ? kTargetBlocks / 2 : kTargetBlocks;   // blocks at a time
+  p.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / xblocks, ytiles, kMaxShares}));
   p.groups = ceil_div(V, p.GC);
   cblocks = dtype == 0 ? p.groups : ceil_div(p.groups, kWaves);
   // The blocks of P's rows that do not fill the GPU once more share out the
   // rows of Z between them, down to about two tiles a share. (At 4096 rows,
   // r = 128, 1187 blocks of which 512 run at a time: 333 us with the last 163
   // in three shares and 7 for joining them, 345 without.)
-  const int64_t ntiles = ceil_div(N, p.RB), slots = p.RP == 512 ? kTargetBlocks / 2 : kTargetBlocks;
+  const int64_t ntiles = ceil_div(N, p.RB);
   p.col_whole = cblocks / slots * slots;
   const int64_t rest = cblocks - p.col_whole;
   p.col_splits = rest ? (int)std::max<int64_t>(1, std::min<int64_t>(slots / rest, ntiles / 2)) : 1;
+  if (p.few) p.col_splits = 1;
   if (p.col_splits == 1) p.col_whole = cblocks;
   p.split_rows = V - std::min(V, p.col_whole * (dtype == 0 ? p.GC : 64));
   p.npad = ceil_div(N, 64) * 64;
@@ -1065,9 +1287,9 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
     o += align256(bytes);
     return at;
   };
-  p.pm = take(size_t(p.shares) * N * 4);
-  p.pl = take(size_t(p.shares) * N * 4);
-  p.po = take(size_t(p.shares) * N * p.RP * 4);
+  p.pm = take(size_t(p.row_splits) * N * 4);
+  p.pl = take(size_t(p.row_splits) * N * 4);
+  p.po = take(size_t(p.row_splits) * N * p.RP * 4);
   p.fwd_total = o;
   o = 0;
   p.zc = take(size_t(N) * p.RP * es);
@@ -1096,9 +1318,24 @@ hipError_t go_bf16(const StreamArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int RP>
+hipError_t go_few(const StreamArgs& a, hipStream_t s) {
+  const auto go = [&](auto kernel, int rows) -> hipError_t {
+    const int bytes = (rows * RP + kWaves * 32 * 32) * 2 + kNear * 8;
+    if (bytes > 65536) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(a.nx, kWaves * 32)), dim3(kWaves * kWave), bytes, s, a);
+    return hipGetLastError();
+  };
+  return a.ny <= 32 ? go(few_columns_kernel<RP, 1>, 32) : go(few_columns_kernel<RP, 2>, 64);
+}
+
 template <int RP, int XT, bool ACC>
 hipError_t go_rows(const StreamArgs& a, int WX, hipStream_t s) {
-  if constexpr (RP < 512) {
+  if constexpr (RP < 256) {
     if (WX == 1) return go_bf16<RP, XT, 1, ACC, false>(a, s);
   }
   if (WX == 2) return go_bf16<RP, XT, 2, ACC, false>(a, s);
@@ -1109,6 +1346,15 @@ template <bool ACC, bool COLS>
 hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) {
   if (dtype == 0) {
     if constexpr (COLS) {
+      if (p.few) {
+        switch (p.RP) {
+          case 32: return go_few<32>(a, s);
+          case 64: return go_few<64>(a, s);
+          case 128: return go_few<128>(a, s);
+          case 256: return go_few<256>(a, s);
+          default: return go_few<512>(a, s);
+        }
+      }
       switch (p.RP) {
         case 32: return go_bf16<32, x_tiles(32), 4, true, true>(a, s);
         case 64: return go_bf16<64, x_tiles(64), 4, true, true>(a, s);
@@ -1141,7 +1387,7 @@ template <typename T>
 void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
   hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)(d.N * (d.G ? ceil_div(d.r, kJoinCols) : 1))), dim3(kWaves * kWave), 0, s,
                      static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t, d.N, d.V, d.r, p.RP, d.k,
-                     d.inv_t, p.shares, reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
+                     d.inv_t, p.row_splits, reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
                      reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
 }
 
@@ -1219,6 +1465,7 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   a.whole = p.col_whole;
   a.splits = p.col_splits;
   a.row_c = reinterpret_cast<float*>(ws + p.row_c);
+  a.row_block = p.RB;
   a.list_start = start;
   a.list = list;
   a.dP = d.dP;
