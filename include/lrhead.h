@@ -280,7 +280,8 @@ int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const vo
  * score of +inf gives undefined ids.
  * Requirements: 1 <= m, nb <= 64, 1 <= n < 2^31, ld >= n, B >= 0. `logits`
  * need only be aligned to its elements; the workspace has at least
- * lrhead_beam_workspace_bytes bytes (0: invalid sizes).
+ * lrhead_beam_workspace_bytes bytes (0: invalid sizes), or is NULL where
+ * n <= 64, which needs none.
  */
 size_t lrhead_beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb);
 int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t* idx,

@@ -1,12 +1,13 @@
 """Python binding of the beam search operators (argument marshalling only)."""
 from __future__ import annotations
 
+import ctypes
 import math
 
 import torch
 
 from . import _lib
-from .head import _DTYPES, _need, _on, _ptr
+from .head import _DTYPES, _on
 
 
 def beam_select(logits: torch.Tensor, score: torch.Tensor, nb: int, *, idx: torch.Tensor | None = None,
@@ -21,36 +22,44 @@ def beam_select(logits: torch.Tensor, score: torch.Tensor, nb: int, *, idx: torc
     Returns (score float32, beam int32, token int32), all [B, nb]; see
     lrhead_beam_select in include/lrhead.h.
     """
-    _need(logits.dtype in _DTYPES, f"unsupported dtype {logits.dtype}")
-    _need(logits.is_cuda and logits.dim() == 3, "logits must be a device tensor [B, m, n]")
+    code = _DTYPES.get(logits.dtype)
+    if code is None or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError(f"logits must be a bfloat16 or float32 device tensor [B, m, n], not {logits.dtype} "
+                         f"{tuple(logits.shape)} on {logits.device}")
     B, m, n = logits.shape
-    _need(n >= 1 and m >= 1, "logits must have beams and columns")
-    ld = logits.stride(1) if m > 1 else logits.stride(0) if B > 1 else n
-    _need((n == 1 or logits.stride(2) == 1) and (B <= 1 or m == 1 or logits.stride(0) == m * ld) and (B * m <= 1 or ld >= n),
-          "logits must be dense rows of an even spacing")
+    s0, ld, s2 = logits.stride()
+    if m == 1:
+        ld = s0
+    if B * m <= 1:
+        ld = n
+    if n < 1 or m < 1 or (n > 1 and s2 != 1) or (B > 1 and m > 1 and s0 != m * ld) or ld < n:
+        raise ValueError("logits must be dense rows of an even spacing, with beams and columns")
     dev = logits.device
-    want = [("score", score, (B, m), (torch.float32,))]
-    if idx is not None:
-        want.append(("idx", idx, (B, m, n), (torch.int32,)))
-    if ended is not None:
-        want.append(("ended", ended, (B, m), (torch.uint8, torch.bool)))
-    for name, t, shape, dtypes in want:
-        _need(t.dtype in dtypes and tuple(t.shape) == shape and t.device == dev and t.is_contiguous(),
-              f"{name} must be a contiguous {dtypes[0]} tensor of shape {shape} on {dev}")
+    if score.dtype != torch.float32 or score.shape != (B, m) or score.device != dev or not score.is_contiguous():
+        raise ValueError(f"score must be a contiguous float32 tensor ({B}, {m}) on {dev}")
+    if idx is not None and (idx.dtype != torch.int32 or idx.shape != (B, m, n) or idx.device != dev
+                            or not idx.is_contiguous()):
+        raise ValueError(f"idx must be a contiguous int32 tensor ({B}, {m}, {n}) on {dev}")
+    if ended is not None and (ended.dtype not in (torch.uint8, torch.bool) or ended.shape != (B, m)
+                              or ended.device != dev or not ended.is_contiguous()):
+        raise ValueError(f"ended must be a contiguous bool or uint8 tensor ({B}, {m}) on {dev}")
     lib = _lib.load()
-    code = _DTYPES[logits.dtype]
     with _on(dev) as stream:
-        nbytes = lib.lrhead_beam_workspace_bytes(code, B, m, n, nb)
-        if nbytes == 0:   # the call itself says why
-            _lib.check(lib.lrhead_beam_select(code, None, n, None, None, None, 0, B, m, n, nb, None, None, None, None,
-                                              0, None), "lrhead_beam_workspace_bytes")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        out = torch.empty((B, nb), dtype=torch.float32, device=dev)
-        beam = torch.empty((B, nb), dtype=torch.int32, device=dev)
-        token = torch.empty((B, nb), dtype=torch.int32, device=dev)
-        _lib.check(lib.lrhead_beam_select(code, _ptr(logits), max(ld, n), _ptr(idx), _ptr(score), _ptr(ended), end_id,
-                                          B, m, n, nb, _ptr(out), _ptr(beam), _ptr(token), _ptr(ws), nbytes, stream),
-                   "lrhead_beam_select")
+        ws, nbytes = None, 0
+        if n > 64:
+            nbytes = lib.lrhead_beam_workspace_bytes(code, B, m, n, nb)
+            if nbytes:   # else the call itself says why
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rows = max(nb, 0)
+        out = torch.empty((B, rows), dtype=torch.float32, device=dev)
+        beam = torch.empty((B, rows), dtype=torch.int32, device=dev)
+        token = torch.empty((B, rows), dtype=torch.int32, device=dev)
+        rc = lib.lrhead_beam_select(code, logits.data_ptr(), ld, None if idx is None else idx.data_ptr(),
+                                    score.data_ptr(), None if ended is None else ended.data_ptr(), end_id, B, m, n, nb,
+                                    out.data_ptr(), beam.data_ptr(), token.data_ptr(),
+                                    None if ws is None else ws.data_ptr(), nbytes, stream)
+        if rc:
+            _lib.check(rc, "lrhead_beam_select")
     return out, beam, token
 
 
@@ -66,43 +75,45 @@ def reorder(states, parent: torch.Tensor, *, length: torch.Tensor | None = None,
     """
     single = isinstance(states, torch.Tensor)
     states = [states] if single else list(states)
-    _need(parent.is_cuda and parent.dtype == torch.int32 and parent.dim() == 2 and parent.is_contiguous(),
-          "parent must be a contiguous int32 device tensor [B, nb]")
+    if not parent.is_cuda or parent.dtype != torch.int32 or parent.dim() != 2 or not parent.is_contiguous():
+        raise ValueError("parent must be a contiguous int32 device tensor [B, nb]")
     dev = parent.device
     B, nb = parent.shape
-    _need(len(states) <= _lib.STATES_MAX, f"at most {_lib.STATES_MAX} states")
     if out is None:
         out = [None] * len(states)
     else:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
-        _need(len(out) == len(states), "out must have one tensor per state")
-    if length is not None:
-        _need(length.device == dev and length.dtype == torch.int32 and tuple(length.shape) == (B,)
-              and length.is_contiguous(), f"length must be a contiguous int32 tensor of shape ({B},) on {dev}")
+        if len(out) != len(states):
+            raise ValueError("out must have one tensor per state")
+    if length is not None and (length.device != dev or length.dtype != torch.int32 or length.shape != (B,)
+                               or not length.is_contiguous()):
+        raise ValueError(f"length must be a contiguous int32 tensor ({B},) on {dev}")
     if not states:
         return []
     m = states[0].shape[1] if states[0].dim() >= 2 else 0
-    arr = (_lib.State * len(states))()
+    table = []   # lrhead_state_t, field by field
     with _on(dev) as stream:
         for i, x in enumerate(states):
-            _need(x.device == dev and x.dim() >= 2 and x.shape[0] == B and x.shape[1] == m and x.is_contiguous(),
-                  f"state {i} must be a contiguous tensor [{B}, {m}, ...] on {dev}")
-            shape = (B, nb, *x.shape[2:])
-            if out[i] is None:
-                out[i] = torch.zeros(shape, dtype=x.dtype, device=dev)
+            shape = x.shape
+            if len(shape) < 2 or shape[0] != B or shape[1] != m or x.device != dev or not x.is_contiguous():
+                raise ValueError(f"state {i} must be a contiguous tensor [{B}, {m}, ...] on {dev}")
             o = out[i]
-            _need(o.device == dev and o.dtype == x.dtype and tuple(o.shape) == shape and o.is_contiguous(),
-                  f"out {i} must be a contiguous {x.dtype} tensor {shape} on {dev}")
-            s = arr[i]
-            s.src, s.dst = x.data_ptr(), o.data_ptr()
+            if o is None:
+                o = out[i] = torch.zeros((B, nb, *shape[2:]), dtype=x.dtype, device=dev)
+            elif (o.dtype != x.dtype or o.shape[:2] != (B, nb) or o.shape[2:] != shape[2:] or o.device != dev
+                  or not o.is_contiguous()):
+                raise ValueError(f"out {i} must be a contiguous {x.dtype} tensor {(B, nb, *shape[2:])} on {dev}")
             if length is None:
-                s.segs, s.positions, s.position_bytes = 1, 1, math.prod(x.shape[2:]) * x.element_size()
+                table += (x.data_ptr(), o.data_ptr(), 1, 1, math.prod(shape[2:]) * x.element_size())
             else:
-                d = dim + x.dim() if dim < 0 else dim
-                _need(2 <= d < x.dim(), f"state {i} has no dimension {dim} behind its beams")
-                s.segs, s.positions = math.prod(x.shape[2:d]), x.shape[d]
-                s.position_bytes = math.prod(x.shape[d + 1:]) * x.element_size()
+                d = dim + len(shape) if dim < 0 else dim
+                if not 2 <= d < len(shape):
+                    raise ValueError(f"state {i} has no dimension {dim} behind its beams")
+                table += (x.data_ptr(), o.data_ptr(), math.prod(shape[2:d]), shape[d],
+                          math.prod(shape[d + 1:]) * x.element_size())
         if nb and m:
-            _lib.check(_lib.load().lrhead_reorder(arr, len(states), _ptr(parent), _ptr(length), B, m, nb, stream),
-                       "lrhead_reorder")
+            rc = _lib.load().lrhead_reorder((ctypes.c_int64 * len(table))(*table), len(states), parent.data_ptr(),
+                                            None if length is None else length.data_ptr(), B, m, nb, stream)
+            if rc:
+                _lib.check(rc, "lrhead_reorder")
     return out[0] if single else out

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBeamWaves = kThreads / kWave;
+constexpr int kMostWaves = 16;   // of a block that joins: a wave per beam up to here
 constexpr float kLog2eHi = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -34,6 +35,11 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t x) {
   const uint32_t hi = wave_max_u32((uint32_t)(x >> 32));
   const uint32_t lo = wave_max_u32((uint32_t)(x >> 32) == hi ? (uint32_t)x : 0u);
   return ((uint64_t)hi << 32) | lo;
+}
+
+template <int S>
+__device__ __forceinline__ uint64_t lane_xor_u64(uint64_t x) {
+  return ((uint64_t)(uint32_t)lane_xor<S>((int)(x >> 32)) << 32) | (uint32_t)lane_xor<S>((int)x);
 }
 
 __device__ __forceinline__ double wave_sum_f64(double x) {
@@ -95,22 +101,23 @@ struct SelectArgs {
 
 // One slice of one row: CH 16-byte chunks per thread, neighbouring threads on
 // neighbouring chunks. The slice's nb best are at least as large as the
-// nb-th largest of the threads' own maxima, a bound that few others pass.
-template <typename T, int CH, bool IDS>
+// nb-th largest of the maxima of 64 * KG groups of threads, a bound that few
+// others pass (KG = 1 up to 16 best, 2 up to 32, else 4). Any bound that 16 KG
+// group maxima at most reach will do: 64 threads then hold what passes it.
+template <typename T, int CH, bool IDS, int KG>
 __global__ void __launch_bounds__(kThreads) beam_slice_kernel(SelectArgs a) {
   constexpr int EP = Elems<T>::n, E = CH * EP;
-  constexpr int kSlice = kThreads * E;
-  __shared__ __attribute__((aligned(16))) uint64_t tmax[kThreads];
-  __shared__ uint64_t cand[64 * E];   // at most nb threads hold a key that passes the bound
+  constexpr int kSlice = kThreads * E, kGroups = 64 * KG;
+  __shared__ __attribute__((aligned(16))) uint64_t gmax[kGroups];
+  __shared__ uint64_t cand[64 * E];
   __shared__ uint32_t red[kBeamWaves];
   __shared__ float reds[kBeamWaves];
-  __shared__ uint64_t bound;
   __shared__ int count;
   const int64_t row = blockIdx.x / a.slices;
   const int slice = blockIdx.x % a.slices;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
-  uint64_t* out = a.keys + ((int64_t)row * a.slices + slice) * a.nb;
   if (a.ended && a.ended[row]) return;   // its one continuation needs no logits
+  uint64_t* out = a.keys + (row * a.slices + slice) * a.nb;
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
   const int64_t c0 = (int64_t)slice * kSlice;
 
@@ -121,10 +128,10 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(SelectArgs a) {
     if (col + EP <= a.n) {
       const u32x4 w = load16_any(x + col);
 #pragma unroll
-      for (int e = 0; e < EP; ++e) v[c * EP + e] = Elems<T>::get(w, e);
+      for (int e = 0; e < EP; ++e) v[c * EP + e] = fmaxf(Elems<T>::get(w, e), neg_inf());   // NaN becomes -inf
     } else {
 #pragma unroll
-      for (int e = 0; e < EP; ++e) v[c * EP + e] = col + e < a.n ? Elems<T>::one(x + col + e) : neg_inf();
+      for (int e = 0; e < EP; ++e) v[c * EP + e] = col + e < a.n ? fmaxf(Elems<T>::one(x + col + e), neg_inf()) : neg_inf();
     }
     if constexpr (IDS) {
 #pragma unroll
@@ -132,10 +139,11 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(SelectArgs a) {
         if (col + e < a.n && a.idx[row * a.n + col + e] < 0) v[c * EP + e] = neg_inf();
     }
   }
+  if (tid == 0) count = 0;
   float hi = neg_inf();
   int at = 0;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {   // NaN compares false and stays out
+  for (int i = 0; i < E; ++i) {
     if (v[i] > hi) {
       hi = v[i];
       at = i;
@@ -143,13 +151,12 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(SelectArgs a) {
   }
   const auto col_of = [&](int i) { return (int)(c0 + (int64_t)((i / EP) * kThreads + tid) * EP + i % EP); };
   const uint64_t mine = hi > neg_inf() ? cand_key(hi, col_of(at)) : 0ull;
-  tmax[tid] = mine;
+  uint64_t most = mine;
+  if constexpr (KG <= 2) most = max(most, lane_xor_u64<1>(most));
+  if constexpr (KG == 1) most = max(most, lane_xor_u64<2>(most));
+  if (tid % (4 / KG) == 0) gmax[tid / (4 / KG)] = most;
   const uint32_t wm = wave_max_u32((uint32_t)(mine >> 32));
   if (lane == 0) red[wave] = wm;
-  if (tid == 0) {
-    bound = 1;
-    count = 0;
-  }
   __syncthreads();
   uint32_t bm = 0;
 #pragma unroll
@@ -162,38 +169,36 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(SelectArgs a) {
     }
     return;
   }
+  uint64_t keys[KG];
+#pragma unroll
+  for (int i = 0; i < KG; ++i) keys[i] = gmax[i * 64 + lane];
+  const uint64_t lim = max(wave_window_threshold<KG>(keys, a.nb, 16 * KG), (uint64_t)1);   // in every wave
+  if (mine >= lim) {
+    const float least = lim > 1 ? key_score(lim) : -__FLT_MAX__;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (v[i] >= least) {
+        const uint64_t key = cand_key(v[i], col_of(i));
+        if (key >= lim) cand[atomicAdd(&count, 1)] = key;
+      }
+    }
+  }
   // log2(e) as the sum of two fp32: one alone is off by 1e-8 of every exponent, in one direction
   const float m = __uint_as_float(order_key_inv(bm));
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const float d = v[i] - m;
-    const float e = exp2_hw(fmaf(d, kLog2eHi, d * kLog2eLo));
-    s += v[i] > neg_inf() ? e : 0.f;
+    s += exp2_hw(fmaf(d, kLog2eHi, d * kLog2eLo));   // 0 of -inf: m is finite
   }
   s = group_sum<kWave>(s);
   if (lane == 0) reds[wave] = s;
-  int rank = 0;
-  const u64x2* t2 = reinterpret_cast<const u64x2*>(tmax);
-#pragma unroll 16
-  for (int q = 0; q < kThreads / 2; ++q) rank += (t2[q].x > mine) + (t2[q].y > mine);
-  if (mine && rank == a.nb - 1) bound = mine;
-  __syncthreads();
-  const uint64_t lim = bound;
-  if (mine >= lim) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if (v[i] > neg_inf()) {
-        const uint64_t key = cand_key(v[i], col_of(i));
-        if (key >= lim) cand[atomicAdd(&count, 1)] = key;
-      }
-    }
-  }
   __syncthreads();
   const int n = count;
   for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = cand[i];
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) r += cand[j] > key;
     if (r < a.nb) out[r] = key;
   }
@@ -213,39 +218,49 @@ struct Lists {
 
 __device__ __forceinline__ void join_beams(const SelectArgs& a, int64_t b, const Lists& L) {
   const int lane = threadIdx.x & 63;
-  int at = 0;
+  int at = 0, beam = -1, col = 0;   // lane j: the j-th best
+  uint64_t got = 0;
   uint64_t head = lane < a.m ? L.total[lane * a.nb] : 0;
   for (int j = 0; j < a.nb; ++j) {
     const uint64_t best = wave_max_u64(head);
-    const int64_t o = b * a.nb + j;
-    if (!best) {
-      if (lane == 0) {
-        a.out_score[o] = neg_inf();
-        a.out_beam[o] = -1;
-        a.out_token[o] = -1;
-      }
-      continue;
-    }
+    if (!best) break;
     const int win = __ffsll((unsigned long long)__ballot(head == best)) - 1;
+    const int from = win * a.nb + __builtin_amdgcn_readlane(at, win);
+    if (lane == j) {
+      got = best;
+      beam = win;
+      col = from;
+    }
     if (lane == win) {
-      const int64_t row = b * a.m + lane;
-      const int col = L.col[lane * a.nb + at];
-      a.out_score[o] = (float)total_of(best);
-      a.out_beam[o] = lane;
-      a.out_token[o] = a.ended && a.ended[row] ? a.end_id : a.idx ? a.idx[row * a.n + col] : col;
       ++at;
       head = at < a.nb ? L.total[lane * a.nb + at] : 0;
     }
   }
+  if (lane >= a.nb) return;
+  const int64_t o = b * a.nb + lane;
+  int token = -1;
+  if (got) {
+    const int64_t row = b * a.m + beam;
+    const int c = L.col[col];
+    token = a.ended && a.ended[row] ? a.end_id : a.idx ? a.idx[row * a.n + c] : c;
+  }
+  a.out_score[o] = got ? (float)total_of(got) : neg_inf();
+  a.out_beam[o] = beam;
+  a.out_token[o] = token;
 }
 
-// Joins the slices of each beam (a wave per beam) and then the beams.
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(SelectArgs a) {
+// Joins the slices of each beam (a wave per beam) and then the beams. Of the
+// slices' lists, a lane takes every 64th; a bound that at
+// least nb of the lanes' best heads reach bounds the beam's nb best, and what
+// passes it is ranked. (Lists that pass it more than kPassed times over, as ascending rows make them,
+// take the best head nb times instead.)
+constexpr int kPassed = 256;
+__global__ void __launch_bounds__(kMostWaves* kWave) beam_join_kernel(SelectArgs a) {
   extern __shared__ uint64_t lds[];
   const Lists L{lds, reinterpret_cast<int*>(lds + a.m * a.nb)};
   const int64_t b = blockIdx.x;
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  for (int i = wave; i < a.m; i += kBeamWaves) {
+  const int wave = wave_id(), lane = threadIdx.x & 63, waves = blockDim.x / kWave;
+  for (int i = wave; i < a.m; i += waves) {
     const int64_t row = b * a.m + i;
     const double c = a.score[row];
     uint64_t* total = L.total + i * a.nb;
@@ -259,18 +274,61 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(SelectArgs a) {
     }
     const float* top = a.top + row * a.slices;
     const float* sum = a.sum + row * a.slices;
+    const uint64_t* keys = a.keys + row * a.slices * a.nb;
     float hi = neg_inf();
-    for (int s = lane; s < a.slices; s += kWave) hi = fmaxf(hi, top[s]);
+    uint64_t best[1] = {0};
+    for (int s = lane; s < a.slices; s += kWave) {
+      hi = fmaxf(hi, top[s]);
+      best[0] = max(best[0], keys[(int64_t)s * a.nb]);
+    }
 #pragma unroll
     for (int o = 32; o; o >>= 1) hi = fmaxf(hi, __shfl_xor(hi, o));
     double l = 0.0;
-    for (int s = lane; s < a.slices; s += kWave)
-      if (sum[s] != 0.f) l += (double)sum[s] * exp((double)top[s] - (double)hi);
+    for (int s = lane; s < a.slices; s += kWave) {
+      const float d = top[s] - hi;
+      if (sum[s] != 0.f) l += (double)sum[s] * (double)exp2_hw(fmaf(d, kLog2eHi, d * kLog2eLo));
+    }
     l = wave_sum_f64(l);
     const double logl = log(l);   // lse - hi: hi may be so large that their sum is hi
 
-    // each lane the best head of its lists (slices lane, lane + 64, ..)
-    const uint64_t* keys = a.keys + row * a.slices * a.nb;
+    const uint64_t lim = max(wave_window_threshold<1>(best, a.nb, min(a.nb + a.nb / 2, 64)), (uint64_t)1);
+    uint64_t* mem = reinterpret_cast<uint64_t*>(L.col + a.m * a.nb + (a.m * a.nb & 1)) + wave * kPassed;
+    int n = 0;   // keys that pass, in the same order in every lane's view
+    if (a.slices <= kWave * 4) {
+      for (int s0 = 0; s0 < a.slices; s0 += kWave) {
+        const int s = s0 + lane;
+        bool more = s < a.slices;
+        for (int j = 0; j < a.nb && n <= kPassed; ++j) {
+          const uint64_t k = more ? keys[(int64_t)s * a.nb + j] : 0;
+          more = k >= lim;
+          const unsigned long long mask = __ballot(more);
+          if (!mask) break;
+          const int at = n + lanes_below(mask);
+          if (more && at < kPassed) mem[at] = k;
+          n += __popcll(mask);
+        }
+      }
+    } else {
+      n = kPassed + 1;
+    }
+    const auto put = [&](int j, uint64_t k) {
+      total[j] = k ? total_key((double)key_score(k) - (double)hi - logl + c) : 0;
+      col[j] = k ? key_id(k) : 0;
+    };
+    if (n <= kPassed) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      for (int q = lane; q < n; q += kWave) {
+        const uint64_t k = mem[q];
+        int r = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) r += mem[j] > k;
+        if (r < a.nb) put(r, k);
+      }
+      for (int j = n + lane; j < a.nb; j += kWave) put(j, 0);
+      continue;
+    }
     uint64_t head = 0;
     const auto refill = [&](uint64_t below) {   // the best of the lane's lists below a key
       head = 0;
@@ -285,12 +343,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(SelectArgs a) {
     };
     refill(~0ull);
     for (int j = 0; j < a.nb; ++j) {
-      const uint64_t best = wave_max_u64(head);
-      if (lane == 0) {
-        total[j] = best ? total_key((double)key_score(best) - (double)hi - logl + c) : 0;
-        col[j] = best ? key_id(best) : 0;
-      }
-      if (best && head == best) refill(best);
+      const uint64_t k = wave_max_u64(head);
+      if (lane == 0) put(j, k);
+      if (k && head == k) refill(k);
     }
   }
   __syncthreads();
@@ -298,14 +353,14 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(SelectArgs a) {
 }
 
 // Rows of at most 64 columns (candidate lists): a wave per beam, a lane per
-// column, everything in one launch; the exponentials in 64 bits.
+// column, everything in one launch.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_lists_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kMostWaves* kWave) beam_lists_kernel(SelectArgs a) {
   extern __shared__ uint64_t lds[];
   const Lists L{lds, reinterpret_cast<int*>(lds + a.m * a.nb)};
   const int64_t b = blockIdx.x;
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  for (int i = wave; i < a.m; i += kBeamWaves) {
+  const int wave = wave_id(), lane = threadIdx.x & 63, waves = blockDim.x / kWave;
+  for (int i = wave; i < a.m; i += waves) {
     const int64_t row = b * a.m + i;
     const double c = a.score[row];
     uint64_t* total = L.total + i * a.nb;
@@ -323,7 +378,8 @@ __global__ void __launch_bounds__(kThreads) beam_lists_kernel(SelectArgs a) {
     x += 0.f;   // -0 and +0 are the same score
     bitonic_sort_desc(x, id);
     const float hi = readlane_f(x, 0);
-    const double l = wave_sum_f64(x > neg_inf() ? exp((double)x - (double)hi) : 0.0);
+    const float d = x - hi;
+    const double l = wave_sum_f64(x > neg_inf() ? (double)exp2_hw(fmaf(d, kLog2eHi, d * kLog2eLo)) : 0.0);
     const double logl = log(l);   // lse - hi: hi may be so large that their sum is hi
     if (lane < a.nb) {
       total[lane] = x > neg_inf() ? total_key((double)x - (double)hi - logl + c) : 0;
@@ -374,18 +430,28 @@ __global__ void __launch_bounds__(kThreads) beam_move_kernel(MoveArgs a) {
   if (a.length) live = min(live, (int64_t)max(a.length[b], 0) * st.pos_bytes);
   const int64_t at = piece * kMoveBytes;
   const int64_t n = (min(live, at + kMoveBytes) - at) / (int64_t)sizeof(U);
-  const U* src = reinterpret_cast<const U*>(st.src + ((b * a.m + p) * st.segs + seg) * st.seg_bytes + at);
-  U* dst = reinterpret_cast<U*>(st.dst + (slot * st.segs + seg) * st.seg_bytes + at);
-  for (int64_t j = threadIdx.x; j < n; j += kThreads) dst[j] = src[j];
+  const U* __restrict__ src = reinterpret_cast<const U*>(st.src + ((b * a.m + p) * st.segs + seg) * st.seg_bytes + at);
+  U* __restrict__ dst = reinterpret_cast<U*>(st.dst + (slot * st.segs + seg) * st.seg_bytes + at);
+  int64_t j = threadIdx.x;
+  for (; j + 3 * kThreads < n; j += 4 * kThreads) {   // four loads in flight
+    U v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = src[j + q * kThreads];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) __builtin_nontemporal_store(v[q], dst + j + q * kThreads);
+  }
+  for (; j < n; j += kThreads) dst[j] = src[j];
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // 16-byte chunks per thread of a slice: the most for which the rows still
-// make four blocks per compute unit, so that few lists are left to join.
+// make four blocks per compute unit, so that few lists are left to join, and
+// at most 32 elements (256 rows of 151936 bf16: 32.8 us with 64, 28.8 with 32,
+// 43.7 with 16, whose bounds and ranks weigh more).
 int slice_chunks(int64_t rows, int64_t n, int per_chunk) {
-  for (int ch = 8; ch > 1; ch /= 2)
+  for (int ch = 32 / per_chunk; ch > 1; ch /= 2)
     if (rows * ceil_div(n, (int64_t)kThreads * per_chunk * ch) >= 1024) return ch;
   return 1;
 }
@@ -394,11 +460,17 @@ int slice_count(int dtype, int64_t rows, int64_t n) {
   return (int)ceil_div(n, (int64_t)kThreads * per * slice_chunks(rows, n, per));
 }
 
+template <typename T, int CH, bool IDS>
+void go_slices(const SelectArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.rows * a.slices)), block(kThreads);
+  if (a.nb <= 16) hipLaunchKernelGGL((beam_slice_kernel<T, CH, IDS, 1>), grid, block, 0, s, a);
+  else if (a.nb <= 32) hipLaunchKernelGGL((beam_slice_kernel<T, CH, IDS, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((beam_slice_kernel<T, CH, IDS, 4>), grid, block, 0, s, a);
+}
 template <typename T, int CH>
 void go_slices(const SelectArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.rows * a.slices));
-  if (a.idx) hipLaunchKernelGGL((beam_slice_kernel<T, CH, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((beam_slice_kernel<T, CH, false>), grid, dim3(kThreads), 0, s, a);
+  if (a.idx) go_slices<T, CH, true>(a, s);
+  else go_slices<T, CH, false>(a, s);
 }
 template <typename T>
 void slices(const SelectArgs& a, hipStream_t s) {
@@ -406,7 +478,8 @@ void slices(const SelectArgs& a, hipStream_t s) {
     case 1: return go_slices<T, 1>(a, s);
     case 2: return go_slices<T, 2>(a, s);
     case 4: return go_slices<T, 4>(a, s);
-    default: return go_slices<T, 8>(a, s);
+    default:
+      if constexpr (sizeof(T) == 4) go_slices<T, 8>(a, s);
   }
 }
 
@@ -417,7 +490,7 @@ bool beam_fits(int dtype, int64_t B, int m, int64_t n) {
 }
 
 size_t beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb) {
-  if (n <= kWave) return 256;
+  if (n <= kWave) return 256;   // not used
   const int64_t rows = B * m;
   const size_t lists = (size_t)rows * slice_count(dtype, rows, n);
   return align256(lists * nb * 8) + 2 * align256(lists * 4);
@@ -440,12 +513,13 @@ hipError_t launch_beam_select(int dtype, const void* x, int64_t ld, const int32_
   a.out_score = out_score;
   a.out_beam = out_beam;
   a.out_token = out_token;
-  const size_t lds = (size_t)m * nb * 12;   // at most 48 KiB
+  const int waves = std::min(m, kMostWaves);
+  const size_t lds = (size_t)m * nb * 12;   // at most 48 KiB; with the joining waves' own at most 80
   if (n <= kWave) {
     if (dtype == 0)
-      hipLaunchKernelGGL(beam_lists_kernel<uint16_t>, dim3((unsigned)B), dim3(kThreads), lds, s, a);
+      hipLaunchKernelGGL(beam_lists_kernel<uint16_t>, dim3((unsigned)B), dim3(waves * kWave), lds, s, a);
     else
-      hipLaunchKernelGGL(beam_lists_kernel<float>, dim3((unsigned)B), dim3(kThreads), lds, s, a);
+      hipLaunchKernelGGL(beam_lists_kernel<float>, dim3((unsigned)B), dim3(waves * kWave), lds, s, a);
     return hipGetLastError();
   }
   a.slices = slice_count(dtype, a.rows, n);
@@ -456,9 +530,15 @@ hipError_t launch_beam_select(int dtype, const void* x, int64_t ld, const int32_
   a.sum = reinterpret_cast<float*>(ws + align256(lists * nb * 8) + align256(lists * 4));
   if (dtype == 0) slices<uint16_t>(a, s);
   else slices<float>(a, s);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)B), dim3(kThreads), lds, s, a);
+  const size_t bytes = lds + 8 + (size_t)waves * kPassed * 8;
+  if (bytes > 65536) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(beam_join_kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)B), dim3(waves * kWave), bytes, s, a);
   return hipGetLastError();
 }
 

@@ -604,7 +604,8 @@ int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t*
   LRH_TRY(check_beam(dtype, B, m, n, nb));
   if (ld < n) return fail(LRHEAD_ERANGE, "ld = %lld below n = %lld", (long long)ld, (long long)n);
   if (B == 0) return LRHEAD_OK;
-  if (!logits || !score || !workspace) return fail(LRHEAD_EINVAL, "logits, score and workspace must be non-NULL");
+  if (!logits || !score || (!workspace && n > 64))
+    return fail(LRHEAD_EINVAL, "logits, score and (for n > 64) workspace must be non-NULL");
   if (reinterpret_cast<uintptr_t>(logits) % elem_bytes(dtype))
     return fail(LRHEAD_EALIGN, "logits are not aligned to their elements");
   if (!aligned16(idx) || !aligned16(score) || !aligned16(ended) || !aligned16(workspace))
@@ -613,7 +614,8 @@ int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t*
   LRH_TRY(check_out(out_beam, "out_beam", true));
   LRH_TRY(check_out(out_token, "out_token", true));
   const size_t need = lrh::beam_workspace_bytes(dtype, B, m, n, nb);
-  if (workspace_bytes < need) return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  if (workspace && workspace_bytes < need)
+    return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
   LRH_HIP(lrh::launch_beam_select(dtype, logits, ld, idx, score, ended, end_id, B, m, n, nb, out_score, out_beam,
                                   out_token, workspace, static_cast<hipStream_t>(stream)),
           "beam selection launch");

@@ -5,32 +5,37 @@ joins them for torch's autograd.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _lib
-from .head import _DTYPES, _need, _on, _ptr
+from .head import _DTYPES, _on
 
 
-def _check(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: torch.Tensor):
-    _need(Z.dtype in _DTYPES and P.dtype == Z.dtype, "Z and P must share a supported dtype (bfloat16 or float32)")
-    _need(Z.is_cuda, "Z must be a device tensor")
-    _need(Z.dim() == 2 and P.dim() == 2 and P.shape[1] == Z.shape[1], "Z must be (N, r) and P (V, r)")
-    N = Z.shape[0]
-    _need(idx.dtype == torch.int32 and logits.dtype == torch.float32, "idx must be int32 and logits float32")
-    _need(idx.dim() == 2 and idx.shape[0] == N and logits.shape == idx.shape, f"idx and logits must be ({N}, k)")
-    for name, t in (("Z", Z), ("P", P), ("idx", idx), ("logits", logits)):
-        _need(t.device == Z.device and t.is_contiguous(), f"{name} must be contiguous on {Z.device}")
-    return N, int(P.shape[0]), int(Z.shape[1]), int(idx.shape[1])
+def _check(Z, P, idx, logits):
+    """(dtype code, N, V, r, k) of a call's inputs."""
+    code = _DTYPES.get(Z.dtype)
+    if code is None or P.dtype != Z.dtype:
+        raise ValueError(f"Z and P must share a supported dtype (bfloat16 or float32), not {Z.dtype} and {P.dtype}")
+    if not Z.is_cuda:
+        raise ValueError("Z must be a device tensor")
+    if Z.dim() != 2 or P.dim() != 2 or P.shape[1] != Z.shape[1]:
+        raise ValueError(f"Z must be (N, r) and P (V, r), not {tuple(Z.shape)} and {tuple(P.shape)}")
+    N, r = Z.shape
+    if idx.dtype != torch.int32 or logits.dtype != torch.float32:
+        raise ValueError(f"idx must be int32 and logits float32, not {idx.dtype} and {logits.dtype}")
+    if idx.dim() != 2 or idx.shape[0] != N or logits.shape != idx.shape:
+        raise ValueError(f"idx and logits must be ({N}, k), not {tuple(idx.shape)} and {tuple(logits.shape)}")
+    dev = Z.device
+    for t in (Z, P, idx, logits):
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"Z, P, idx and logits must be contiguous on {dev}")
+    return code, N, P.shape[0], r, idx.shape[1]
 
 
 def _workspace(lib, code, V, r, N, k, device):
     n = lib.lrhead_distill_workspace_bytes(code, V, r, N, k)
-    if n == 0:   # the call itself says why
-        _lib.check(lib.lrhead_distill(code, V, r, None, None, N, None, None, k, 1.0, None, None, None, None, 0, None),
-                   "lrhead_distill_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    # without sizes that can be, the call itself says why
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 def distill(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: torch.Tensor, *, temperature: float = 1.0,
@@ -40,17 +45,19 @@ def distill(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: torch.T
     Head.full_topk returns them; an id outside [0, V) marks an empty place):
     (loss [N], lse [N], dloss/dZ [N, r] or None), float32. See lrhead_distill
     in include/lrhead.h."""
-    N, V, r, k = _check(Z, P, idx, logits)
+    code, N, V, r, k = _check(Z, P, idx, logits)
     lib = _lib.load()
-    code, dev = _DTYPES[Z.dtype], Z.device
+    dev = Z.device
     with _on(dev) as stream:
         ws = _workspace(lib, code, V, r, N, k, dev)
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         lse = torch.empty(N, dtype=torch.float32, device=dev)
         grad = torch.empty((N, r), dtype=torch.float32, device=dev) if want_grad else None
-        _lib.check(lib.lrhead_distill(code, V, r, _ptr(P), _ptr(Z), N, _ptr(idx), _ptr(logits), k, temperature,
-                                      _ptr(loss), _ptr(lse), _ptr(grad), _ptr(ws), ws.numel(), stream),
-                   "lrhead_distill")
+        rc = lib.lrhead_distill(code, V, r, P.data_ptr(), Z.data_ptr(), N, idx.data_ptr(), logits.data_ptr(), k,
+                                temperature, loss.data_ptr(), lse.data_ptr(), None if grad is None else grad.data_ptr(),
+                                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), stream)
+        if rc:
+            _lib.check(rc, "lrhead_distill")
     return loss, lse, grad
 
 
@@ -61,26 +68,26 @@ def distill_grad(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: to
     None) in Z's dtype, from lse and grad of distill() on the same inputs
     (grad may be None without dZ). weight: [N] float32, None for ones. See
     lrhead_distill_grad in include/lrhead.h."""
-    N, V, r, k = _check(Z, P, idx, logits)
+    code, N, V, r, k = _check(Z, P, idx, logits)
     dev = Z.device
-    want = [("lse", lse, (N,))]
-    if want_dZ:
-        _need(grad is not None, "dZ needs the grad of distill()")
-        want.append(("grad", grad, (N, r)))
-    if weight is not None:
-        want.append(("weight", weight, (N,)))
-    for name, t, shape in want:
-        _need(t.dtype == torch.float32 and tuple(t.shape) == shape and t.device == dev and t.is_contiguous(),
-              f"{name} must be a contiguous float32 tensor of shape {shape} on {dev}")
+    if want_dZ and grad is None:
+        raise ValueError("dZ needs the grad of distill()")
+    for name, t, shape in (("lse", lse, (N,)), ("grad", grad if want_dZ else None, (N, r)), ("weight", weight, (N,))):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {dev}")
     lib = _lib.load()
-    code = _DTYPES[Z.dtype]
     with _on(dev) as stream:
         ws = _workspace(lib, code, V, r, N, k, dev)
         dZ = torch.empty_like(Z) if want_dZ else None
         dP = torch.empty_like(P) if want_dP else None
-        _lib.check(lib.lrhead_distill_grad(code, V, r, _ptr(P), _ptr(Z), N, _ptr(idx), _ptr(logits), k, temperature,
-                                           _ptr(lse), _ptr(grad) if want_dZ else None, _ptr(weight), _ptr(dZ),
-                                           _ptr(dP), _ptr(ws), ws.numel(), stream), "lrhead_distill_grad")
+        rc = lib.lrhead_distill_grad(code, V, r, P.data_ptr(), Z.data_ptr(), N, idx.data_ptr(), logits.data_ptr(), k,
+                                     temperature, lse.data_ptr(), grad.data_ptr() if want_dZ else None,
+                                     None if weight is None else weight.data_ptr(),
+                                     None if dZ is None else dZ.data_ptr(), None if dP is None else dP.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), stream)
+        if rc:
+            _lib.check(rc, "lrhead_distill_grad")
     return dZ, dP
 
 
