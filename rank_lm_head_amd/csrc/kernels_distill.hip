@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   const int64_t x0 = (xtile * WX + wx) * (32 * XT);
 
   f32x16 acc[XT][ACC ? RT : 1] = {};
-  float m[XT], l[XT];
+  float m[XT], l[XT], odd[XT];   // the sum in two parts
 #pragma unroll
   for (int xt = 0; xt < XT; ++xt) {
     m[xt] = neg_inf();
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   for (int attempt = 0;; ++attempt) {
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
-      l[xt] = 0.f;
+      l[xt] = odd[xt] = 0.f;
       if constexpr (!COLS) {
 #pragma unroll
         for (int rt = 0; rt < (ACC ? RT : 1); ++rt) acc[xt][rt] = f32x16{};
@@ -488,15 +488,12 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
       } else {
         if constexpr (!std::is_same_v<decltype(left), std::integral_constant<int, 32>>) mask(S, left);
 #pragma unroll
-        for (int xt = 0; xt < XT; ++xt) {
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int xt = 0; xt < XT; ++xt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             S[xt][i] = exp2_hw(fmaf(S[xt][i], a.scale, -m[xt]));
-            part[i & 3] += S[xt][i];
+            (i & 1 ? odd : l)[xt] += S[xt][i];
           }
-          l[xt] += (part[0] + part[1]) + (part[2] + part[3]);
-        }
       }
       if constexpr (ACC) {
         // E as the right operand. It is rounded to bf16 here (off by at most
@@ -530,7 +527,10 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
     // score.
     bool over = false;
 #pragma unroll
-    for (int xt = 0; xt < XT; ++xt) over |= !(l[xt] <= kMostSum);
+    for (int xt = 0; xt < XT; ++xt) {
+      l[xt] += odd[xt];
+      over |= !(l[xt] <= kMostSum);
+    }
     if (attempt || !__syncthreads_or(over)) break;
     each_subtile([&](const uint16_t* tile, const float*, const float*, auto left) {
       f32x16 S[XT];
