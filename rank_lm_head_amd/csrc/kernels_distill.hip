@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
     if constexpr (!COLS) {
       if (t_full < t_end) one_tile((int)(t_full - t_begin) & 1, t_full, std::true_type());
     }
+    if constexpr (!COLS) __builtin_amdgcn_s_setprio(0);
     __syncthreads();   // the tiles may be filled again
   };
   const auto mask = [&](f32x16 (&S)[XT], int left) {   // the rows past the vocabulary's end
@@ -468,7 +469,13 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
     }
     each_subtile([&](const uint16_t* tile, const float* row_c, const float* row_s, auto left) {
       f32x16 S[XT];
+      // A wave's matrix instructions go before the other's vector instructions:
+      // the two fall out of step sooner and wait less for the same unit (rows
+      // pass, r = 128: 307 -> 295 us; the columns pass gains nothing, and
+      // spills at r = 256).
+      if constexpr (!COLS) __builtin_amdgcn_s_setprio(1);
       scores<RP, XT>(tile, at, X, S);
+      if constexpr (!COLS) __builtin_amdgcn_s_setprio(0);
       uint32_t sign[8];
       if constexpr (COLS) {
         f32x4 c[4];
@@ -501,6 +508,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
           bf16x8 E[XT];
+          if (!COLS && s2 == 0) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
           for (int xt = 0; xt < XT; ++xt) {
             u32x4 v;
@@ -630,7 +638,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
 // flight rather than for reuse. All rows of Z sit in LDS and all weights of a
 // wave's 32 columns in registers; dP then takes shape 32 columns of r at a
 // time, which leaves room for a second block (r = 512: one block and 256
-// accumulators in the general kernel; 64 rows, 151936 tokens: PLACEHOLDER).
+// accumulators in the general kernel; 64 rows, 151936 tokens: 173 -> 78 us).
 constexpr int kNear = 512;
 template <int RP, int NS>
 __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArgs a) {
@@ -903,12 +911,15 @@ __device__ __forceinline__ bool teacher(int64_t V, int& id, float x, float& p, f
   return true;
 }
 
-// Joins the shares of the rows pass. A block takes one row and 64 of its
-// columns: 16 lanes hold 4 columns each, and 16 such groups share out the
+// Joins the shares of the rows pass. A block takes one row and 4 L of its
+// columns: L lanes hold 4 columns each, and 256 / L such groups share out the
 // shares of the weighted sum and the teacher's places. The first block of a
-// row also writes its lse and loss.
-constexpr int kJoinCols = 64;
-template <typename T>
+// row also writes its lse and loss. What bounds it is the chain of dependent
+// loads (shares' maxima, ids, the ids' rows), so a row gets as few blocks as
+// its columns allow, and the sums are on their way before their weights are
+// made (4096 rows, r = 128, 16 shares: 31 us with two blocks a row, 24 with
+// one; 2048 rows, r = 256: 49 us with four, 40 with one).
+template <typename T, int L>
 __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
     const T* __restrict__ Z, const T* __restrict__ P, const int32_t* __restrict__ idx, const float* __restrict__ t,
     int64_t N, int64_t V, int r, int RP, int k, float inv_t, int shares, const float* __restrict__ pm,
@@ -916,25 +927,46 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
     float* __restrict__ G) {
   __shared__ float sp[kWave], sdot[kWave], red[kWaves * 2], share_w[kMaxShares];
   __shared__ int sid[kWave];
-  __shared__ f32x4 part[kWaves * 4][16];
+  constexpr int kGroups = kWaves * kWave / L, kJoinCols = 4 * L;
+  __shared__ f32x4 part[kGroups][L];
   const int chunks = G ? (r + kJoinCols - 1) / kJoinCols : 1;
   const int64_t n = blockIdx.x / chunks;
   const int chunk = blockIdx.x % chunks;
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
+  const int group = tid / L, sub = tid % L;
+  const int c = chunk * kJoinCols + sub * 4;
+  const bool sums = G && c < r;
   int id = lane < k ? idx[n * k + lane] : -1;
-  float p, logp;
   const float tl = lane < k ? t[n * k + lane] * inv_t : 0.f;
+  float m = neg_inf();
+  for (int s = tid; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
+  // the first shares' sums, on their way while their weights are made
+  constexpr int kAhead = 32 / kGroups;
+  f32x4 early[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int s = group + i * kGroups;
+    early[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (sums && s < shares) early[i] = *reinterpret_cast<const f32x4*>(po + ((int64_t)s * N + n) * RP + c);
+  }
+  float p, logp;
   const bool any = teacher(V, id, tl, p, logp);   // every wave: the same values
   if (wave == 0) {
     sid[lane] = id;
     sp[lane] = p;
   }
-  float m = neg_inf();
-  for (int s = tid; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
 #pragma unroll
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   if (lane == 0) red[wave] = m;
   __syncthreads();
+  constexpr int kPlaces = kWave / kGroups;   // of a group: k <= 64
+  T places[kPlaces][4];
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    const int v = sid[group + i * kGroups];
+    const T* q = P + (sums && v != INT_MAX ? (int64_t)v * r + c : 0);
+    __builtin_memcpy(places[i], __builtin_assume_aligned(q, 4 * sizeof(T)), 4 * sizeof(T));
+  }
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   float l = 0.f;
   for (int s = tid; s < shares; s += kWaves * kWave) {
@@ -945,15 +977,14 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   }
   l = group_sum<kWave>(l);
   if (lane == 0) red[kWaves + wave] = l;
-  const int group = tid >> 4, sub = tid & 15;
   if (chunk == 0) {   // the places' scores: 16 lanes per place
-    for (int j = group; j < k; j += kWaves * 4) {
+    for (int j = tid / 16; j < k; j += kWaves * 4) {
       const int v = sid[j];
       float d = 0.f;
       if (v != INT_MAX)
-        for (int c = sub * 8; c < r; c += 128) d = dot8(P + (int64_t)v * r + c, Z + n * r + c, d);
+        for (int e = tid % 16 * 8; e < r; e += 128) d = dot8(P + (int64_t)v * r + e, Z + n * r + e, d);
       d = group_sum<16>(d);
-      if (sub == 0) sdot[j] = d;
+      if (tid % 16 == 0) sdot[j] = d;
     }
   }
   __syncthreads();
@@ -969,33 +1000,36 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   }
   if (!G) return;
   const float il = 1.f / l;
-  const int c = chunk * kJoinCols + sub * 4;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  if (c < r) {
-#pragma unroll 4
-    for (int s = group; s < shares; s += kWaves * 4) {
+  if (sums) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = group + i * kGroups;
+      const float w = s < shares ? share_w[s] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = w != 0.f ? fmaf(early[i][e], w, o[e]) : o[e];
+    }
+#pragma unroll 8
+    for (int s = group + kAhead * kGroups; s < shares; s += kGroups) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(po + ((int64_t)s * N + n) * RP + c);
       const float w = share_w[s];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], w, o[i]);
+      for (int e = 0; e < 4; ++e) o[e] = w != 0.f ? fmaf(v[e], w, o[e]) : o[e];
     }
     o *= il;
 #pragma unroll
-    for (int i0 = 0; i0 < 4; ++i0) {   // k <= 64
-      const int j = group + i0 * (kWaves * 4);
+    for (int i = 0; i < kPlaces; ++i) {
+      const int j = group + i * kGroups;
       const bool real = sid[j] != INT_MAX;
-      const T* q = P + (real ? (int64_t)sid[j] * r + c : 0);
-      T v[4];
-      __builtin_memcpy(v, __builtin_assume_aligned(q, sizeof(v)), sizeof(v));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = real ? fmaf(-sp[j], widen<T>(v[i]), o[i]) : o[i];
+      for (int e = 0; e < 4; ++e) o[e] = real ? fmaf(-sp[j], widen<T>(places[i][e]), o[e]) : o[e];
     }
   }
   part[group][sub] = o;
   __syncthreads();
   if (group == 0 && c < r) {
 #pragma unroll
-    for (int g = 1; g < kWaves * 4; ++g) o += part[g][sub];
+    for (int g = 1; g < kGroups; ++g) o += part[g][sub];
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = any ? o[i] * inv_t : 0.f;
     *reinterpret_cast<f32x4*>(G + n * r + c) = o;
@@ -1383,12 +1417,18 @@ hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) 
   return hipGetLastError();
 }
 
+template <typename T, int L>
+void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
+  hipLaunchKernelGGL((distill_finish_kernel<T, L>), dim3((unsigned)(d.N * (d.G ? ceil_div(d.r, 4 * L) : 1))),
+                     dim3(kWaves * kWave), 0, s, static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t,
+                     d.N, d.V, d.r, p.RP, d.k, d.inv_t, p.row_splits, reinterpret_cast<float*>(ws + p.pm),
+                     reinterpret_cast<float*>(ws + p.pl), reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
+}
 template <typename T>
 void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
-  hipLaunchKernelGGL(distill_finish_kernel<T>, dim3((unsigned)(d.N * (d.G ? ceil_div(d.r, kJoinCols) : 1))), dim3(kWaves * kWave), 0, s,
-                     static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t, d.N, d.V, d.r, p.RP, d.k,
-                     d.inv_t, p.row_splits, reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
-                     reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
+  if (d.r <= 64 || !d.G) finish<T, 16>(p, d, ws, s);
+  else if (d.r <= 128) finish<T, 32>(p, d, ws, s);
+  else finish<T, 64>(p, d, ws, s);
 }
 
 template <typename T>
