@@ -248,8 +248,10 @@ int lrhead_factor(const void* W, int64_t V, int64_t d, int r, int q,
  *
  * Requirements: 1 <= V < 2^31, r as for lrhead_create, 0 <= N <= 2^20,
  * 1 <= k <= 64, and a workspace of lrhead_distill_workspace_bytes bytes (0:
- * invalid sizes), whose contents need not survive between the calls. N == 0
- * writes no row, but dP (zeros).
+ * invalid sizes, or so many that a launch would pass 2^32 threads: V from 2^27
+ * on in fp32, and with many rows less), whose contents need not survive
+ * between the calls. P, Z, grad, dZ, dP and the workspace are 16-byte aligned,
+ * the rest to its elements. N == 0 writes no row, but dP (zeros).
  */
 size_t lrhead_distill_workspace_bytes(int dtype, int64_t V, int64_t r, int64_t N, int k);
 int lrhead_distill(int dtype, int64_t V, int64_t r, const void* P, const void* Z, int64_t N,
@@ -278,8 +280,10 @@ int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const vo
  * at its score. Slots past the last candidate hold -inf, -1 and -1. Totals
  * are formed in fp64 (the sum of exponentials to about 1e-7). A logit or
  * score of +inf gives undefined ids.
- * Requirements: 1 <= m, nb <= 64, 1 <= n < 2^31, ld >= n, B >= 0. `logits`
- * need only be aligned to its elements; the workspace has at least
+ * Requirements: 1 <= m, nb <= 64, 1 <= n < 2^31, ld >= n, 0 <= B <= 2^20, and
+ * fewer than 2^24 slices of rows in all (up to 8192 columns each; B m rows of
+ * more than 64 columns have at least one). Inputs need only be aligned to their
+ * elements, out_* to 16 bytes; the workspace has at least
  * lrhead_beam_workspace_bytes bytes (0: invalid sizes), or is NULL where
  * n <= 64, which needs none.
  */

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kMostWaves* kWave) beam_join_kernel(SelectArgs
     const uint64_t lim = max(wave_window_threshold<1>(best, a.nb, min(a.nb + a.nb / 2, 64)), (uint64_t)1);
     uint64_t* mem = reinterpret_cast<uint64_t*>(L.col + a.m * a.nb + (a.m * a.nb & 1)) + wave * kPassed;
     int n = 0;   // keys that pass, in the same order in every lane's view
-    if (a.slices <= kWave * 4) {
+    if (a.slices <= kWave * 16) {
       for (int s0 = 0; s0 < a.slices; s0 += kWave) {
         const int s = s0 + lane;
         bool more = s < a.slices;
@@ -394,6 +394,8 @@ __global__ void __launch_bounds__(kMostWaves* kWave) beam_lists_kernel(SelectArg
 
 constexpr int kStatesPerLaunch = 32;
 constexpr int kMoveBytes = 16384;   // a block's piece of a segment
+constexpr int64_t kBlocksX = 1 << 20;             // a row of a launch's blocks
+constexpr int64_t kMostBlocks = kBlocksX * 4096;
 
 struct MoveState {
   const char* src;
@@ -407,6 +409,7 @@ struct MoveState {
 struct MoveArgs {
   MoveState st[kStatesPerLaunch];
   int states;
+  int64_t blocks;
   const int32_t* parent;   // B x nb
   const int32_t* length;   // B, or NULL
   int m, nb;
@@ -416,10 +419,12 @@ struct MoveArgs {
 // unit that the addresses and sizes of all states allow.
 template <typename U>
 __global__ void __launch_bounds__(kThreads) beam_move_kernel(MoveArgs a) {
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= a.blocks) return;
   int s = 0;
-  while (s + 1 < a.states && (int64_t)blockIdx.x >= a.st[s + 1].first) ++s;
+  while (s + 1 < a.states && block >= a.st[s + 1].first) ++s;
   const MoveState& st = a.st[s];
-  int64_t i = blockIdx.x - st.first;
+  int64_t i = block - st.first;
   const int64_t piece = i % st.pieces;
   i /= st.pieces;
   const int64_t seg = i % st.segs, slot = i / st.segs;
@@ -486,7 +491,7 @@ void slices(const SelectArgs& a, hipStream_t s) {
 }  // namespace
 
 bool beam_fits(int dtype, int64_t B, int m, int64_t n) {
-  return n <= kWave || B * m * slice_count(dtype, B * m, n) <= INT32_MAX;
+  return n <= kWave || B * m * slice_count(dtype, B * m, n) <= kMostThreads / kThreads;
 }
 
 size_t beam_workspace_bytes(int dtype, int64_t B, int m, int64_t n, int nb) {
@@ -562,7 +567,7 @@ hipError_t launch_beam_move(const BeamState* states, int n_states, const int32_t
       st.seg_bytes = in.positions * in.pos_bytes * (length ? 1 : in.segs);
       st.pieces = ceil_div(st.seg_bytes, kMoveBytes);
       const int64_t more = B * nb * st.segs * st.pieces;
-      if (a.states && blocks + more > INT32_MAX) break;   // the rest in the next launch
+      if (a.states && blocks + more > kMostBlocks) break;   // the rest in the next launch
       st.first = blocks;
       blocks += more;
       bits |= reinterpret_cast<uintptr_t>(in.src) | reinterpret_cast<uintptr_t>(in.dst) | (uintptr_t)st.seg_bytes;
@@ -571,8 +576,10 @@ hipError_t launch_beam_move(const BeamState* states, int n_states, const int32_t
       ++s0;
     }
     if (!blocks) continue;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), block(kThreads);
+    if (blocks > kMostBlocks) return hipErrorInvalidValue;
+    a.blocks = blocks;
+    const int64_t x = std::min(blocks, kBlocksX);
+    const dim3 grid((unsigned)x, (unsigned)ceil_div(blocks, x)), block(kThreads);
     if (bits % 16 == 0) hipLaunchKernelGGL(beam_move_kernel<u32x4>, grid, block, 0, s, a);
     else if (bits % 4 == 0) hipLaunchKernelGGL(beam_move_kernel<uint32_t>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(beam_move_kernel<uint8_t>, grid, block, 0, s, a);

@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
       }
       if constexpr (ACC) {
         // E as the right operand. It is rounded to bf16 here (off by at most
-        // 2^-9 of itself, nearest even); products and sums stay in fp32.
+        // 2^-8 of itself, nearest even); products and sums stay in fp32.
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
           bf16x8 E[XT];
@@ -1441,6 +1441,13 @@ void prep(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
 }
 
 }  // namespace
+
+bool distill_fits(int dtype, int64_t V, int r, int64_t N) {
+  const Plan p = plan(dtype, V, r, N, 1);
+  const int64_t lists = p.groups * kListWaves * kWave;
+  const int64_t tables = p.npad / kWave * ceil_div(p.groups / 4 + 1, kTableWords * kWaves) * kWaves * kWave;
+  return std::max(lists, tables) <= kMostThreads;
+}
 
 size_t distill_workspace_bytes(int dtype, int64_t V, int r, int64_t N, int k) {
   const Plan p = plan(dtype, V, r, N, k);

@@ -202,6 +202,8 @@ size_t factor_workspace_bytes(int64_t V, int64_t d, int r);
 hipError_t launch_factor(const void* W, int64_t V, int64_t d, int r, int q, const float* omega, void* P, void* Q,
                          void* workspace, hipStream_t stream);
 
+constexpr int64_t kMostThreads = UINT32_MAX;   // of one dimension of a grid
+
 // ------------------------------------------------------ kernels_beam.hip
 // The nb best (beam, column) of each of B sequences, see lrhead_beam_select.
 // beam_fits: whether the launch fits a grid.
@@ -242,6 +244,8 @@ struct DistillArgs {
   void* dZ;
   void* dP;
 };
+// distill_fits: whether the launches of both calls fit a grid.
+bool distill_fits(int dtype, int64_t V, int r, int64_t N);
 size_t distill_workspace_bytes(int dtype, int64_t V, int r, int64_t N, int k);
 hipError_t launch_distill(const DistillArgs& d, void* workspace, hipStream_t stream);
 hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_t stream);

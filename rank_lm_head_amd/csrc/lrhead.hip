@@ -76,6 +76,7 @@ int hip_fail(hipError_t e, const char* what) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t elem_bytes(int dtype) { return dtype == LRHEAD_BF16 ? 2 : 4; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 struct Layout {
   size_t z, part_s, part_i, raw, b1_keys, b1_lgs, sync, batch, total;
@@ -306,6 +307,8 @@ int check_distill(int dtype, int64_t V, int64_t r, int64_t N, int k) {
   if (r < 8 || r > LRHEAD_R_MAX || r % 8) return fail(LRHEAD_ERANGE, "r = %lld: need a multiple of 8 in [8, %d]", (long long)r, LRHEAD_R_MAX);
   if (N < 0 || N > kBMaxLimit) return fail(LRHEAD_ERANGE, "N = %lld outside [0, 2^20]", (long long)N);
   if (k < 1 || k > LRHEAD_K_MAX) return fail(LRHEAD_ERANGE, "k = %d outside [1, %d]", k, LRHEAD_K_MAX);
+  if (!lrh::distill_fits(dtype, V, (int)r, N > 0 ? N : 1))
+    return fail(LRHEAD_ERANGE, "V = %lld with N = %lld is too large for one call", (long long)V, (long long)N);
   return LRHEAD_OK;
 }
 
@@ -553,9 +556,10 @@ int lrhead_distill(int dtype, int64_t V, int64_t r, const void* P, const void* Z
   if (N == 0) return LRHEAD_OK;
   if (!P || !Z || !idx || !logits || !loss || !lse || !workspace)
     return fail(LRHEAD_EINVAL, "P, Z, idx, logits, loss, lse and workspace must be non-NULL");
-  if (!aligned16(P) || !aligned16(Z) || !aligned16(idx) || !aligned16(logits) || !aligned16(loss) ||
-      !aligned16(lse) || !aligned16(grad) || !aligned16(workspace))
-    return fail(LRHEAD_EALIGN, "P, Z, idx, logits, loss, lse, grad and workspace must be 16-byte aligned");
+  if (!aligned16(P) || !aligned16(Z) || !aligned16(grad) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "P, Z, grad and workspace must be 16-byte aligned");
+  if (!aligned4(idx) || !aligned4(logits) || !aligned4(loss) || !aligned4(lse))
+    return fail(LRHEAD_EALIGN, "idx, logits, loss and lse must be 4-byte aligned");
   const size_t need = lrh::distill_workspace_bytes(dtype, V, (int)r, N, k);
   if (workspace_bytes < need) return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
   lrh::DistillArgs d = distill_args(dtype, V, r, P, Z, N, idx, logits, k, temperature);
@@ -575,9 +579,10 @@ int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const vo
   if (N > 0 && (!P || !Z || !idx || !logits || !lse || !workspace))
     return fail(LRHEAD_EINVAL, "P, Z, idx, logits, lse and workspace must be non-NULL");
   if (N > 0 && dZ && !grad) return fail(LRHEAD_EINVAL, "dZ needs grad");
-  if (!aligned16(P) || !aligned16(Z) || !aligned16(idx) || !aligned16(logits) || !aligned16(lse) ||
-      !aligned16(grad) || !aligned16(weight) || !aligned16(dZ) || !aligned16(dP) || !aligned16(workspace))
-    return fail(LRHEAD_EALIGN, "a pointer is not 16-byte aligned");
+  if (!aligned16(P) || !aligned16(Z) || !aligned16(grad) || !aligned16(dZ) || !aligned16(dP) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "P, Z, grad, dZ, dP and workspace must be 16-byte aligned");
+  if (!aligned4(idx) || !aligned4(logits) || !aligned4(lse) || !aligned4(weight))
+    return fail(LRHEAD_EALIGN, "idx, logits, lse and weight must be 4-byte aligned");
   lrh::DistillArgs d = distill_args(dtype, V, r, P, Z, N, idx, logits, k, temperature);
   if (N > 0) {
     const size_t need = lrh::distill_workspace_bytes(dtype, V, (int)r, N, k);
@@ -608,8 +613,8 @@ int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t*
     return fail(LRHEAD_EINVAL, "logits, score and (for n > 64) workspace must be non-NULL");
   if (reinterpret_cast<uintptr_t>(logits) % elem_bytes(dtype))
     return fail(LRHEAD_EALIGN, "logits are not aligned to their elements");
-  if (!aligned16(idx) || !aligned16(score) || !aligned16(ended) || !aligned16(workspace))
-    return fail(LRHEAD_EALIGN, "idx, score, ended and workspace must be 16-byte aligned");
+  if (!aligned4(idx) || !aligned4(score) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "idx and score must be 4-byte aligned, the workspace 16-byte");
   LRH_TRY(check_out(out_score, "out_score", true));
   LRH_TRY(check_out(out_beam, "out_beam", true));
   LRH_TRY(check_out(out_token, "out_token", true));

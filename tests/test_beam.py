@@ -13,6 +13,7 @@ from rank_lm_head_amd import _lib
 DEV = "cuda:0"
 A = ctypes.c_void_p(0x10000)        # aligned stand-ins: never dereferenced
 MIS = ctypes.c_void_p(0x10008)
+ODD = ctypes.c_void_p(0x10002)
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 NEG = float("-inf")
 
@@ -29,8 +30,9 @@ def _select(dtype=_lib.FP32, x=A, ld=100, idx=None, score=A, ended=None, B=2, m=
     (dict(nb=65), _lib.ERANGE), (dict(n=0), _lib.ERANGE), (dict(n=1 << 31, ld=1 << 31), _lib.ERANGE),
     (dict(B=-1), _lib.ERANGE), (dict(B=1 << 20, m=64, n=1 << 30, ld=1 << 30), _lib.ERANGE), (dict(ld=99), _lib.ERANGE),
     (dict(x=None), _lib.EINVAL), (dict(score=None), _lib.EINVAL), (dict(o=None), _lib.EINVAL),
-    (dict(ot=None), _lib.EINVAL), (dict(ws=None), _lib.EINVAL), (dict(x=ctypes.c_void_p(0x10002)), _lib.EALIGN),
-    (dict(idx=MIS), _lib.EALIGN), (dict(ob=MIS), _lib.EALIGN), (dict(nbytes=16), _lib.EWORKSPACE),
+    (dict(ot=None), _lib.EINVAL), (dict(ws=None), _lib.EINVAL), (dict(x=ODD), _lib.EALIGN),
+    (dict(idx=ODD), _lib.EALIGN), (dict(score=ODD), _lib.EALIGN), (dict(ws=MIS), _lib.EALIGN),
+    (dict(B=1 << 20, m=17, n=65), _lib.ERANGE), (dict(ob=MIS), _lib.EALIGN), (dict(nbytes=16), _lib.EWORKSPACE),
 ])
 def test_select_refuses_bad_arguments_before_hip(kwargs, code):
     assert _select(**kwargs) == code
@@ -257,6 +259,27 @@ def test_rows_of_a_wider_matrix():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,nb", [(262144 + 900, 64), (600001, 7), (1100000, 33)])
+def test_many_slices(n, nb):
+    """One long row or two: more slices than a wave's lanes hold at once."""
+    x, score, _ = draw(1, 2, n, "fp32", seed=n)
+    check(x, score, nb)
+    check(x[:, :1].contiguous(), score[:, :1].contiguous(), nb)
+    up = torch.linspace(-9, 9, n, device=DEV).repeat(1, 2, 1).contiguous()   # all of the best in the last slice
+    check(up, score, nb)
+
+
+@pytest.mark.gpu
+def test_inputs_off_16_bytes():
+    x, score, _ = draw(5, 3, 900, "bf16", seed=9)
+    ids = torch.randint(0, 5000, (5, 3, 900), dtype=torch.int32, device=DEV)
+    ended = torch.rand(5, 3, device=DEV) < 0.3
+    got = lr.beam_select(x[1:], score[1:], 4, idx=ids[1:], ended=ended[1:], end_id=2)
+    want = lr.beam_select(x[1:].clone(), score[1:].clone(), 4, idx=ids[1:].clone(), ended=ended[1:].clone(), end_id=2)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """Rows that start behind 2^32 bytes."""
     n = 151936
@@ -342,6 +365,18 @@ def test_reorder_many_states_and_odd_addresses():
     with pytest.raises(lr.LrheadError):
         lr.reorder(xs[0], parent, out=xs[0])
     assert lr.reorder([], parent) == []
+
+
+@pytest.mark.gpu
+def test_reorder_of_many_short_segments():
+    """More blocks than one row of a launch."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randint(0, 100, (1, 2, 600001, 3), generator=g, dtype=torch.uint8).to(DEV)
+    got = lr.reorder(x, torch.tensor([[1, 0]], dtype=torch.int32, device=DEV),
+                     length=torch.tensor([2], dtype=torch.int32, device=DEV), dim=-1)
+    want = x[:, [1, 0]].clone()
+    want[..., 2] = 0
+    assert torch.equal(got, want)
 
 
 @pytest.mark.gpu

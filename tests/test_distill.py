@@ -19,6 +19,7 @@ from rank_lm_head_amd import _lib
 DEV = "cuda:0"
 A = ctypes.c_void_p(0x10000)        # aligned stand-ins: never dereferenced
 MIS = ctypes.c_void_p(0x10008)
+ODD = ctypes.c_void_p(0x10002)
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 H32 = torch.finfo(torch.float32).eps / 2   # half a step of fp32
 
@@ -42,7 +43,9 @@ def _grad(dtype=_lib.BF16, V=1000, r=16, P=A, Z=A, N=4, idx=A, lg=A, k=4, T=1.0,
     (dict(k=0), _lib.ERANGE), (dict(k=65), _lib.ERANGE), (dict(T=0.0), _lib.ERANGE), (dict(T=-1.0), _lib.ERANGE),
     (dict(T=float("nan")), _lib.ERANGE), (dict(T=float("inf")), _lib.ERANGE), (dict(P=None), _lib.EINVAL),
     (dict(idx=None), _lib.EINVAL), (dict(lse=None), _lib.EINVAL), (dict(ws=None), _lib.EINVAL),
-    (dict(Z=MIS), _lib.EALIGN), (dict(grad=MIS), _lib.EALIGN), (dict(n=64), _lib.EWORKSPACE),
+    (dict(Z=MIS), _lib.EALIGN), (dict(grad=MIS), _lib.EALIGN), (dict(idx=ODD), _lib.EALIGN),
+    (dict(lse=ODD), _lib.EALIGN), (dict(n=64), _lib.EWORKSPACE),
+    (dict(dtype=_lib.FP32, V=1 << 28), _lib.ERANGE), (dict(V=1 << 28, N=1 << 20), _lib.ERANGE),
 ])
 def test_calls_refuse_bad_arguments_before_hip(call, kwargs, code):
     assert call(**kwargs) == code
@@ -57,7 +60,7 @@ def test_workspace_sizes():
     ws = _lib.load().lrhead_distill_workspace_bytes
     assert ws(_lib.BF16, 151936, 128, 4096, 32) > 0
     for bad in [(3, 100, 16, 1, 1), (_lib.BF16, 0, 16, 1, 1), (_lib.BF16, 100, 15, 1, 1), (_lib.BF16, 100, 16, -1, 1),
-                (_lib.BF16, 100, 16, 1, 65)]:
+                (_lib.BF16, 100, 16, 1, 65), (_lib.FP32, 1 << 27, 16, 1, 1), (_lib.BF16, 1 << 25, 128, 1 << 20, 1)]:
         assert ws(*bad) == 0
 
 
@@ -311,6 +314,28 @@ def test_autograd_gives_the_calls_gradients():
     # an expanded gradient, as that of a sum
     gs, = torch.autograd.grad(lr.distill_loss(z2, P, idx, t, temperature=2.0).sum(), z2)
     assert torch.equal(gs, lr.distill_grad(Z, P, idx, t, lse, grad, temperature=2.0)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_micro_batches_of_odd_sizes(dt):
+    """Views that start off 16 bytes, forward and backward: the rows' own
+    results do not depend on where the batch is cut."""
+    Z, P, idx, t, w = inputs(45, 700, 32, 5, dt, seed=14)
+    loss, lse, grad = lr.distill(Z, P, idx, t)
+    want = lr.distill_grad(Z[7:], P, idx[7:], t[7:], lse[7:], grad[7:], w[7:])
+    same = lr.distill_grad(Z[7:].clone(), P, idx[7:].clone(), t[7:].clone(), lse[7:].clone(), grad[7:].clone(),
+                           w[7:].clone())
+    assert all(torch.equal(a, b) for a, b in zip(want, same))
+    z = Z.clone().requires_grad_()
+    whole = torch.cat([lr.distill_loss(z[:7], P, idx[:7], t[:7]), lr.distill_loss(z[7:], P, idx[7:], t[7:])])
+    (whole * w).sum().backward()          # the second part's gradient is a view from element 7 on
+    ref = reference(Z, P, idx, t, 1.0, w)
+    b = bounds(ref, dt, 32, 45, 5)
+    assert bool(((whole.detach().double().cpu() - ref["loss"]).abs() <= b["loss"]).all())
+    tol = b["grad"] * w.double().cpu().abs()[:, None]
+    tol = tol + b["out"] * (ref["dZ"].abs() + tol) + H32 * 2 * ref["dZ"].abs()
+    assert bool(((z.grad.double().cpu() - ref["dZ"]).abs() <= tol).all())
 
 
 @pytest.mark.gpu
