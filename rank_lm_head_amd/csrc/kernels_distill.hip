@@ -110,6 +110,11 @@ __device__ __forceinline__ int swz_row(int y) {
   else return (y >> 2) & 3;
 }
 
+// Where share `split` of `splits` (at most 2^10) begins in a list of teacher places.
+__device__ __forceinline__ uint32_t share_of(uint32_t places, int split, int splits) {
+  return (uint32_t)((uint64_t)places * (uint32_t)split / (uint32_t)splits);
+}
+
 // Rows of a tile: 32 for each of the waves that share one out, and at least
 // 16 KiB.
 template <int RP, int WX>
@@ -311,13 +316,14 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
     }
   };
   if constexpr (COLS) {
-    if (split == 0) {
+    const uint32_t e_first = a.list_start[xtile], places = a.list_start[xtile + 1] - e_first;
+    const uint32_t e_end = e_first + share_of(places, split + 1, splits);
+    uint32_t e = e_first + share_of(places, split, splits);
+    if (e < e_end) {
       // First the teacher's part of the block's columns, -w p / T z_n for every
       // place: the places' rows of Z are gathered into the tiles' LDS and go
       // through the same product, with the places' weights as the right
       // operand, each the sum of two bf16 (within 2^-17 of it; in one word).
-      const uint32_t e_end = a.list_start[xtile + 1];
-      uint32_t e = a.list_start[xtile];
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
       const auto gather = [&](int buf, uint32_t e0) {   // returns the lane's place (of TY)
@@ -334,8 +340,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
         }
         return en;
       };
-      uint2 en = {0u, 0u};
-      if (e < e_end) en = gather(0, e);
+      uint2 en = gather(0, e);
       for (int buf = 0; e < e_end; e += TY, buf ^= 1) {
         __builtin_amdgcn_s_waitcnt(0xF70);
         __syncthreads();
@@ -639,16 +644,17 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
 // wave's 32 columns in registers; dP then takes shape 32 columns of r at a
 // time, which leaves room for a second block (r = 512: one block and 256
 // accumulators in the general kernel; 64 rows, 151936 tokens: 173 -> 78 us).
-constexpr int kNear = 512;
+// The teacher's weights are scattered into a table of the wave's columns by
+// 16 rows, and join q's in fp32; a wave with any of them takes its weights as
+// two bf16 (hi + lo, within 2^-17 of their sum), others as one.
 template <int RP, int NS>
 __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArgs a) {
   constexpr int TY = NS * 32, KS = RP / 16, RT = RP / 32;
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   const int lane = threadIdx.x & 63, h = lane >> 5, wave = wave_id();
   uint16_t* const scratch = lds + TY * RP + wave * (32 * 32);
-  uint2* const near = reinterpret_cast<uint2*>(lds + TY * RP + kWaves * (32 * 32));   // the first places
   const int64_t x0 = ((int64_t)blockIdx.x * kWaves + wave) * 32;
-  const uint32_t e0 = a.list_start[blockIdx.x], e1 = a.list_start[blockIdx.x + 1];
+  const uint32_t e0 = a.list_start[blockIdx.x], count = a.list_start[blockIdx.x + 1] - e0;
 
   TileCopy<RP, TY> copy;
   copy.init(a.Y, a.ny, RP, RP);
@@ -665,38 +671,33 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArg
       X[ks] = __builtin_bit_cast(bf16x8, ok ? v : u32x4{0u, 0u, 0u, 0u});
     }
   }
-  // The first places, zeros behind the last. 16 places make a step: their rows
-  // for the left operand (by k slot and by the lane's part in a transposing
-  // read), their weights for the right one.
-  for (uint32_t i = threadIdx.x; i < kNear; i += kWaves * kWave) {
-    near[i] = i < e1 - e0 ? a.list[e0 + i] : uint2{0u, 0u};
-    if (i >= e1 - e0 + 16) break;
-  }
-  const int ya = h * 4 + ((lane & 15) >> 2);
-  int na, nb;
-  bf16x8 hi, lo;
-  const auto take = [&](auto&& entry) __attribute__((always_inline)) {
-    na = (int)(entry(ya).x & kRowMask);
-    nb = (int)(entry(ya + 8).x & kRowMask);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint2 en = entry((k >> 2) * 8 + h * 4 + (k & 3));
-      const uint32_t w = (int)(en.x >> kRowBits) == wave * 32 + (lane & 31) ? en.y : 0u;
-      hi[k] = __builtin_bit_cast(__bf16, (uint16_t)w);
-      lo[k] = __builtin_bit_cast(__bf16, (uint16_t)(w >> 16));
-    }
+  // Place i of the block: its row and column and its weight, or kNone if it is
+  // another wave's. An id that occurs more than once in a row has its
+  // entries side by side; the first takes their sum, the others are kNone.
+  constexpr uint32_t kNone = ~0u;
+  const auto place = [&](uint32_t i) {
+    uint2 en = {kNone, 0u};
+    if (i >= count) return en;
+    en = a.list[e0 + i];
+    const uint32_t key = en.x;
+    if ((int)(key >> (kRowBits + 5)) != wave || (i && a.list[e0 + i - 1].x == key)) return uint2{kNone, 0u};
+    for (uint32_t j = i + 1; j < count && a.list[e0 + j].x == key; ++j)
+      en.y = __float_as_uint(__uint_as_float(en.y) + __uint_as_float(a.list[e0 + j].y));
+    return en;
   };
-  const auto places = [&](uint32_t i) {   // from place e0 + i on
-    if (i < kNear) take([&](int y) { return near[i + y]; });
-    else take([&](int y) { return i + y < e1 - e0 ? a.list[e0 + i + y] : uint2{0u, 0u}; });
-  };
+  const uint2 first = place(lane);
+  const bool have = count > kWave || __ballot(first.x != kNone);
   Places<RP> at;
   at.init();
   __builtin_amdgcn_s_waitcnt(0xF70);
   __syncthreads();
-  places(0);
 
-  bf16x8 E[NS][2];
+  const auto ordered = [] {   // the wave's LDS writes come before its reads
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  bf16x8 E[NS][2], lo[NS][2] = {};
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     f32x16 S[1];
@@ -714,13 +715,38 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArg
       }
 #pragma unroll
     for (int s2 = 0; s2 < 2; ++s2) {
-      u32x4 v;
+      if (have) {
+        float* table = reinterpret_cast<float*>(scratch);   // [column][row of 16]
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = pack_bf16(e[s2 * 8 + i * 2], e[s2 * 8 + i * 2 + 1]);
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4*>(table + (i * kWave + lane) * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+        ordered();
+        for (uint32_t i = lane; i < (count + kWave - 1) / kWave * kWave; i += kWave) {
+          const uint2 en = i < kWave ? first : place(i);
+          const uint32_t row = en.x & kRowMask;
+          if (en.x != kNone && row / 16 == (uint32_t)(s * 2 + s2))
+            table[((en.x >> kRowBits) & 31) * 16 + row % 16] = __uint_as_float(en.y);
+        }
+        ordered();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(table + (lane & 31) * 16 + g * 8 + h * 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[s2 * 8 + g * 4 + i] += w[i];
+        }
+        ordered();
+      }
+      u32x4 v, r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float c0 = e[s2 * 8 + i * 2], c1 = e[s2 * 8 + i * 2 + 1];
+        v[i] = pack_bf16(c0, c1);
+        r[i] = pack_bf16(c0 - __uint_as_float(v[i] << 16), c1 - __uint_as_float(v[i] & 0xffff0000u));
+      }
       E[s][s2] = __builtin_bit_cast(bf16x8, v);
+      if (have) lo[s][s2] = __builtin_bit_cast(bf16x8, r);
     }
   }
-  const int have = (int)min(a.nx - x0, (int64_t)32);
+  const int rows = (int)min(a.nx - x0, (int64_t)32);
   uint16_t* out = static_cast<uint16_t*>(a.dP) + x0 * a.r;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -729,22 +755,12 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArg
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
-      for (int s2 = 0; s2 < 2; ++s2)
-        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(columns<RP>(lds + (s * 32 + s2 * 16) * RP, at, rt), E[s][s2],
-                                                         acc[0], 0, 0, 0);
-    for (uint32_t i = 0; i < e1 - e0; i += 16) {
-      if (e1 - e0 > 16) places(i);   // more than one step: made again for each 32 columns
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const int c = rt * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), half = (lane & 1) * 4;
-      const s16x4 va = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4_t)(lds + na * RP + (c ^ swz_row<RP>(na)) * 8 + half));
-      const s16x4 vb = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4_t)(lds + nb * RP + (c ^ swz_row<RP>(nb)) * 8 + half));
-      const bf16x8 A = __builtin_bit_cast(bf16x8, s16x8{va[0], va[1], va[2], va[3], vb[0], vb[1], vb[2], vb[3]});
-      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi, acc[0], 0, 0, 0);
-      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo, acc[0], 0, 0, 0);
-    }
-    store_rows<32, 32>(acc, scratch, out + rt * 32, a.r, have, a.r - rt * 32);
+      for (int s2 = 0; s2 < 2; ++s2) {
+        const bf16x8 A = columns<RP>(lds + (s * 32 + s2 * 16) * RP, at, rt);
+        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, E[s][s2], acc[0], 0, 0, 0);
+        if (have) acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[s][s2], acc[0], 0, 0, 0);
+      }
+    store_rows<32, 32>(acc, scratch, out + rt * 32, a.r, rows, a.r - rt * 32);
   }
 }
 
@@ -836,9 +852,10 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
   }
 
   if constexpr (COLS) {
-    if (split == 0 && x0 < a.nx) {
-      const uint32_t e1 = a.list_start[x0 / 16 + 1];
-      for (uint32_t e0 = a.list_start[x0 / 16]; e0 < e1; e0 += 4) {   // four places a step
+    if (x0 < a.nx) {
+      const uint32_t first = a.list_start[x0 / 16], places = a.list_start[x0 / 16 + 1] - first;
+      const uint32_t e1 = first + share_of(places, split + 1, splits);
+      for (uint32_t e0 = first + share_of(places, split, splits); e0 < e1; e0 += 4) {   // four places a step
         const uint2 en = a.list[min(e0 + g, e1 - 1)];
         const bool mine = e0 + g < e1 && (int)(en.x >> kRowBits) == col;
         const float B = mine ? __uint_as_float(en.y) : 0.f;
@@ -1146,8 +1163,8 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_table_kernel(const int*
   }
 }
 
-// A place's weight as the columns pass takes it: fp32, or two bf16 that add
-// up to it.
+// A place's weight as the columns pass takes it: fp32, or (bf16, many rows)
+// two bf16 that add up to it.
 __device__ __forceinline__ uint32_t place_weight(float w, bool pairs) {
   if (!pairs) return __float_as_uint(w);
   const uint16_t hi = f32_to_bf16(w);
@@ -1355,7 +1372,7 @@ hipError_t go_bf16(const StreamArgs& a, hipStream_t s) {
 template <int RP>
 hipError_t go_few(const StreamArgs& a, hipStream_t s) {
   const auto go = [&](auto kernel, int rows) -> hipError_t {
-    const int bytes = (rows * RP + kWaves * 32 * 32) * 2 + kNear * 8;
+    const int bytes = (rows * RP + kWaves * 32 * 32) * 2;
     if (bytes > 65536) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1500,7 +1517,7 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   hipLaunchKernelGGL(distill_table_kernel, dim3((unsigned)(row_blocks * ceil_div(words, kTableWords * kWaves))),
                      dim3(kWaves * kWave), 0, s, srt_id, (int)d.N, (int)p.npad, d.k, p.GC, words, row_blocks, table);
   hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(kListWaves * kWave), 0, s, table, srt_id,
-                     srt_w, (int)p.npad, d.k, p.GC, d.dtype == 0, start, list);
+                     srt_w, (int)p.npad, d.k, p.GC, d.dtype == 0 && !p.few, start, list);
   StreamArgs a{};
   a.X = d.P;
   a.nx = d.V;
