@@ -85,6 +85,10 @@ struct StreamArgs {
   int row_block;        // RB
   const uint32_t* list_start;   // [groups + 1]: the teacher places of a group of columns in `list`
   const uint2* list;    // (row | local column << kRowBits, -w p / T), by row within a group
+  int64_t groups;
+  int chunk_bits;       // log2 of the places of a chunk of the list
+  const uint32_t* chunk_in;     // [chunk] c0 | c1 << 16 of the group that it lies in, 0 if it is not in one
+  float* chunk_part;    // [chunk] its results, in the order of the accumulators
   void* dP;             // V x r, from whole blocks
   float* part;          // [share][row of X past the whole blocks'][RP], from the others
 };
@@ -275,6 +279,131 @@ __device__ __forceinline__ f32x4 quad(const f32x16& v, int g) {
 // and 334 us with one tile and two waves, 377 and 411 us with two and one.
 constexpr int x_tiles(int RP) { return RP <= 64 ? 2 : 1; }
 
+// A column group's teacher places, from e0 to e1 of the list. Whole chunks of
+// the list (chunks c0 to c1) are summed by other blocks before the columns
+// pass, so that a group that many rows name (a frequent token) does not hold
+// one block up; the rest, before and behind them, are the group's own. (The
+// gradient call of 4096 rows, r = 128, k = 32, without and with chunks: all
+// places below 32 of the 151936 tokens 4937 and 621 us, below 1000 791 and
+// 389, uniform 350 and 332.)
+// A group adds as many results of blocks of its chunks, at most:
+constexpr int most_parts(int RP) { return RP <= 256 ? 64 : 16; }
+struct Listed {
+  uint32_t e0, head, tail, e1;   // own places: from e0 on, `head` of them; from `tail` to e1
+  int c0, c1;
+  __device__ __forceinline__ Listed(uint32_t first, uint32_t end, int bits) : e0(first), e1(end) {
+    c0 = (int)((first + (1u << bits) - 1) >> bits);
+    c1 = (int)(end >> bits);
+    if (c0 < c1) {
+      head = ((uint32_t)c0 << bits) - first;
+      tail = (uint32_t)c1 << bits;
+    } else {
+      c1 = c0;
+      head = end - first;
+      tail = end;
+    }
+  }
+  __device__ __forceinline__ uint32_t count() const { return head + (e1 - tail); }
+  __device__ __forceinline__ uint32_t at(uint32_t i) const { return i < head ? e0 + i : tail + (i - head); }
+};
+
+// f(accumulator, quad, where it is among the chunks' results) for all of a wave's.
+template <int RP, int XT, typename F>
+__device__ __forceinline__ void each_quad(int chunk, int wave, f32x16 (&acc)[XT][RP / 32], F&& f) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+    for (int rt = 0; rt < RP / 32; ++rt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        f(acc[xt][rt], g, (((((int64_t)chunk * kWaves + wave) * XT + xt) * (RP / 32) + rt) * 4 + g) * (kWave * 4) + lane * 4);
+}
+
+// Adds the teacher's part of a block's columns, -w p / T z_n for places i0 to
+// i1 (place i is a.list[where(i)]): the places' rows of Z are gathered into
+// the tiles' LDS and go through the product of the dense part, with the places'
+// weights as the right operand, each the sum of two bf16 (within 2^-17 of
+// it; in one word).
+template <int RP, int XT, int WX, typename At>
+__device__ __forceinline__ void add_places(const StreamArgs& a, uint16_t* lds, const Places<RP>& at, uint32_t i0,
+                                           uint32_t i1, At&& where, f32x16 (&acc)[XT][RP / 32]) {
+  constexpr int TY = bf16_tile_rows<RP, WX>(), RT = RP / 32;
+  constexpr int kLoads = TileCopy<RP, TY>::kLoads;
+  const int lane = threadIdx.x & 63, h = lane >> 5, wave = wave_id(), wx = wave % WX;
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
+  const auto gather = [&](int buf, uint32_t base) {   // returns the lane's place (of TY)
+    const uint32_t i = base + lane % TY;
+    const uint2 en = i < i1 ? a.list[where(i)] : uint2{0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int p = (j * kWaves + wave) * kWave + lane;
+      const int row = p / (RP / 8), c = (p % (RP / 8)) ^ swz_row<RP>(row);
+      const uint32_t n = (uint32_t)__shfl((int)en.x, row) & kRowMask;
+      const uint32_t off = base + row < i1 ? n * (uint32_t)(RP * 2) + (uint32_t)c * 16u : 0xfffffff0u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(lds + buf * TY * RP + (j * kWaves + wave) * kWave * 8),
+                                               16, (int)off, 0, 0, 0);
+    }
+    return en;
+  };
+  uint2 en = gather(0, i0);
+  for (int buf = 0; i0 < i1; i0 += TY, buf ^= 1) {
+    __builtin_amdgcn_s_waitcnt(0xF70);
+    __syncthreads();
+    uint2 next = {0u, 0u};
+    if (i0 + TY < i1) next = gather(buf ^ 1, i0 + TY);
+    const uint16_t* tile = lds + buf * TY * RP;
+#pragma unroll 1
+    for (int s = 0; s < TY / 16; ++s) {
+      if (i0 + s * 16 >= i1) break;
+      bf16x8 hi[XT], lo[XT];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int y = s * 16 + (k >> 2) * 8 + h * 4 + (k & 3);
+        const int col = (int)((uint32_t)__shfl((int)en.x, y) >> kRowBits) - wx * (32 * XT);
+        const uint32_t w = (uint32_t)__shfl((int)en.y, y);
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+          const uint32_t v = col == xt * 32 + (lane & 31) ? w : 0u;
+          hi[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)v);
+          lo[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)(v >> 16));
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const bf16x8 A = columns<RP>(tile + s * 16 * RP, at, rt);
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+          acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi[xt], acc[xt][rt], 0, 0, 0);
+          acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[xt], acc[xt][rt], 0, 0, 0);
+        }
+      }
+    }
+    en = next;
+  }
+}
+
+// The teacher's part of a share of a group's whole chunks; of a group's chunks'
+// blocks, the first most_parts have a share.
+template <int RP, int XT>
+__global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) chunk_kernel(StreamArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  const uint32_t c = blockIdx.x;
+  if (c << a.chunk_bits >= a.list_start[a.groups]) return;
+  const uint32_t in = a.chunk_in[c];
+  const uint32_t c0 = in & 0xffff, all = (in >> 16) - c0, j = c - c0, parts = min(all, (uint32_t)most_parts(RP));
+  if (!in || j >= parts) return;
+  Places<RP> at;
+  at.init();
+  f32x16 acc[XT][RP / 32] = {};
+  add_places<RP, XT, kWaves>(a, lds, at, (c0 + share_of(all, j, parts)) << a.chunk_bits,
+                             (c0 + share_of(all, j + 1, parts)) << a.chunk_bits, [](uint32_t i) { return i; }, acc);
+  each_quad<RP, XT>((int)c, wave_id(), acc, [&](f32x16& v, int g, int64_t to) {
+    *reinterpret_cast<f32x4*>(a.chunk_part + to) = quad(v, g);
+  });
+}
+
 // bf16. RP: r rounded up to a tile size; a wave owns XT * 32 rows of X, WX of
 // the block's four waves sit side by side on X and 4 / WX share out a
 // tile's rows of Y.
@@ -316,65 +445,10 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
     }
   };
   if constexpr (COLS) {
-    const uint32_t e_first = a.list_start[xtile], places = a.list_start[xtile + 1] - e_first;
-    const uint32_t e_end = e_first + share_of(places, split + 1, splits);
-    uint32_t e = e_first + share_of(places, split, splits);
-    if (e < e_end) {
-      // First the teacher's part of the block's columns, -w p / T z_n for every
-      // place: the places' rows of Z are gathered into the tiles' LDS and go
-      // through the same product, with the places' weights as the right
-      // operand, each the sum of two bf16 (within 2^-17 of it; in one word).
-      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<void*>(a.Y), (short)0, (int)((uint32_t)a.ny * (uint32_t)(RP * 2)), kRawBufferFlags);
-      const auto gather = [&](int buf, uint32_t e0) {   // returns the lane's place (of TY)
-        const uint32_t i = e0 + lane % TY;
-        const uint2 en = i < e_end ? a.list[i] : uint2{0u, 0u};
-#pragma unroll
-        for (int j = 0; j < copy.kLoads; ++j) {
-          const int p = (j * kWaves + wave) * kWave + lane;
-          const int row = p / (RP / 8), c = (p % (RP / 8)) ^ swz_row<RP>(row);
-          const uint32_t n = (uint32_t)__shfl((int)en.x, row) & kRowMask;
-          const uint32_t off = e0 + row < e_end ? n * (uint32_t)(RP * 2) + (uint32_t)c * 16u : 0xfffffff0u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(lds + buf * TY * RP + (j * kWaves + wave) * kWave * 8),
-                                                   16, (int)off, 0, 0, 0);
-        }
-        return en;
-      };
-      uint2 en = gather(0, e);
-      for (int buf = 0; e < e_end; e += TY, buf ^= 1) {
-        __builtin_amdgcn_s_waitcnt(0xF70);
-        __syncthreads();
-        uint2 next = {0u, 0u};
-        if (e + TY < e_end) next = gather(buf ^ 1, e + TY);
-        const uint16_t* tile = lds + buf * TY * RP;
-#pragma unroll 1
-        for (int s = 0; s < TY / 16; ++s) {
-          if (e + s * 16 >= e_end) break;
-          bf16x8 hi[XT], lo[XT];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int y = s * 16 + (k >> 2) * 8 + h * 4 + (k & 3);
-            const int col = (int)((uint32_t)__shfl((int)en.x, y) >> kRowBits) - wx * (32 * XT);
-            const uint32_t w = (uint32_t)__shfl((int)en.y, y);
-#pragma unroll
-            for (int xt = 0; xt < XT; ++xt) {
-              const uint32_t v = col == xt * 32 + (lane & 31) ? w : 0u;
-              hi[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)v);
-              lo[xt][k] = __builtin_bit_cast(__bf16, (uint16_t)(v >> 16));
-            }
-          }
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const bf16x8 A = columns<RP>(tile + s * 16 * RP, at, rt);
-#pragma unroll
-            for (int xt = 0; xt < XT; ++xt) {
-              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, hi[xt], acc[xt][rt], 0, 0, 0);
-              acc[xt][rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A, lo[xt], acc[xt][rt], 0, 0, 0);
-            }
-          }
-        }
-        en = next;
-      }
+    const Listed all(a.list_start[xtile], a.list_start[xtile + 1], a.chunk_bits);
+    const uint32_t i0 = share_of(all.count(), split, splits), i1 = share_of(all.count(), split + 1, splits);
+    if (i0 < i1) {
+      add_places<RP, XT, WX>(a, lds, at, i0, i1, [&](uint32_t i) { return all.at(i); }, acc);
       __syncthreads();   // the tiles may be filled again
     }
   }
@@ -574,6 +648,15 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
   constexpr int kOut2 = kFit >= RP * 2 ? RP : kFit >= RP ? RP / 2 : RP / 4;
   constexpr int kOut4 = kFit >= RP * 4 ? RP : kFit >= RP * 2 ? RP / 2 : RP / 4;
   if constexpr (COLS) {
+    // The group's chunks (here and not before the dense part, where X needs the registers).
+    const Listed all(a.list_start[xtile], a.list_start[xtile + 1], a.chunk_bits);
+    const uint32_t parts = min(all.c1 - all.c0, most_parts(RP));
+    for (uint32_t c = share_of(parts, split, splits); c < share_of(parts, split + 1, splits); ++c)
+      each_quad<RP, XT>(all.c0 + (int)c, wave, acc, [&](f32x16& v, int g, int64_t at) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(a.chunk_part + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[g * 4 + i] += q[i];
+      });
 #pragma unroll
     for (int xt = 0; xt < XT; ++xt) {
       const int64_t x = x0 + xt * 32;
@@ -1177,7 +1260,8 @@ __device__ __forceinline__ uint32_t place_weight(float w, bool pairs) {
 constexpr int kListWaves = 8, kListRows = kListWaves * kWave * 8;
 __global__ void __launch_bounds__(kListWaves* kWave) distill_list_kernel(
     const uint32_t* __restrict__ table, const int* __restrict__ srt_id, const float* __restrict__ srt_w, int npad,
-    int k, int GC, bool pairs, uint32_t* __restrict__ start, uint2* __restrict__ list) {
+    int k, int GC, bool pairs, int bits, uint32_t chunks, uint32_t* __restrict__ start,
+    uint2* __restrict__ list, uint32_t* __restrict__ chunk_in) {
   __shared__ uint32_t below[kListWaves], scan[kListWaves];
   const int64_t g = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -1197,6 +1281,7 @@ __global__ void __launch_bounds__(kListWaves* kWave) distill_list_kernel(
   at = 0;
 #pragma unroll
   for (int w = 0; w < kListWaves; ++w) at += below[w];
+  const uint32_t begin = at;
   if (threadIdx.x == 0) start[g] = at;
   for (int n0 = 0; n0 < npad; n0 += kListRows) {
     const int n = n0 + threadIdx.x * 8;
@@ -1240,13 +1325,26 @@ __global__ void __launch_bounds__(kListWaves* kWave) distill_list_kernel(
     for (int q = 0; q < 8; ++q) {
       if (first[q] < last[q])
         list[o++] = uint2{(uint32_t)(n + q) | (uint32_t)(id[q] - g * GC) << kRowBits, place_weight(-wt[q], pairs)};
-      for (uint32_t j = first[q] + 1; j < last[q]; ++j) {
-        const int64_t i = (int64_t)(n + q) * k + j;
-        list[o++] = uint2{(uint32_t)(n + q) | (uint32_t)(srt_id[i] - g * GC) << kRowBits,
-                          place_weight(-srt_w[i], pairs)};
+      for (uint32_t j = first[q] + 1; j < last[q]; j += 2) {   // two at a time
+        int jd[2];
+        float jw[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int64_t i = (int64_t)(n + q) * k + min(j + u, last[q] - 1);
+          jd[u] = srt_id[i];
+          jw[u] = srt_w[i];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (j + u < last[q])
+            list[o++] = uint2{(uint32_t)(n + q) | (uint32_t)(jd[u] - g * GC) << kRowBits, place_weight(-jw[u], pairs)};
       }
     }
   }
+  // the chunks that begin here: `at` is the list's end by now
+  for (uint32_t c = ((begin + (1u << bits) - 1) >> bits) + threadIdx.x; c < chunks && c << bits < at;
+       c += kListWaves * kWave)
+    chunk_in[c] = (c + 1) << bits <= at ? (begin + (1u << bits) - 1) >> bits | (at >> bits) << 16 : 0u;
   if (g == (int64_t)gridDim.x - 1 && threadIdx.x == 0) start[g + 1] = at;
 }
 
@@ -1291,9 +1389,11 @@ struct Plan {
   int64_t split_rows;   // their rows of P
   int RB;            // rows of a tile of the columns pass
   int64_t npad;
+  int chunk_bits;    // log2 of the places of a chunk of the list
+  int64_t chunks;    // whole ones, at most
   // workspace offsets
   size_t pm, pl, po, fwd_total;
-  size_t zc, row_c, srt_id, srt_w, table, start, list, part, bwd_total;
+  size_t zc, row_c, srt_id, srt_w, table, start, list, part, chunk_in, chunk_part, bwd_total;
 };
 
 Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
@@ -1332,6 +1432,11 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   if (p.col_splits == 1) p.col_whole = cblocks;
   p.split_rows = V - std::min(V, p.col_whole * (dtype == 0 ? p.GC : 64));
   p.npad = ceil_div(N, 64) * 64;
+  // A chunk takes about as long as four tiles of the dense part; there are at
+  // most 512.
+  p.chunk_bits = 8;
+  while (N * k >> p.chunk_bits > 512) ++p.chunk_bits;
+  p.chunks = dtype == 0 && !p.few ? N * k >> p.chunk_bits : 0;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1351,6 +1456,8 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   p.start = take(size_t(p.groups + 1) * 4);
   p.list = take(size_t(N) * k * 8);
   p.part = take(p.col_splits > 1 ? size_t(p.col_splits) * p.split_rows * p.RP * 4 : 0);
+  p.chunk_in = take(size_t(p.chunks) * 4);
+  p.chunk_part = take(size_t(p.chunks) * p.GC * p.RP * 4);
   p.bwd_total = o;
   return p;
 }
@@ -1432,6 +1539,28 @@ hipError_t stream(int dtype, const Plan& p, const StreamArgs& a, hipStream_t s) 
     default: hipLaunchKernelGGL((stream_f32_kernel<512, ACC, COLS>), grid, block, 0, s, a); break;
   }
   return hipGetLastError();
+}
+
+template <int RP>
+hipError_t go_chunks(const Plan& p, const StreamArgs& a, hipStream_t s) {
+  const auto kernel = chunk_kernel<RP, x_tiles(RP)>;
+  constexpr int bytes = bf16_lds_bytes<RP, kWaves>();
+  if constexpr (bytes > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)p.chunks), dim3(kWaves * kWave), bytes, s, a);
+  return hipGetLastError();
+}
+hipError_t chunks(const Plan& p, const StreamArgs& a, hipStream_t s) {
+  switch (p.RP) {
+    case 32: return go_chunks<32>(p, a, s);
+    case 64: return go_chunks<64>(p, a, s);
+    case 128: return go_chunks<128>(p, a, s);
+    case 256: return go_chunks<256>(p, a, s);
+    default: return go_chunks<512>(p, a, s);
+  }
 }
 
 template <typename T, int L>
@@ -1517,7 +1646,8 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   hipLaunchKernelGGL(distill_table_kernel, dim3((unsigned)(row_blocks * ceil_div(words, kTableWords * kWaves))),
                      dim3(kWaves * kWave), 0, s, srt_id, (int)d.N, (int)p.npad, d.k, p.GC, words, row_blocks, table);
   hipLaunchKernelGGL(distill_list_kernel, dim3((unsigned)p.groups), dim3(kListWaves * kWave), 0, s, table, srt_id,
-                     srt_w, (int)p.npad, d.k, p.GC, d.dtype == 0 && !p.few, start, list);
+                     srt_w, (int)p.npad, d.k, p.GC, d.dtype == 0 && !p.few, p.chunk_bits, (uint32_t)p.chunks, start, list,
+                     reinterpret_cast<uint32_t*>(ws + p.chunk_in));
   StreamArgs a{};
   a.X = d.P;
   a.nx = d.V;
@@ -1534,6 +1664,14 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   a.list = list;
   a.dP = d.dP;
   a.part = reinterpret_cast<float*>(ws + p.part);
+  a.groups = p.groups;
+  a.chunk_bits = p.chunk_bits;
+  a.chunk_in = reinterpret_cast<const uint32_t*>(ws + p.chunk_in);
+  a.chunk_part = reinterpret_cast<float*>(ws + p.chunk_part);
+  if (p.chunks) {
+    e = chunks(p, a, s);
+    if (e != hipSuccess) return e;
+  }
   e = stream<true, true>(d.dtype, p, a, s);
   if (e != hipSuccess) return e;
   if (p.col_splits > 1) {   // at most 512 blocks of rows: the index fits 32 bits

@@ -317,6 +317,20 @@ def test_autograd_gives_the_calls_gradients():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt,N,r,k", [
+    ("bf16", 700, 32, 64), ("bf16", 700, 64, 64), ("bf16", 701, 128, 64), ("bf16", 300, 256, 63), ("bf16", 200, 512, 64),
+    ("bf16", 64, 128, 64), ("bf16", 33, 512, 64), ("fp32", 150, 40, 64),
+])
+@pytest.mark.parametrize("span", [1, 20, 400])
+def test_frequent_tokens(dt, N, r, k, span):
+    """Most rows name the same few tokens (with span 1, the same one k times over)."""
+    Z, P, idx, t, w = inputs(N, 1500, r, k, dt, seed=N + span)
+    idx = 100 + idx % span
+    idx[:, -1] = torch.arange(N, dtype=torch.int32, device=DEV) % 1500
+    check(Z, P, idx.contiguous(), t, w, 1.0, dt)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_micro_batches_of_odd_sizes(dt):
     """Views that start off 16 bytes, forward and backward: the rows' own
