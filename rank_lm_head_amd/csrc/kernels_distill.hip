@@ -854,7 +854,8 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) few_columns_kernel(StreamArg
 template <int RP, bool ACC, bool COLS>
 __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs a) {
   constexpr int TY = 16, LD = RP + 4, KC = RP / 16, RT = RP / 16;
-  __shared__ __attribute__((aligned(16))) float tile[TY * LD];
+  constexpr int kBufs = RP <= 256 ? 2 : 1;   // as many as fit 64 KB
+  __shared__ __attribute__((aligned(16))) float tiles[kBufs][TY * LD];
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15, wave = wave_id();
   const bool whole = blockIdx.x < a.whole;
   const int splits = whole ? 1 : a.splits;
@@ -876,20 +877,30 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
 
   const int64_t nt = (a.ny + TY - 1) / TY;
   const int64_t t_begin = nt * split / splits, t_end = nt * (split + 1) / splits;
-  for (int64_t t = t_begin; t < t_end; ++t) {
-    __syncthreads();
+  constexpr int kLoads = (TY * RP / 4 + kWaves * kWave - 1) / (kWaves * kWave);
+  f32x4 next[kLoads];   // the next tile, on its way during a tile's products
+  const auto load = [&](int64_t t) {
 #pragma unroll
-    for (int i = 0; i < TY * RP / 4; i += kWaves * kWave) {
-      const int p = i + threadIdx.x;
+    for (int i = 0; i < kLoads; ++i) {
+      const int p = i * kWaves * kWave + threadIdx.x;
       const int row = p / (RP / 4), c = (p % (RP / 4)) * 4;
       const int64_t y = t * TY + row;
-      if (p < TY * RP / 4) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (y < a.ny && c < a.r) v = *reinterpret_cast<const f32x4*>(Yp + y * a.ldy + c);
-        *reinterpret_cast<f32x4*>(tile + row * LD + c) = v;
-      }
+      next[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (row < TY && y < a.ny && c < a.r) next[i] = *reinterpret_cast<const f32x4*>(Yp + y * a.ldy + c);
     }
-    __syncthreads();
+  };
+  if (t_begin < t_end) load(t_begin);
+  for (int64_t t = t_begin; t < t_end; ++t) {
+    float* const tile = tiles[t % kBufs];
+    if constexpr (kBufs == 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int p = i * kWaves * kWave + threadIdx.x;
+      const int row = p / (RP / 4), c = (p % (RP / 4)) * 4;
+      if (row < TY) *reinterpret_cast<f32x4*>(tile + row * LD + c) = next[i];
+    }
+    __syncthreads();   // also: every wave is done with the tile before this one
+    if (t + 1 < t_end) load(t + 1);
     const int64_t y0 = t * TY;
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -938,15 +949,32 @@ __global__ void __launch_bounds__(kWaves* kWave, 1) stream_f32_kernel(StreamArgs
     if (x0 < a.nx) {
       const uint32_t first = a.list_start[x0 / 16], places = a.list_start[x0 / 16 + 1] - first;
       const uint32_t e1 = first + share_of(places, split + 1, splits);
-      for (uint32_t e0 = first + share_of(places, split, splits); e0 < e1; e0 += 4) {   // four places a step
-        const uint2 en = a.list[min(e0 + g, e1 - 1)];
-        const bool mine = e0 + g < e1 && (int)(en.x >> kRowBits) == col;
-        const float B = mine ? __uint_as_float(en.y) : 0.f;
-        const float* z = Yp + (int64_t)(en.x & kRowMask) * a.ldy;
+      uint32_t e0 = first + share_of(places, split, splits);
+      // Sixteen places a step, four to a product; the next step's are on their way.
+      uint2 en[4] = {};
+      const auto take = [&] {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) en[u] = a.list[min(e0 + u * 4 + g, e1 - 1)];
+      };
+      if (e0 < e1) take();
+      while (e0 < e1) {
+        float B[4];
+        const float* z[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bool mine = e0 + u * 4 + g < e1 && (int)(en[u].x >> kRowBits) == col;
+          B[u] = mine ? __uint_as_float(en[u].y) : 0.f;
+          z[u] = Yp + (int64_t)(en[u].x & kRowMask) * a.ldy + col;
+        }
+        e0 += 16;
+        if (e0 < e1) take();
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const int c = rt * 16 + col;
-          acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(z[c], B, acc[rt], 0, 0, 0);
+          float A[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) A[u] = z[u][rt * 16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[u], B[u], acc[rt], 0, 0, 0);
         }
       }
     }
