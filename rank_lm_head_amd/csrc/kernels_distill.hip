@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
 // flight rather than for reuse. All rows of Z sit in LDS and all weights of a
 // wave's 32 columns in registers; dP then takes shape 32 columns of r at a
 // time, which leaves room for a second block (r = 512: one block and 256
-// accumulators in the general kernel; 64 rows, 151936 tokens: 173 -> 78 us).
+// accumulators in the general kernel; 64 rows, 151936 tokens: 173 -> 71 us).
 // The teacher's weights are scattered into a table of the wave's columns by
 // 16 rows, and join q's in fp32; a wave with any of them takes its weights as
 // two bf16 (hi + lo, within 2^-17 of their sum), others as one.
@@ -1452,16 +1452,19 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
   // rows of Z between them, down to about two tiles a share. (At 4096 rows,
   // r = 128, 1187 blocks of which 512 run at a time: 333 us with the last 163
   // in three shares and 7 for joining them, 345 without.)
+  // In fp32 four blocks fit a compute unit up to r = 128 (2000 rows, 20000
+  // tokens, r = 64: 313 blocks, 229 us whole and 126 + 5 in three shares).
   const int64_t ntiles = ceil_div(N, p.RB);
-  p.col_whole = cblocks / slots * slots;
+  const int64_t col_slots = dtype != 0 && p.RP <= 128 ? 2 * slots : slots;
+  p.col_whole = cblocks / col_slots * col_slots;
   const int64_t rest = cblocks - p.col_whole;
-  p.col_splits = rest ? (int)std::max<int64_t>(1, std::min<int64_t>(slots / rest, ntiles / 2)) : 1;
+  p.col_splits = rest ? (int)std::max<int64_t>(1, std::min<int64_t>(col_slots / rest, ntiles / 2)) : 1;
   if (p.few) p.col_splits = 1;
   if (p.col_splits == 1) p.col_whole = cblocks;
   p.split_rows = V - std::min(V, p.col_whole * (dtype == 0 ? p.GC : 64));
   p.npad = ceil_div(N, 64) * 64;
-  // A chunk takes about as long as four tiles of the dense part; there are at
-  // most 512.
+  // A chunk of 256 takes 10 us at r = 128 (1024: 40 us, longer than the columns
+  // pass gains by it at 4096 rows); there are at most 512.
   p.chunk_bits = 8;
   while (N * k >> p.chunk_bits > 512) ++p.chunk_bits;
   p.chunks = dtype == 0 && !p.few ? N * k >> p.chunk_bits : 0;
@@ -1702,7 +1705,7 @@ hipError_t launch_distill_grad(const DistillArgs& d, void* workspace, hipStream_
   }
   e = stream<true, true>(d.dtype, p, a, s);
   if (e != hipSuccess) return e;
-  if (p.col_splits > 1) {   // at most 512 blocks of rows: the index fits 32 bits
+  if (p.col_splits > 1) {   // at most 1024 blocks of rows (fp32, 64 rows each): the index fits 32 bits
     const dim3 grid((unsigned)ceil_div(p.split_rows * p.RP, 1024));
     const int64_t first = (d.V - p.split_rows) * d.r;
     if (d.dtype == 0)
