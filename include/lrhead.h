@@ -232,9 +232,12 @@ int lrhead_factor(const void* W, int64_t V, int64_t d, int r, int q,
  * A place whose id lies outside [0, V), or whose logit is NaN or -inf, is
  * empty; a row of empty places has loss 0 and gradient 0. An id that occurs
  * twice in a row counts twice. Ids need no order. The scores are never
- * stored; they, the sums and the statistics are fp32 (bf16: the weights q
- * of the gradients are rounded to bf16, products and sums are fp32). With
- * grad == NULL the call computes loss and lse alone, at half the work.
+ * stored; they, the sums and the statistics are fp32. (bf16: in the
+ * gradients q[v] is rounded to bf16 where v is no place of the row's teacher,
+ * off by 2^-8 of itself at most; at the places q - p is formed from an
+ * unrounded q, so that it keeps its digits when the two are close. Products
+ * and sums are fp32.) With grad == NULL the call computes loss and lse alone,
+ * at half the work.
  * loss, lse: N fp32; grad: N x r fp32. T = temperature > 0.
  *
  * lrhead_distill_grad: with the rows' weights w (N fp32: the gradient that

@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(kWaves* kWave, RP == 512 ? 1 : 2) stream_bf16_
       }
       if constexpr (ACC) {
         // E as the right operand. It is rounded to bf16 here (off by at most
-        // 2^-8 of itself, nearest even); products and sums stay in fp32.
+        // 2^-8 of itself, nearest even; q_lost makes it good where a
+        // teacher's p is taken from it); products and sums stay in fp32.
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
           bf16x8 E[XT];
@@ -1009,14 +1010,57 @@ template <typename T> __device__ __forceinline__ float widen(T x);
 template <> __device__ __forceinline__ float widen<uint16_t>(uint16_t x) { return bf16_to_f32(x); }
 template <> __device__ __forceinline__ float widen<float>(float x) { return x; }
 
-__device__ __forceinline__ float dot8(const uint16_t* a, const uint16_t* b, float acc) {
-  return dot8_bf16(load16(a), load16(b), acc);
-}
 __device__ __forceinline__ float dot8(const float* a, const float* b, float acc) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc = fmaf(a[i], b[i], acc);
   return acc;
 }
+
+// The scores of up to 32 TILES places against the row z, bit for bit as the
+// streaming passes make them: the same instruction over the same 16 columns
+// at a time. (An element of its result depends on its own row and column alone,
+// wherever they sit and whichever operand they are.) Lanes l and l + 32 give the ids
+// of places l, l + 32, .. (INT_MAX: none, score 0); place l + 32 t's score
+// is got[t] of lane l. The whole wave takes part, but z is read once only, as the
+// one row of the left operand.
+template <int TILES, int kAhead>
+__device__ __forceinline__ void place_scores(const uint16_t* __restrict__ P, const uint16_t* __restrict__ z, int r,
+                                             const int (&id)[TILES], float (&got)[TILES]) {
+  const int h = (threadIdx.x & 63) >> 5, x = threadIdx.x & 31;
+  f32x16 S[TILES];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) S[t] = f32x16{};
+  for (int c0 = 0; c0 < r; c0 += kAhead * 16) {
+    u32x4 A[kAhead], B[TILES][kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = c0 + i * 16 + h * 8;
+      A[i] = u32x4{0u, 0u, 0u, 0u};
+      if (x == 0 && c < r) A[i] = load16(z + c);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        B[t][i] = u32x4{0u, 0u, 0u, 0u};
+        if (c < r && id[t] != INT_MAX) B[t][i] = load16(P + (int64_t)id[t] * r + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+        S[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, A[i]),
+                                                       __builtin_bit_cast(bf16x8, B[t][i]), S[t], 0, 0, 0);
+  }
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) got[t] = S[t][0];
+}
+
+// What the rounding of a weight q to bf16 takes away from it (exact in fp32).
+// The gradients are sums of q - p. Away from the teacher's places the rounding is
+// 2^-8 of a term at most; at them it would be 2^-8 of q, however small q - p is
+// (a student that agrees with its teacher, q = 0.7 and losses of 0.001: dP and dZ
+// off by 13 and 16% in norm). So the places' weights are p - q_lost: N k scores
+// made once more, and what the streams add up to is q - p in fp32.
+__device__ __forceinline__ float q_lost(float q) { return q - __uint_as_float(pack_bf16(q, 0.f) << 16); }
 
 // The teacher's distribution over a row's places, lane j holding place j's id
 // (any, outside [0, V) past k) and logit / T: a place is empty (p = 0, id =
@@ -1044,17 +1088,18 @@ __device__ __forceinline__ bool teacher(int64_t V, int& id, float x, float& p, f
 // shares of the weighted sum and the teacher's places. The first block of a
 // row also writes its lse and loss. What bounds it is the chain of dependent
 // loads (shares' maxima, ids, the ids' rows), so a row gets as few blocks as
-// its columns allow, and the sums are on their way before their weights are
-// made (4096 rows, r = 128, 16 shares: 31 us with two blocks a row, 24 with
-// one; 2048 rows, r = 256: 49 us with four, 40 with one).
+// its columns allow (49 us with four blocks a row at 2048 rows, r = 256, 40 with
+// one), the first sums are on their way before their weights are made, and the
+// registers leave room for five blocks a compute unit (4096 rows, r = 128, 16 shares:
+// 35 us with four, 30 with five; the scores made again are 10 of them).
 template <typename T, int L>
-__global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
+__global__ void __launch_bounds__(kWaves* kWave, sizeof(T) == 2 ? 5 : 3) distill_finish_kernel(
     const T* __restrict__ Z, const T* __restrict__ P, const int32_t* __restrict__ idx, const float* __restrict__ t,
-    int64_t N, int64_t V, int r, int RP, int k, float inv_t, int shares, const float* __restrict__ pm,
-    const float* __restrict__ pl, const float* __restrict__ po, float* __restrict__ loss, float* __restrict__ lse,
-    float* __restrict__ G) {
-  __shared__ float sp[kWave], sdot[kWave], red[kWaves * 2], share_w[kMaxShares];
-  __shared__ int sid[kWave];
+    int64_t N, int64_t V, int r, int RP, int k, float inv_t, float scale, int ty_bits, int shares,
+    const float* __restrict__ pm, const float* __restrict__ pl, const float* __restrict__ po, float* __restrict__ loss,
+    float* __restrict__ lse, float* __restrict__ G) {
+  __shared__ float sp[kWave], sdot[kWave], lost[kWave], red[kWaves * 2], share_w[kMaxShares];
+  __shared__ __attribute__((aligned(16))) int sid[kWave];
   constexpr int kGroups = kWaves * kWave / L, kJoinCols = 4 * L;
   __shared__ f32x4 part[kGroups][L];
   const int chunks = G ? (r + kJoinCols - 1) / kJoinCols : 1;
@@ -1069,7 +1114,7 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   float m = neg_inf();
   for (int s = tid; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
   // the first shares' sums, on their way while their weights are made
-  constexpr int kAhead = 32 / kGroups;
+  constexpr int kAhead = 16 / kGroups;
   f32x4 early[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
@@ -1087,14 +1132,6 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   if (lane == 0) red[wave] = m;
   __syncthreads();
-  constexpr int kPlaces = kWave / kGroups;   // of a group: k <= 64
-  T places[kPlaces][4];
-#pragma unroll
-  for (int i = 0; i < kPlaces; ++i) {
-    const int v = sid[group + i * kGroups];
-    const T* q = P + (sums && v != INT_MAX ? (int64_t)v * r + c : 0);
-    __builtin_memcpy(places[i], __builtin_assume_aligned(q, 4 * sizeof(T)), 4 * sizeof(T));
-  }
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   float l = 0.f;
   for (int s = tid; s < shares; s += kWaves * kWave) {
@@ -1105,7 +1142,35 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
   }
   l = group_sum<kWave>(l);
   if (lane == 0) red[kWaves + wave] = l;
-  if (chunk == 0) {   // the places' scores: 16 lanes per place
+  if constexpr (sizeof(T) == 2) {   // the places' scores, and what their q have lost
+    if (wave < k) {   // of place 4 j + w in lane j of wave w
+      const int j = (lane & 15) * kWaves + wave;
+      const int v[1] = {(lane & 31) < 16 ? sid[j] : INT_MAX};
+      // the share that the id's tile belongs to, and its reference
+      const double tiles = (double)((V + (1 << ty_bits) - 1) >> ty_bits);
+      float ref = 0.f;
+      if (v[0] != INT_MAX) {
+        const int64_t share = (int64_t)((double)(((int64_t)(v[0] >> ty_bits) + 1) * shares - 1) / tiles);
+        ref = pm[share * N + n];
+      }
+      float s[1];
+      place_scores<1, 4>(P, Z + n * r, r, v, s);
+      // An id that occurred before: q is in the sum once. Lanes 16 apart look through 16 places each.
+      int again = 0;
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const u32x4 o = load16(sid + (lane & 48) + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) again |= (int)o[u] == sid[j] && (lane & 48) + i + u < j;
+      }
+      again |= __shfl_xor(again, 16);
+      again |= __shfl_xor(again, 32);
+      if (lane < 16) {
+        sdot[j] = s[0];
+        lost[j] = again ? 0.f : q_lost(exp2_hw(fmaf(s[0], scale, -ref))) * exp2_hw(ref - m);
+      }
+    }
+  } else if (chunk == 0) {   // the places' scores: 16 lanes per place
     for (int j = tid / 16; j < k; j += kWaves * 4) {
       const int v = sid[j];
       float d = 0.f;
@@ -1114,6 +1179,14 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
       d = group_sum<16>(d);
       if (tid % 16 == 0) sdot[j] = d;
     }
+  }
+  constexpr int kPlaces = kWave / kGroups;   // of a group: k <= 64
+  T places[kPlaces][4];
+#pragma unroll
+  for (int i = 0; i < kPlaces; ++i) {
+    const int v = sid[group + i * kGroups];
+    const T* q = P + (sums && v != INT_MAX ? (int64_t)v * r + c : 0);
+    __builtin_memcpy(places[i], __builtin_assume_aligned(q, 4 * sizeof(T)), 4 * sizeof(T));
   }
   __syncthreads();
   l = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
@@ -1149,8 +1222,9 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
     for (int i = 0; i < kPlaces; ++i) {
       const int j = group + i * kGroups;
       const bool real = sid[j] != INT_MAX;
+      const float w = sizeof(T) == 2 ? fmaf(lost[j], il, -sp[j]) : -sp[j];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = real ? fmaf(-sp[j], widen<T>(places[i][e]), o[e]) : o[e];
+      for (int e = 0; e < 4; ++e) o[e] = real ? fmaf(w, widen<T>(places[i][e]), o[e]) : o[e];
     }
   }
   part[group][sub] = o;
@@ -1167,13 +1241,14 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_finish_kernel(
 // Per row, before the columns pass: the exponent's offset and the sign of the
 // weight, the row of Z (zeros without weight, so that what a masked row holds,
 // NaN included, cannot reach dP), the places in ascending order of their ids
-// with w p / T, and dZ = w G. One wave per row, all its loads up front.
+// with w p / T (less what the columns pass rounds away of w q / T, if P is given),
+// and dZ = w G. One wave per row, all its loads but the places' rows up front.
 template <typename T>
 __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
-    const T* __restrict__ Z, const int32_t* __restrict__ idx, const float* __restrict__ t,
-    const float* __restrict__ lse, const float* __restrict__ G, const float* __restrict__ weight, int N, int64_t V,
-    int r, int RP, int k, float inv_t, T* __restrict__ zc, float* __restrict__ row_c, int RB,
-    int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
+    const T* __restrict__ Z, const T* __restrict__ P, float scale, const int32_t* __restrict__ idx,
+    const float* __restrict__ t, const float* __restrict__ lse, const float* __restrict__ G,
+    const float* __restrict__ weight, int N, int64_t V, int r, int RP, int k, float inv_t, T* __restrict__ zc,
+    float* __restrict__ row_c, int RB, int* __restrict__ srt_id, float* __restrict__ srt_w, T* __restrict__ dZ) {
   const int n = blockIdx.x * kWaves + wave_id();
   const int lane = threadIdx.x & 63;
   const int at = lane * 8;   // 8 columns a lane: r <= 512
@@ -1212,21 +1287,37 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     for (int i = 0; i < 8; ++i) z[i] = live ? z[i] : T(0);
     __builtin_memcpy(__builtin_assume_aligned(zc + (int64_t)n * RP + at, 16), z, sizeof(z));
   }
+  // |c| may be subnormal: log2 of 2^64 |c| is not
+  const float lc = log2_hw(fabsf(c) * 0x1p64f) - 64.f;
+  const float offset = live ? ls * kLog2e - lc : __builtin_inff();
   if (lane == 0) {
-    // |c| may be subnormal: log2 of 2^64 |c| is not
-    const float lc = log2_hw(fabsf(c) * 0x1p64f) - 64.f;
-    *row_c_at(row_c, n, RB) = live ? ls * kLog2e - lc : __builtin_inff();
+    *row_c_at(row_c, n, RB) = offset;
     *row_sign_at(row_c, n, RB) = live && c < 0.f ? 0x8000 : 0;
   }
+  const float wt = p * c;
   if (!live) id = INT_MAX;
+  float lost = 0.f;
+  if constexpr (sizeof(T) == 2) {
+    if (P && live) {
+      const int v[2] = {__shfl(id, lane & 31), __shfl(id, 32 + (lane & 31))};
+      float got[2] = {};
+      if (k > 32) place_scores<2, 4>(P, Z + (int64_t)n * r, r, v, got);
+      else place_scores<1, 8>(P, Z + (int64_t)n * r, r, {v[0]}, reinterpret_cast<float(&)[1]>(got));
+      const float behind = __shfl(got[1], lane & 31);
+      const float s = lane < 32 ? got[0] : behind;
+      lost = copysignf(1.f, c) * q_lost(exp2_hw(fmaf(s, scale, -offset)));
+    }
+  }
   int rank = 0;
+  bool again = false;   // an id that occurred before: q is in the sum once
   for (int j = 0; j < k; ++j) {
     const int o = __builtin_amdgcn_readlane(id, j);
     rank += o < id || (o == id && j < lane);
+    again |= o == id && j < lane;
   }
   if (lane < k) {
     srt_id[(int64_t)n * k + rank] = id;
-    srt_w[(int64_t)n * k + rank] = p * c;
+    srt_w[(int64_t)n * k + rank] = again ? wt : wt - lost;
   }
 }
 
@@ -1409,6 +1500,7 @@ struct Plan {
   int RP;
   bool few;          // the columns pass for few rows
   int XT, WX;        // rows pass
+  int TY;            // rows of P of a tile of the rows pass
   int row_splits;    // blocks along Y
   int GC;            // columns pass: columns of a group (bf16: a block, fp32: a wave)
   int64_t groups;
@@ -1433,16 +1525,17 @@ Plan plan(int dtype, int64_t V, int r, int64_t N, int k) {
     p.XT = x_tiles(p.RP);
     p.WX = N <= 32 * p.XT && p.RP < 256 ? 1 : N <= 64 * p.XT ? 2 : 4;
     xblocks = ceil_div(N, p.WX * 32 * p.XT);
-    ytiles = ceil_div(V, std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX)));
+    p.TY = std::max(p.RP <= 128 ? 64 : 32, 32 * (kWaves / p.WX));
     p.few = N <= 64;
     p.GC = kWaves * 32 * (p.few ? 1 : p.XT);
   } else {
     p.XT = 1;
     p.WX = 4;
     xblocks = ceil_div(N, 64);
-    ytiles = ceil_div(V, 16);
+    p.TY = 16;
     p.GC = 16;
   }
+  ytiles = ceil_div(V, p.TY);
   p.RB = dtype == 0 && p.RP > 128 ? 32 : 64;
   const int64_t slots = p.RP == 512 && dtype == 0 ? kTargetBlocks / 2 : kTargetBlocks;   // blocks at a time
   p.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / xblocks, ytiles, kMaxShares}));
@@ -1598,8 +1691,9 @@ template <typename T, int L>
 void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
   hipLaunchKernelGGL((distill_finish_kernel<T, L>), dim3((unsigned)(d.N * (d.G ? ceil_div(d.r, 4 * L) : 1))),
                      dim3(kWaves * kWave), 0, s, static_cast<const T*>(d.Z), static_cast<const T*>(d.P), d.idx, d.t,
-                     d.N, d.V, d.r, p.RP, d.k, d.inv_t, p.row_splits, reinterpret_cast<float*>(ws + p.pm),
-                     reinterpret_cast<float*>(ws + p.pl), reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
+                     d.N, d.V, d.r, p.RP, d.k, d.inv_t, d.scale, __builtin_ctz(p.TY), p.row_splits,
+                     reinterpret_cast<float*>(ws + p.pm), reinterpret_cast<float*>(ws + p.pl),
+                     reinterpret_cast<float*>(ws + p.po), d.loss, d.lse, d.G);
 }
 template <typename T>
 void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
@@ -1611,7 +1705,9 @@ void finish(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
 template <typename T>
 void prep(const Plan& p, const DistillArgs& d, char* ws, hipStream_t s) {
   hipLaunchKernelGGL(distill_prep_kernel<T>, dim3((unsigned)(p.npad / kWaves)), dim3(kWaves * kWave), 0, s,
-                     static_cast<const T*>(d.Z), d.idx, d.t, d.lse, d.G, d.weight, (int)d.N, d.V, d.r, p.RP, d.k, d.inv_t,
+                     static_cast<const T*>(d.Z),
+                     d.dtype == 0 && !p.few ? static_cast<const T*>(d.P) : nullptr, d.scale, d.idx, d.t, d.lse,
+                     d.G, d.weight, (int)d.N, d.V, d.r, p.RP, d.k, d.inv_t,
                      d.dP ? reinterpret_cast<T*>(ws + p.zc) : nullptr, reinterpret_cast<float*>(ws + p.row_c),
                      p.RB, reinterpret_cast<int*>(ws + p.srt_id),
                      reinterpret_cast<float*>(ws + p.srt_w), static_cast<T*>(d.dZ));
