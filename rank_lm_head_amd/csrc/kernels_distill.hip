@@ -1063,19 +1063,21 @@ __device__ __forceinline__ void place_scores(const uint16_t* __restrict__ P, con
 __device__ __forceinline__ float q_lost(float q) { return q - __uint_as_float(pack_bf16(q, 0.f) << 16); }
 
 // The teacher's distribution over a row's places, lane j holding place j's id
-// (any, outside [0, V) past k) and logit / T: a place is empty (p = 0, id =
+// (any, outside [0, V) past k) and logit: a place is empty (p = 0, id =
 // INT_MAX) when its id lies outside [0, V) or its logit is NaN or -inf. logp
 // is log p where p > 0. Returns whether the row has a place at all. The
+// largest logit is taken away before the division by T, whose result alone may
+// have no place in fp32 (T < 1, logits at the type's lowest value). The
 // exponent is taken in two parts: log2(e) rounded to fp32 alone would be off
 // by 1e-8 of it.
-__device__ __forceinline__ bool teacher(int64_t V, int& id, float x, float& p, float& logp) {
+__device__ __forceinline__ bool teacher(int64_t V, float inv_t, int& id, float x, float& p, float& logp) {
   const bool real = id >= 0 && id < V && x > neg_inf();
   const uint32_t mk = wave_max_u32(real ? order_key(x) : 0u);
   if (!real) id = INT_MAX;
   p = 0.f;
   logp = 0.f;
   if (!mk) return false;
-  const float d = x - __uint_as_float(order_key_inv(mk));
+  const float d = (x - __uint_as_float(order_key_inv(mk))) * inv_t;
   const float e = real ? exp2_hw(fmaf(d, kLog2e, d * kLog2eLo)) : 0.f;
   const float s = group_sum<kWave>(e);
   p = e / s;
@@ -1110,7 +1112,7 @@ __global__ void __launch_bounds__(kWaves* kWave, sizeof(T) == 2 ? 5 : 3) distill
   const int c = chunk * kJoinCols + sub * 4;
   const bool sums = G && c < r;
   int id = lane < k ? idx[n * k + lane] : -1;
-  const float tl = lane < k ? t[n * k + lane] * inv_t : 0.f;
+  const float tl = lane < k ? t[n * k + lane] : 0.f;
   float m = neg_inf();
   for (int s = tid; s < shares; s += kWaves * kWave) m = fmaxf(m, pm[(int64_t)s * N + n]);
   // the first shares' sums, on their way while their weights are made
@@ -1123,7 +1125,7 @@ __global__ void __launch_bounds__(kWaves* kWave, sizeof(T) == 2 ? 5 : 3) distill
     if (sums && s < shares) early[i] = *reinterpret_cast<const f32x4*>(po + ((int64_t)s * N + n) * RP + c);
   }
   float p, logp;
-  const bool any = teacher(V, id, tl, p, logp);   // every wave: the same values
+  const bool any = teacher(V, inv_t, id, tl, p, logp);   // every wave: the same values
   if (wave == 0) {
     sid[lane] = id;
     sp[lane] = p;
@@ -1261,7 +1263,7 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
   }
   const int64_t place = (int64_t)n * k + lane, elem = (int64_t)n * r + at;
   int id = lane < k ? idx[place] : -1;
-  const float tl = lane < k ? t[place] * inv_t : 0.f;
+  const float tl = lane < k ? t[place] : 0.f;
   const float w = weight ? weight[n] : 1.f;
   const float ls = lse[n];
   f32x4 g[2] = {};
@@ -1273,7 +1275,7 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
   if (zc && at < r) __builtin_memcpy(z, __builtin_assume_aligned(Z + elem, 16), sizeof(z));
 
   float p, logp;
-  const bool live = teacher(V, id, tl, p, logp) && w != 0.f;
+  const bool live = teacher(V, inv_t, id, tl, p, logp) && w != 0.f;
   const float c = w * inv_t;
   if (dZ && at < r) {
     T v[8];
