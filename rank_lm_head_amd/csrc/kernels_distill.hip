@@ -1289,8 +1289,9 @@ __global__ void __launch_bounds__(kWaves* kWave) distill_prep_kernel(
     for (int i = 0; i < 8; ++i) z[i] = live ? z[i] : T(0);
     __builtin_memcpy(__builtin_assume_aligned(zc + (int64_t)n * RP + at, 16), z, sizeof(z));
   }
-  // |c| may be subnormal: log2 of 2^64 |c| is not
-  const float lc = log2_hw(fabsf(c) * 0x1p64f) - 64.f;
+  // |c| may be subnormal: log2 of 2^64 |c| is not (and would not be finite for large ones)
+  const bool small = fabsf(c) < 0x1p-64f;
+  const float lc = log2_hw(small ? fabsf(c) * 0x1p64f : fabsf(c)) - (small ? 64.f : 0.f);
   const float offset = live ? ls * kLog2e - lc : __builtin_inff();
   if (lane == 0) {
     *row_c_at(row_c, n, RB) = offset;

@@ -25,3 +25,18 @@ def test_teacher_logits_whose_quotient_by_the_temperature_has_no_place_in_fp32(N
     Z, w = (Z.float() * T).to(Z.dtype), w * T
     loss, lse, grad, dZ, dP = check(Z, P, idx, t, w, T, dt)
     assert bool(torch.isfinite(loss).all()) and bool(grad[0].any()) and bool(grad[2].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [20, 200])
+@pytest.mark.parametrize("T,w_size,z_size,p_size", [
+    (1.0, 1e20, 1.0, 1.0), (1.0, 1e25, 1.0, 1.0), (1e-20, 1.0, 1e-10, 1e-10), (1e-5, 1e18, 1e-5, 1.0),
+    (1.0, 1e-30, 1.0, 1.0), (1e20, 1.0, 1e10, 1e10), (64.0, 1.0, 8.0, 8.0),
+])
+def test_weights_of_any_size(T, w_size, z_size, p_size, N, dt):
+    """|w| / T from below the smallest normal number to far above 2^64."""
+    Z, P, idx, t, w = inputs(N, 900, 64, 6, dt, seed=N)
+    Z, P = (Z.float() * z_size).to(Z.dtype), (P.float() * p_size).to(P.dtype)
+    loss, lse, grad, dZ, dP = check(Z, P, idx, t * T, w * w_size, T, dt)
+    assert bool(torch.isfinite(dP).all())
