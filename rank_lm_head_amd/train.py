@@ -6,6 +6,7 @@ joins them for torch's autograd.
 from __future__ import annotations
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _lib
 from .head import _DTYPES, _on
@@ -121,9 +122,13 @@ class _Distill(torch.autograd.Function):
 
 def distill_loss(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: torch.Tensor, *,
                  temperature: float = 1.0) -> torch.Tensor:
-    """distill()'s loss [N], differentiable in Z and P. The teacher's logits
+    """distill()'s loss [N], differentiable in Z and P (backwards only:
+    tensors with a forward-mode tangent are refused). The teacher's logits
     get no gradient. Not for graph capture with gradients: capture distill and
     distill_grad."""
+    # a tangent does not show in requires_grad, and no_grad does not end it
+    if any(unpack_dual(x).tangent is not None for x in (Z, P, logits)):
+        raise NotImplementedError("distill_loss has no forward-mode derivative")
     if not (torch.is_grad_enabled() and (Z.requires_grad or P.requires_grad)):
         return distill(Z, P, idx, logits, temperature=temperature, want_grad=False)[0]
     return _Distill.apply(Z, P, idx, logits, float(temperature))
