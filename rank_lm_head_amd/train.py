@@ -92,10 +92,12 @@ def distill_grad(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: to
     return dZ, dP
 
 
-def _no_capture() -> None:
+def _no_capture(device) -> None:
     # Under graph capture autograd's own accumulation nodes may belong to
     # another stream; the process would end, so the call is refused.
-    if torch.cuda.is_current_stream_capturing():
+    with _on(device):
+        capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
         raise RuntimeError("distill_loss cannot be captured with gradients; capture distill and distill_grad")
 
 
@@ -103,7 +105,8 @@ class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Z, P, idx, logits, temperature):
         need_dZ = ctx.needs_input_grad[0]
-        _no_capture()
+        if Z.is_cuda:   # else distill() says so
+            _no_capture(Z.device)
         loss, lse, grad = distill(Z, P, idx, logits, temperature=temperature, want_grad=need_dZ)
         ctx.save_for_backward(Z, P, idx, logits, lse, grad)
         ctx.temperature = temperature
@@ -112,8 +115,8 @@ class _Distill(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        _no_capture()
         Z, P, idx, logits, lse, grad = ctx.saved_tensors
+        _no_capture(Z.device)
         dZ, dP = distill_grad(Z, P, idx, logits, lse, grad, g.to(torch.float32).contiguous(),
                               temperature=ctx.temperature, want_dZ=ctx.needs_input_grad[0],
                               want_dP=ctx.needs_input_grad[1])

@@ -41,3 +41,11 @@ def test_without_tangents_the_loss_comes_through(stub):
     Z, P, idx, t = stub
     assert not lr.distill_loss(Z, P, idx, t).requires_grad
     assert lr.distill_loss(Z.requires_grad_(), P, idx, t).requires_grad
+
+
+def test_tensors_that_need_gradients_are_checked_first():
+    """A CPU tensor is refused as such, with gradients as without."""
+    idx, t = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, 4)
+    for Z in (torch.zeros(3, 16), torch.zeros(3, 16, requires_grad=True)):
+        with pytest.raises(ValueError, match="device tensor"):
+            lr.distill_loss(Z, torch.zeros(50, 16), idx, t)
