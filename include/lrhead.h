@@ -304,8 +304,8 @@ int lrhead_beam_select(int dtype, const void* logits, int64_t ld, const int32_t*
  * length[b] positions of each segment are moved (clamped to [0, positions]);
  * the others keep what dst held, and so do slots whose parent lies outside
  * [0, m). Requirements: m, nb >= 1; B, n_states, segs, positions,
- * position_bytes >= 0; no dst may overlap another dst or any src
- * (LRHEAD_EINVAL). src and dst may have any alignment; 16 bytes in
+ * position_bytes >= 0; no dst may overlap another dst, any src, parent or
+ * length (LRHEAD_EINVAL). src and dst may have any alignment; 16 bytes in
  * addresses and sizes are fastest. n_states <= LRHEAD_STATES_MAX.
  */
 #define LRHEAD_STATES_MAX 1024

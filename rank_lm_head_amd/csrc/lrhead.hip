@@ -638,7 +638,7 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
     uintptr_t lo, hi;
     bool dst;
   };
-  static thread_local Range ranges[2 * LRHEAD_STATES_MAX];
+  static thread_local Range ranges[2 * LRHEAD_STATES_MAX + 2];
   static thread_local lrh::BeamState moves[LRHEAD_STATES_MAX];
   int n = 0, n_moves = 0;
   for (int i = 0; i < n_states; ++i) {
@@ -657,11 +657,16 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
     ranges[n++] = {b, b + (uintptr_t)dst, true};
     moves[n_moves++] = {s.src, s.dst, s.segs, s.positions, s.position_bytes};
   }
+  int64_t slots = 0;
+  if (__builtin_mul_overflow(B, (int64_t)nb * 4, &slots)) return fail(LRHEAD_ERANGE, "B nb passes 64 bits");
+  ranges[n++] = {reinterpret_cast<uintptr_t>(parent), reinterpret_cast<uintptr_t>(parent) + (uintptr_t)slots, false};
+  if (length)
+    ranges[n++] = {reinterpret_cast<uintptr_t>(length), reinterpret_cast<uintptr_t>(length) + (uintptr_t)B * 4, false};
   std::sort(ranges, ranges + n, [](const Range& x, const Range& y) { return x.lo < y.lo; });
   uintptr_t any_end = 0, dst_end = 0;   // how far the ranges, and the destinations, before this one reach
   for (int i = 0; i < n; ++i) {
     if (ranges[i].lo < dst_end || (ranges[i].dst && ranges[i].lo < any_end))
-      return fail(LRHEAD_EINVAL, "a destination overlaps another state");
+      return fail(LRHEAD_EINVAL, "a destination overlaps another state, parent or length");
     any_end = std::max(any_end, ranges[i].hi);
     if (ranges[i].dst) dst_end = std::max(dst_end, ranges[i].hi);
   }
