@@ -22,6 +22,9 @@ def beam_select(logits: torch.Tensor, score: torch.Tensor, nb: int, *, idx: torc
     Returns (score float32, beam int32, token int32), all [B, nb]; see
     lrhead_beam_select in include/lrhead.h.
     """
+    for name, v in (("nb", nb), ("end_id", end_id)):
+        if not -2 ** 31 <= v < 2 ** 31:   # the C call takes 32 bits, and would get those
+            raise ValueError(f"{name} = {v} does not fit int32")
     code = _DTYPES.get(logits.dtype)
     if code is None or not logits.is_cuda or logits.dim() != 3:
         raise ValueError(f"logits must be a bfloat16 or float32 device tensor [B, m, n], not {logits.dtype} "

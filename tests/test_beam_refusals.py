@@ -2,7 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
+import rank_lm_head_amd as lr
 from rank_lm_head_amd import _lib
 from test_beam import _states
 
@@ -18,3 +20,10 @@ def test_reorder_refuses_indexes_inside_a_destination(parent, length):
     rc = _lib.load().lrhead_reorder(arr, 1, ctypes.c_void_p(parent), None if length is None else ctypes.c_void_p(length),
                                     2, 2, 2, None)
     assert rc == _lib.EINVAL
+
+
+@pytest.mark.parametrize("kwargs", [dict(nb=2 ** 32 + 2), dict(nb=-2 ** 32 + 2), dict(nb=2, end_id=2 ** 31),
+                                    dict(nb=2, end_id=-2 ** 40)])
+def test_select_refuses_integers_past_32_bits(kwargs):
+    with pytest.raises(ValueError, match="does not fit"):
+        lr.beam_select(torch.zeros(1, 2, 8), torch.zeros(1, 2), **kwargs)
