@@ -238,7 +238,10 @@ int lrhead_factor(const void* W, int64_t V, int64_t d, int r, int q,
  * unrounded q, so that it keeps its digits when the two are close. Products
  * and sums are fp32.) With grad == NULL the call computes loss and lse alone,
  * at half the work.
- * loss, lse: N fp32; grad: N x r fp32. T = temperature > 0.
+ * loss, lse: N fp32; grad: N x r fp32. T = temperature, 1e-30 <= T <= 1e30.
+ * The exponents s / T - lse are fp32 as well: q is off by about 2^-22 of the
+ * largest |s / T|, relatively, and from |s / T| = 2^20 on says nothing. A
+ * logit of +inf gives NaN.
  *
  * lrhead_distill_grad: with the rows' weights w (N fp32: the gradient that
  * arrives at loss; NULL: 1), the lse and grad of lrhead_distill on the same
@@ -277,7 +280,11 @@ int lrhead_distill_grad(int dtype, int64_t V, int64_t r, const void* P, const vo
  * over beams i and columns v, larger first, ties to the lower beam, then the
  * lower column. out_score[b, j] is that total, out_beam[b, j] the beam i, and
  * out_token[b, j] the column v, or with idx (B x m x n int32, the ids of
- * candidate lists) idx[b, i, v]. A logit that is NaN or -inf, or has a
+ * candidate lists) idx[b, i, v]. The sum is over the n columns given: with
+ * candidate lists the totals are, as in lrhead_branch, those of the draft
+ * distribution over each beam's own candidates, not of the vocabulary (whose
+ * normaliser needs all V logits), so a beam whose list holds little of its
+ * mass counts as if it held all. A logit that is NaN or -inf, or has a
  * negative id, is no candidate and has no share of the sum. With `ended`
  * (B x m bytes), a beam whose byte is not 0 has one continuation: end_id,
  * at its score. Slots past the last candidate hold -inf, -1 and -1. Totals

@@ -17,7 +17,9 @@ def beam_select(logits: torch.Tensor, score: torch.Tensor, nb: int, *, idx: torc
     logits: [B, m, n], bfloat16 or float32, rows evenly spaced and dense
     (a view of the first n columns of wider rows will do); score: [B, m]
     float32 path log probabilities; idx: [B, m, n] int32 ids of candidate
-    lists (as Head.draft returns them), None where a column is its own id;
+    lists (as Head.draft returns them), None where a column is its own id.
+    Probabilities are over the n columns: those of candidate lists are the
+    draft distribution's, as branch() gives them, not the vocabulary's.
     ended: [B, m] bool or uint8, beams that only carry on with end_id.
     Returns (score float32, beam int32, token int32), all [B, nb]; see
     lrhead_beam_select in include/lrhead.h.

@@ -43,7 +43,8 @@ def distill(Z: torch.Tensor, P: torch.Tensor, idx: torch.Tensor, logits: torch.T
             want_grad: bool = True):
     """The loss of the rows Z ([N, r]) under the head P ([V, r]) against a
     teacher's top logits (idx int32 and logits float32, [N, k], as
-    Head.full_topk returns them; an id outside [0, V) marks an empty place):
+    Head.full_topk returns them; an id outside [0, V), or a logit that is NaN
+    or -inf, marks an empty place):
     (loss [N], lse [N], dloss/dZ [N, r] or None), float32. See lrhead_distill
     in include/lrhead.h."""
     code, N, V, r, k = _check(Z, P, idx, logits)
