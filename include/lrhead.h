@@ -327,6 +327,116 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
                    const int32_t* length, int64_t B, int m, int nb, void* stream);
 
 /*
+ * Sampling: a token of each of B rows of logits (n columns in `dtype`, `ld`
+ * elements from row to row) from given random numbers u (B fp32 in [0, 1)).
+ * The draft distribution that lrhead_branch ranks, drawn from ("EAGLE-4",
+ * section "Retrieve vocabulary candidates cheaply, then score them exactly":
+ * the probabilities come from the exact logits), and the target's own samples.
+ * With the settings T, top_k, top_p and min_p of a row, in the order of larger
+ * logit first, ties to the lower column:
+ *   w_v  = exp((x_v - max x) / T);
+ *   K    = the first top_k columns (0 or less, or n and more: all);
+ *   S    = those of K before which less than top_p of K's mass lies (the first
+ *          always; 1 or more: all), and of weight min_p at least (0 or less: any);
+ *   token: the lowest column of S at which the mass of S, summed in column
+ *          order, passes u times the mass of S; with idx (B x n int32, the ids
+ *          of candidate lists) its id;
+ *   prob:  its weight over the mass of S. probs (n <= 64 only, may be NULL,
+ *          B x n): that of every column, 0 outside S.
+ * T = 0 takes the first column (as negative values and NaN do), T = inf makes
+ * all weights 1. NaN in top_p counts as 1, in min_p and u as 0; u is held to
+ * [0, 1], and a column of weight 0 is never drawn. A logit that is NaN or
+ * -inf, or has a negative id, is no candidate; +inf counts as the largest
+ * finite fp32. A row without candidates gives token -1 and probabilities 0.
+ * Weights are good to 4e-14 and sums to 1e-12 of the mass at n = 2^17 (half
+ * a unit of 2^-51, or of 2^(ceil(log2 n) - 62) for n above 2^11, per weight),
+ * and do not vary from call to call.
+ * Each setting is one value for all rows or, where its pointer is not NULL, an
+ * array of B device values.
+ * Requirements: 1 <= n <= 2^24, ld >= n, 0 <= B <= 2^20 and B rows of n
+ * columns less than 2^37 in all (ERANGE), inputs aligned to their
+ * elements, outputs and workspace to 16 bytes; the workspace has at least
+ * lrhead_sample_workspace_bytes bytes (0: invalid sizes), or is NULL where
+ * n <= 64, which needs none. `prob` may be NULL.
+ */
+typedef struct {
+  const float* temperature;   /* arrays, or NULL */
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;      /* where the array is NULL */
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} lrhead_sampling_t;
+size_t lrhead_sample_workspace_bytes(int dtype, int64_t B, int64_t n);
+int lrhead_sample(int dtype, const void* logits, int64_t ld, const int32_t* idx, const float* u,
+                  const lrhead_sampling_t* how, int64_t B, int64_t n, int32_t* token, float* prob,
+                  float* probs, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's logits, so that what
+ * comes out is distributed as the target's own samples ("EAGLE-4 Triples Qwen3
+ * Inference Speed by Adapting to Serving Load", section "Runtime-sized
+ * speculation": a chain of drafted tokens, of a size chosen at run time). For B
+ * sequences of up to s drafted tokens (token: B x s int32) with s + 1 rows of
+ * the target's logits each (B x (s+1) rows of n columns in `dtype`, `ld`
+ * elements from row to row): with p_j the target's distribution of row j under
+ * the sequence's settings (`how`, arrays of B values) as lrhead_sample has it,
+ * and q_j the drafter's, given as lists (idx and probs: B x s x k, ids and
+ * probabilities as lrhead_sample's token ids and probs; an id that occurs twice
+ * counts twice, one outside [0, n) not at all, negative and NaN probabilities
+ * as 0):
+ *   token j is accepted while u[b, j] q_j(token_j) < p_j(token_j);
+ *   at the first that is not, the token drawn from max(0, p_j - q_j) (from p_j
+ *   where that has no mass) takes its place, and the sequence ends;
+ *   after length[b] accepted ones, the token drawn from p of the next row is
+ *   added.
+ * Draws go by u[b, s] and by column order, as in lrhead_sample (u: B x (s+1)
+ * fp32). idx == NULL and probs == NULL (k ignored): the drafted token had
+ * probability 1 (greedy drafting). length (B int32, held to [0, s]; NULL: s):
+ * the drafted tokens that there are; rows behind row length[b] are not read.
+ * out_token (B x (s+1)): the accepted tokens, the drawn one, and -1 behind it;
+ * count[b]: how many there are in all. A row without candidates accepts
+ * nothing and draws -1, which count leaves out.
+ * Requirements: 0 <= s <= 255, 1 <= k <= 64, n, ld and alignment as for
+ * lrhead_sample, with B (s+1) rows in its place of B <= 2^20; the workspace
+ * has at least lrhead_verify_workspace_bytes bytes (0: invalid sizes).
+ */
+size_t lrhead_verify_workspace_bytes(int dtype, int64_t B, int s, int64_t n);
+int lrhead_verify(int dtype, const void* logits, int64_t ld, const int32_t* token,
+                  const int32_t* idx, const float* probs, int k, const int32_t* length,
+                  const float* u, const lrhead_sampling_t* how, int64_t B, int s, int64_t n,
+                  int32_t* out_token, int32_t* count, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
+ * Embedding: the rows that drafted tokens hand to a drafter's next step, and
+ * the gradient of their matrix (with W tied to the full head, its second part).
+ *   lrhead_embed:       out[i,:] = scale W[token[i],:], zeros for a token
+ *                       outside [0, V) (the slots that lrhead_verify and
+ *                       lrhead_beam_select leave empty);
+ *   lrhead_embed_grad:  dW[v,:] = scale sum_{i: token[i] = v} dY[i,:],
+ *                       written whole (zeros for tokens that do not occur), or
+ *                       with `add` added to the rows of tokens that occur, the
+ *                       others left as they were.
+ * W, dW: V x d; out, dY: N x d, all in `dtype`, token: N int32. Products and
+ * sums are fp32 and rounded once; the sums' order goes by N and the tokens
+ * alone, so the results do not vary from call to call. scale is finite.
+ * Requirements: 1 <= V < 2^31, 1 <= d <= 65536, 0 <= N <= 2^20 and N d < 2^35
+ * (more may be refused, ERANGE); every pointer aligned to its elements, the workspace to 16
+ * bytes, with at least lrhead_embed_grad_workspace_bytes bytes (0: invalid
+ * sizes). N == 0 writes no row, but dW (zeros) unless `add`. out may not
+ * overlap W, nor dW dY.
+ */
+int lrhead_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* token, int64_t N,
+                 float scale, void* out, void* stream);
+size_t lrhead_embed_grad_workspace_bytes(int dtype, int64_t V, int64_t d, int64_t N);
+int lrhead_embed_grad(int dtype, const void* dY, const int32_t* token, int64_t N, int64_t V,
+                      int64_t d, float scale, int add, void* dW, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * Profiling aid: hipEvent_t handles (passed as void*) that later calls on
  * this handle attach to the dispatch of the vocabulary score pass
  * (lrhead_candidates, lrhead_draft, fullhead_topk; for row batches its main

@@ -25,6 +25,13 @@ class State(ctypes.Structure):
                 ("positions", ctypes.c_int64), ("position_bytes", ctypes.c_int64)]
 
 
+class Sampling(ctypes.Structure):
+    """lrhead_sampling_t"""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+
+
 _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 
@@ -52,6 +59,17 @@ SIGNATURES = {
     "lrhead_beam_select": (ctypes.c_int, [ctypes.c_int, _vp, _c_i64, _vp, _vp, _vp, ctypes.c_int, _c_i64, ctypes.c_int,
                                           _c_i64, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "lrhead_reorder": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _c_i64, ctypes.c_int, ctypes.c_int, _vp]),
+    "lrhead_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64]),
+    "lrhead_sample": (ctypes.c_int, [ctypes.c_int, _vp, _c_i64, _vp, _vp, ctypes.POINTER(Sampling), _c_i64, _c_i64, _vp,
+                                     _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lrhead_verify_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, ctypes.c_int, _c_i64]),
+    "lrhead_verify": (ctypes.c_int, [ctypes.c_int, _vp, _c_i64, _vp, _vp, _vp, ctypes.c_int, _vp, _vp,
+                                     ctypes.POINTER(Sampling), _c_i64, ctypes.c_int, _c_i64, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]),
+    "lrhead_embed": (ctypes.c_int, [ctypes.c_int, _vp, _c_i64, _c_i64, _vp, _c_i64, ctypes.c_float, _vp, _vp]),
+    "lrhead_embed_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64]),
+    "lrhead_embed_grad": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _c_i64, _c_i64, _c_i64, ctypes.c_float, ctypes.c_int,
+                                         _vp, _vp, ctypes.c_size_t, _vp]),
     "lrhead_set_stage_events": (ctypes.c_int, [_vp, _vp, _vp]),
     "lrhead_destroy": (None, [_vp]),
     "lrhead_strerror": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,0 +1,691 @@
+// kernels_embed.hip — the rows of an embedding matrix at given tokens, and
+// the matrix's gradient.
+//
+//   out[n, :] = scale W[t_n, :]            (zeros for t_n outside [0, V))
+//   dW[v, :]  = scale sum_{n: t_n = v} dY[n, :]
+//
+// The lookup is one read and one write of each row. The gradient is made
+// without atomics on values, so that it does not vary: the positions are
+// sorted by token (a stable radix sort), a wave sums the rows of `chunk`
+// neighbouring places of the sorted order in registers, and runs of one token
+// that pass the end of a chunk are joined afterwards, chunk after chunk. Sums
+// are fp32, scaled and rounded once. What bounds it is the read of dY and the
+// write of dW.
+#include <algorithm>
+
+#include "device.h"
+#include "launch.h"
+#include "topk.h"
+
+namespace lrh {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kDigitBits = 9;                 // of a pass of the sort, at most
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kSmallSort = 16384;             // places that one block sorts
+constexpr int kSortTile = 4096;               // places of a block of the larger sort
+constexpr int kFillPiece = 16384;             // bytes that a block clears at a time
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// 16 bytes at an address aligned to its elements only.
+__device__ __forceinline__ u32x4 load16_any(const void* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void store16_any(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+template <typename T> struct Elems;
+template <> struct Elems<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ float get(u32x4 v, int e) { return __uint_as_float(v[e]); }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[4]) {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+};
+template <> struct Elems<uint16_t> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ float get(u32x4 v, int e) {
+    return __uint_as_float((e & 1) ? (v[e >> 1] & 0xffff0000u) : (v[e >> 1] << 16));
+  }
+  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (uint32_t)f32_to_bf16(f[2 * q]) | (uint32_t)f32_to_bf16(f[2 * q + 1]) << 16;
+    return v;
+  }
+};
+
+// ------------------------------------------------------------------- lookup
+
+struct EmbedArgs {
+  const void* W;
+  int64_t V, d;
+  const int32_t* token;
+  int64_t N;
+  float scale;
+  void* out;
+  int pieces;   // of a row
+};
+
+// A wave copies one piece of one row: four 16-byte loads a lane in flight.
+constexpr int kEmbedChunks = 4;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
+  constexpr int EP = Elems<T>::n;
+  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
+  const int64_t n = w / a.pieces;
+  if (n >= a.N) return;
+  const int64_t c0 = (w % a.pieces) * (kEmbedChunks * kWave * EP) + (threadIdx.x & 63) * EP;
+  const int t = a.token[n];
+  const bool have = t >= 0 && t < a.V;
+  const T* src = static_cast<const T*>(a.W) + (have ? (int64_t)t * a.d : 0);
+  T* dst = static_cast<T*>(a.out) + n * a.d;
+  u32x4 v[kEmbedChunks];
+#pragma unroll
+  for (int i = 0; i < kEmbedChunks; ++i) {
+    const int64_t c = c0 + i * (kWave * EP);
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (have && c + EP <= a.d) v[i] = load16_any(src + c);
+  }
+#pragma unroll
+  for (int i = 0; i < kEmbedChunks; ++i) {
+    const int64_t c = c0 + i * (kWave * EP);
+    if (c + EP <= a.d) {
+      if (a.scale != 1.f) {
+        float f[EP];
+#pragma unroll
+        for (int e = 0; e < EP; ++e) f[e] = Elems<T>::get(v[i], e) * a.scale;
+        v[i] = have ? Elems<T>::pack(f) : u32x4{0u, 0u, 0u, 0u};   // 0 of a missing token, whatever the scale
+      }
+      store16_any(dst + c, v[i]);
+    } else {
+      for (int64_t e = c; e < a.d; ++e)
+        dst[e] = !have ? T(0) : a.scale != 1.f ? store_cast<T>(Elems<T>::one(src + e) * a.scale) : src[e];
+    }
+  }
+}
+
+// --------------------------------------------------------------------- sort
+
+struct GradArgs {
+  const void* dY;
+  const int32_t* token;
+  int64_t N, V, d;
+  float scale;
+  void* dW;
+  bool add;             // to what dW holds; else its other rows are cleared
+  int bits, passes;     // of a pass's digit, of the keys
+  int at_bits;          // one block's sort: bits of a place
+  int tiles;            // blocks of the larger sort
+  uint32_t* count;      // [digit][tile]
+  uint32_t *key[2], *at[2];   // sorted tokens (V: none) and their places; [0] holds the result
+  int chunk;            // sorted places of a wave
+  int64_t chunks;
+  int pieces;           // waves along a row
+  float* part;          // [chunk][2][d]: runs that began before the chunk, and that go on behind it
+};
+
+__device__ __forceinline__ uint32_t key_of(const GradArgs& a, int64_t i) {
+  const int t = a.token[i];
+  return t >= 0 && t < a.V ? (uint32_t)t : (uint32_t)a.V;
+}
+
+// The lanes whose digit is this lane's; all of the wave's lanes call it.
+__device__ __forceinline__ unsigned long long same_digit(uint32_t digit, int bits, bool live) {
+  unsigned long long m = __ballot(live);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (digit >> b) & 1;
+    const unsigned long long v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+// Exclusive prefix sums of hist[digit][wave], digit by digit, in place.
+// hist: [kSortWaves][1 << bits]; sums: kSortWaves words.
+__device__ __forceinline__ void scan_hist(uint32_t* hist, int digits, uint32_t* sums) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  // a thread takes a digit's counts of 16 waves; with fewer threads than digits times that never
+  uint32_t mine = 0;
+  if (tid < digits)
+    for (int w = 0; w < kSortWaves; ++w) mine += hist[w * digits + tid];
+  const uint32_t incl = wave_incl_scan_u32(mine);
+  if (lane == 63) sums[wave] = incl;
+  __syncthreads();
+  uint32_t at = incl - mine;
+  for (int w = 0; w < wave; ++w) at += sums[w];
+  if (tid < digits)
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = hist[w * digits + tid];
+      hist[w * digits + tid] = at;
+      at += c;
+    }
+  __syncthreads();
+}
+
+// Clears a share of dW: blocks [0, blocks) take pieces in turn.
+__device__ __forceinline__ void clear(const GradArgs& a, size_t elem, int64_t block, int64_t blocks, int64_t from, int64_t to) {
+  char* p = static_cast<char*>(a.dW);
+  for (int64_t at = from + block * kFillPiece; at < to; at += blocks * kFillPiece) {
+    const int64_t end = min(to, at + kFillPiece);
+    for (int64_t o = at + (int64_t)threadIdx.x * 16; o < end; o += (int64_t)blockDim.x * 16) {
+      if (o + 16 <= end) {
+        store16_any(p + o, u32x4{0u, 0u, 0u, 0u});
+      } else {
+        for (int64_t q = o; q < end; q += elem)
+          if (elem == 2) *reinterpret_cast<uint16_t*>(p + q) = 0;
+          else *reinterpret_cast<uint32_t*>(p + q) = 0;
+      }
+    }
+  }
+}
+
+// Up to kSmallSort places: block 0 sorts them in LDS, a token and its place
+// as one 32-bit word, while the other blocks clear dW. A wave owns a stretch
+// of the places, so equal digits keep their order by wave, round and lane.
+template <size_t kElem>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(GradArgs a) {
+  extern __shared__ uint32_t lds[];
+  const int64_t bytes = a.V * a.d * (int64_t)kElem;
+  if (blockIdx.x > 0) {
+    clear(a, kElem, blockIdx.x - 1, gridDim.x - 1, 0, bytes);
+    return;
+  }
+  constexpr int kMost = kSmallSort / kSortThreads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  const int n = (int)a.N;
+  uint32_t* sums = lds;                     // kSortWaves
+  uint32_t* hist = lds + 64;                // [kSortWaves][kDigits]
+  uint32_t* word = hist + kSortWaves * kDigits;   // n
+  const int rounds = (n + kSortThreads - 1) / kSortThreads;
+  const int first = wave * rounds * kWave;
+  uint32_t v[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int p = first + i * kWave + lane;
+    v[i] = i < rounds && p < n ? key_of(a, p) << a.at_bits | (uint32_t)p : 0u;
+  }
+  const int digits = 1 << a.bits;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = a.at_bits + pass * a.bits;
+    for (int i = tid; i < kSortWaves * digits; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    uint32_t rank[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i < rounds) {
+        const bool live = first + i * kWave + lane < n;
+        const uint32_t digit = (v[i] >> shift) & (digits - 1);
+        const unsigned long long same = same_digit(digit, a.bits, live);
+        uint32_t* h = hist + wave * digits + digit;
+        const int below = lanes_below(same);
+        uint32_t had = 0;
+        if (live) had = *h;
+        __builtin_amdgcn_wave_barrier();
+        if (live && below == 0) *h = had + __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        rank[i] = had + below;
+      }
+    }
+    __syncthreads();
+    scan_hist(hist, digits, sums);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i < rounds && first + i * kWave + lane < n) {
+        const uint32_t digit = (v[i] >> shift) & (digits - 1);
+        word[hist[wave * digits + digit] + rank[i]] = v[i];
+      }
+    }
+    __syncthreads();
+    if (pass + 1 < a.passes) {
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int p = first + i * kWave + lane;
+        if (i < rounds && p < n) v[i] = word[p];
+      }
+    }
+  }
+  for (int p = tid; p < n; p += kSortThreads) {
+    const uint32_t x = word[p];
+    a.key[0][p] = a.at_bits < 32 ? x >> a.at_bits : 0u;
+    a.at[0][p] = x & (uint32_t)((1ull << a.at_bits) - 1);
+  }
+}
+
+// The larger sort, a pass of it in three launches: each block counts the
+// digits of its tile; one block makes places of the counts (and the others
+// clear dW); each block moves its tile, in order.
+constexpr int kTileRounds = kSortTile / kSortThreads;
+__device__ __forceinline__ void tile_ranks(const GradArgs& a, int pass, const uint32_t (&key)[kTileRounds],
+                                           uint32_t (&rank)[kTileRounds], uint32_t* hist, int64_t first) {
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int digits = 1 << a.bits, shift = pass * a.bits;
+  for (int i = threadIdx.x; i < kSortWaves * digits; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kTileRounds; ++i) {
+    const bool live = first + i * kWave + lane < a.N;
+    const uint32_t digit = (key[i] >> shift) & (digits - 1);
+    const unsigned long long same = same_digit(digit, a.bits, live);
+    uint32_t* h = hist + wave * digits + digit;
+    const int below = lanes_below(same);
+    uint32_t had = 0;
+    if (live) had = *h;
+    __builtin_amdgcn_wave_barrier();
+    if (live && below == 0) *h = had + __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    rank[i] = had + below;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void tile_keys(const GradArgs& a, int pass, int64_t first, uint32_t (&key)[kTileRounds]) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t* from = a.key[(a.passes - pass) & 1];
+#pragma unroll
+  for (int i = 0; i < kTileRounds; ++i) {
+    const int64_t p = first + i * kWave + lane;
+    key[i] = p >= a.N ? 0u : pass == 0 ? key_of(a, p) : from[p];
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(GradArgs a, int pass) {
+  __shared__ uint32_t hist[kSortWaves * kDigits];
+  const int64_t first = (int64_t)blockIdx.x * kSortTile + wave_id() * (kTileRounds * kWave);
+  uint32_t key[kTileRounds], rank[kTileRounds];
+  tile_keys(a, pass, first, key);
+  tile_ranks(a, pass, key, rank, hist, first);
+  const int digits = 1 << a.bits;
+  for (int g = threadIdx.x; g < digits; g += kSortThreads) {
+    uint32_t c = 0;
+    for (int w = 0; w < kSortWaves; ++w) c += hist[w * digits + g];
+    a.count[(int64_t)g * a.tiles + blockIdx.x] = c;
+  }
+}
+
+template <size_t kElem>
+__global__ void __launch_bounds__(kSortThreads) embed_places_kernel(GradArgs a, int pass) {
+  if (blockIdx.x > 0) {   // a share of dW for each pass
+    const int64_t bytes = a.V * a.d * (int64_t)kElem;
+    const int64_t share = (bytes / a.passes) & ~(int64_t)15;
+    clear(a, kElem, blockIdx.x - 1, gridDim.x - 1, share * pass, pass + 1 == a.passes ? bytes : share * (pass + 1));
+    return;
+  }
+  __shared__ uint32_t sums[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  const int total = a.tiles << a.bits;
+  uint32_t before = 0;
+  for (int i0 = 0; i0 < total; i0 += kSortThreads * 4) {
+    uint32_t c[4], mine = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + tid * 4 + q;
+      c[q] = i < total ? a.count[i] : 0u;
+      mine += c[q];
+    }
+    const uint32_t incl = wave_incl_scan_u32(mine);
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    uint32_t at = before + incl - mine, all = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (w < wave) at += sums[w];
+      all += sums[w];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + tid * 4 + q;
+      if (i < total) a.count[i] = at;
+      at += c[q];
+    }
+    before += all;
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_move_kernel(GradArgs a, int pass) {
+  __shared__ uint32_t hist[kSortWaves * kDigits];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int64_t first = (int64_t)blockIdx.x * kSortTile + wave * (kTileRounds * kWave);
+  uint32_t key[kTileRounds], rank[kTileRounds];
+  tile_keys(a, pass, first, key);
+  tile_ranks(a, pass, key, rank, hist, first);
+  const int digits = 1 << a.bits, shift = pass * a.bits;
+  for (int g = threadIdx.x; g < digits; g += kSortThreads) {   // where each wave's digits begin
+    uint32_t at = a.count[(int64_t)g * a.tiles + blockIdx.x];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = hist[w * digits + g];
+      hist[w * digits + g] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  const uint32_t* from = a.at[(a.passes - pass) & 1];
+  uint32_t* to_key = a.key[(a.passes - pass - 1) & 1];
+  uint32_t* to_at = a.at[(a.passes - pass - 1) & 1];
+#pragma unroll
+  for (int i = 0; i < kTileRounds; ++i) {
+    const int64_t p = first + i * kWave + lane;
+    if (p >= a.N) continue;
+    const uint32_t o = hist[wave * digits + ((key[i] >> shift) & (digits - 1))] + rank[i];
+    to_key[o] = key[i];
+    to_at[o] = pass == 0 ? (uint32_t)p : from[p];
+  }
+}
+
+// --------------------------------------------------------------------- sums
+
+// A wave's columns of a row of dY or dW: 16 bytes a lane.
+template <typename T>
+struct Row {
+  static constexpr int EP = Elems<T>::n;
+  float f[EP];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < EP; ++e) f[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(u32x4 v) {
+#pragma unroll
+    for (int e = 0; e < EP; ++e) f[e] += Elems<T>::get(v, e);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* row, int64_t c, int64_t d) {
+  constexpr int EP = Elems<T>::n;
+  if (c + EP <= d) return load16_any(row + c);
+  float f[EP];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) f[e] = c + e < d ? Elems<T>::one(row + c + e) : 0.f;
+  return Elems<T>::pack(f);
+}
+
+// dW[key, c..] = scale r (+ what is there), rounded once.
+template <typename T>
+__device__ __forceinline__ void put(const GradArgs& a, uint32_t key, int64_t c, Row<T>& r) {
+  constexpr int EP = Elems<T>::n;
+  if (c >= a.d) return;
+  T* row = static_cast<T*>(a.dW) + (int64_t)key * a.d;
+  float f[EP];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) f[e] = r.f[e] * a.scale;
+  if (a.add) {
+    const u32x4 old = load_piece(row, c, a.d);
+#pragma unroll
+    for (int e = 0; e < EP; ++e) f[e] += Elems<T>::get(old, e);
+  }
+  if (c + EP <= a.d) {
+    store16_any(row + c, Elems<T>::pack(f));
+  } else {
+    for (int e = 0; c + e < a.d; ++e) row[c + e] = store_cast<T>(f[e]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float* part_of(const GradArgs& a, int64_t chunk, int side, int piece) {
+  constexpr int EP = Elems<T>::n;
+  return a.part + ((chunk * 2 + side) * a.pieces + piece) * (kWave * EP) + (threadIdx.x & 63) * EP;
+}
+
+// Sums of the sorted places [chunk * a.chunk, ...): runs inside the chunk go
+// to dW, those that pass one of its ends to a.part. Lanes hold 64 places at
+// a time; kAhead rows are on their way.
+constexpr int kAhead = 8;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(GradArgs a) {
+  constexpr int EP = Elems<T>::n;
+  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
+  const int64_t chunk = w / a.pieces;
+  if (chunk >= a.chunks) return;
+  const int piece = (int)(w % a.pieces), lane = threadIdx.x & 63;
+  const int64_t c = (int64_t)piece * (kWave * EP) + lane * EP;
+  const int64_t p0 = chunk * a.chunk, p1 = min(a.N, p0 + a.chunk);
+  const uint32_t *keys = a.key[0], *at = a.at[0];
+  const T* dY = static_cast<const T*>(a.dY);
+  const uint32_t none = (uint32_t)a.V;
+  uint32_t run = keys[p0];
+  bool began = p0 == 0 || keys[p0 - 1] != run;   // the run begins in this chunk
+  Row<T> sum;
+  sum.zero();
+  for (int64_t q0 = p0; q0 < p1; q0 += kWave) {
+    const int n = (int)min((int64_t)kWave, p1 - q0);
+    const int key_l = lane < n ? (int)keys[q0 + lane] : (int)none;
+    const int at_l = lane < n ? (int)at[q0 + lane] : 0;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      u32x4 v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j;
+        v[j] = u32x4{0u, 0u, 0u, 0u};
+        if (i < n && (uint32_t)__builtin_amdgcn_readlane(key_l, i) != none)
+          v[j] = load_piece(dY + (int64_t)(uint32_t)__builtin_amdgcn_readlane(at_l, i) * a.d, c, a.d);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j;
+        if (i < n) {
+          const uint32_t k = (uint32_t)__builtin_amdgcn_readlane(key_l, i);
+          if (k != run) {
+            if (run != none) {
+              if (began) {
+                put<T>(a, run, c, sum);
+              } else {
+                float* o = part_of<T>(a, chunk, 0, piece);
+#pragma unroll
+                for (int e = 0; e < EP; ++e) o[e] = sum.f[e];
+              }
+            }
+            sum.zero();
+            run = k;
+            began = true;
+          }
+          sum.add(v[j]);
+        }
+      }
+    }
+  }
+  if (run == none) return;
+  const bool more = p1 < a.N && keys[p1] == run;
+  if (began && !more) {
+    put<T>(a, run, c, sum);
+    return;
+  }
+  float* o = part_of<T>(a, chunk, began ? 1 : 0, piece);
+#pragma unroll
+  for (int e = 0; e < EP; ++e) o[e] = sum.f[e];
+}
+
+// Joins the runs that pass the end of the chunk that they begin in.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(GradArgs a) {
+  constexpr int EP = Elems<T>::n;
+  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
+  const int64_t chunk = w / a.pieces;
+  if (chunk + 1 >= a.chunks) return;   // nothing behind it
+  const int piece = (int)(w % a.pieces), lane = threadIdx.x & 63;
+  const int64_t c = (int64_t)piece * (kWave * EP) + lane * EP;
+  const uint32_t* keys = a.key[0];
+  const int64_t p0 = chunk * a.chunk, p1 = p0 + a.chunk;
+  const uint32_t run = keys[p1 - 1];
+  if (run == (uint32_t)a.V || keys[p1] != run) return;
+  if (keys[p0] == run && p0 > 0 && keys[p0 - 1] == run) return;   // it began before
+  Row<T> sum;
+  const float* o = part_of<T>(a, chunk, 1, piece);
+#pragma unroll
+  for (int e = 0; e < EP; ++e) sum.f[e] = o[e];
+  // the run's further chunks: those that begin with its token
+  for (int64_t c0 = chunk + 1; c0 < a.chunks; c0 += kWave) {
+    const bool in = c0 + lane < a.chunks && keys[(c0 + lane) * a.chunk] == run;
+    const unsigned long long m = __ballot(in);
+    const int n = m == ~0ull ? kWave : __ffsll((unsigned long long)~m) - 1;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      float f[kAhead][EP];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float* o = part_of<T>(a, c0 + min(i0 + j, n - 1), 0, piece);
+#pragma unroll
+        for (int e = 0; e < EP; ++e) f[j][e] = o[e];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j < n) {
+#pragma unroll
+          for (int e = 0; e < EP; ++e) sum.f[e] += f[j][e];
+        }
+      }
+    }
+    if (n < kWave) break;
+  }
+  put<T>(a, run, c, sum);
+}
+
+struct GradPlan {
+  int bits, passes, at_bits, tiles, chunk, pieces;
+  int64_t chunks;
+  bool small;
+};
+int bits_of(uint64_t x) { return x ? 64 - __builtin_clzll(x) : 0; }
+GradPlan plan(int dtype, int64_t V, int64_t d, int64_t N) {
+  GradPlan p;
+  const int all = std::max(1, bits_of((uint64_t)V));   // of tokens and V itself
+  p.passes = (all + kDigitBits - 1) / kDigitBits;
+  p.bits = (all + p.passes - 1) / p.passes;
+  p.at_bits = std::max(1, bits_of((uint64_t)(N - 1)));
+  p.small = N <= kSmallSort && all + p.at_bits <= 32;
+  p.tiles = (int)ceil_div(N, kSortTile);
+  p.pieces = (int)ceil_div(d, kWave * (dtype == 0 ? 8 : 4));
+  p.chunk = 16;
+  while (p.chunk < 256 && N / p.chunk > 4096) p.chunk *= 2;
+  p.chunks = ceil_div(N, p.chunk);
+  return p;
+}
+struct GradSpace {
+  size_t key[2], at[2], count, part, total;
+};
+GradSpace space(int dtype, int64_t V, int64_t d, int64_t N) {
+  const GradPlan p = plan(dtype, V, d, N);
+  GradSpace s{};
+  size_t o = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  s.key[0] = take((size_t)N * 4);
+  s.at[0] = take((size_t)N * 4);
+  if (!p.small) {
+    s.key[1] = take((size_t)N * 4);
+    s.at[1] = take((size_t)N * 4);
+    s.count = take(((size_t)p.tiles << p.bits) * 4);
+  }
+  s.part = take((size_t)p.chunks * 2 * p.pieces * kWave * (dtype == 0 ? 8 : 4) * 4);
+  s.total = o;
+  return s;
+}
+
+template <typename T>
+hipError_t embed_grad(const GradArgs& a, const GradPlan& p, hipStream_t s) {
+  // blocks that clear dW: eight a compute unit at most, of which each has several pieces
+  const int64_t fill = a.add ? 0 : std::min<int64_t>(1024, ceil_div(a.V * a.d * (int64_t)sizeof(T), kFillPiece));
+  if (p.small) {
+    const size_t lds = (64 + kSortWaves * kDigits + (size_t)a.N) * 4;
+    if (lds > 65536) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(embed_sort_kernel<sizeof(T)>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(embed_sort_kernel<sizeof(T)>, dim3((unsigned)(1 + fill)), dim3(kSortThreads), lds, s, a);
+  } else {
+    for (int pass = 0; pass < a.passes; ++pass) {
+      hipLaunchKernelGGL(embed_count_kernel, dim3(a.tiles), dim3(kSortThreads), 0, s, a, pass);
+      hipLaunchKernelGGL(embed_places_kernel<sizeof(T)>, dim3((unsigned)(1 + fill)), dim3(kSortThreads), 0, s, a, pass);
+      hipLaunchKernelGGL(embed_move_kernel, dim3(a.tiles), dim3(kSortThreads), 0, s, a, pass);
+    }
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)ceil_div(a.chunks * a.pieces, kWaves));
+  hipLaunchKernelGGL(embed_sum_kernel<T>, grid, dim3(kThreads), 0, s, a);
+  if (a.chunks > 1) hipLaunchKernelGGL(embed_join_kernel<T>, grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <size_t kElem>
+__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(GradArgs a) {
+  clear(a, kElem, blockIdx.x, gridDim.x, 0, a.V * a.d * (int64_t)kElem);
+}
+
+}  // namespace
+
+bool embed_fits(int dtype, int64_t d, int64_t N) {
+  const int64_t pieces = ceil_div(d, kEmbedChunks * kWave * (dtype == 0 ? 8 : 4));
+  return ceil_div(N * pieces, kWaves) <= kMostThreads / kThreads;
+}
+
+bool embed_grad_fits(int dtype, int64_t V, int64_t d, int64_t N) {
+  const GradPlan p = plan(dtype, V, d, N);
+  return ceil_div(p.chunks * p.pieces, kWaves) <= kMostThreads / kThreads;
+}
+
+hipError_t launch_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* token, int64_t N, float scale,
+                        void* out, hipStream_t s) {
+  EmbedArgs a{W, V, d, token, N, scale, out, (int)ceil_div(d, kEmbedChunks * kWave * (dtype == 0 ? 8 : 4))};
+  const dim3 grid((unsigned)ceil_div(N * a.pieces, kWaves)), block(kThreads);
+  if (dtype == 0) hipLaunchKernelGGL(embed_kernel<uint16_t>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(embed_kernel<float>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+size_t embed_grad_workspace_bytes(int dtype, int64_t V, int64_t d, int64_t N) { return space(dtype, V, d, N).total; }
+
+hipError_t launch_embed_grad(int dtype, const void* dY, const int32_t* token, int64_t N, int64_t V, int64_t d,
+                             float scale, bool add, void* dW, void* workspace, hipStream_t s) {
+  GradArgs a{};
+  a.dY = dY;
+  a.token = token;
+  a.N = N;
+  a.V = V;
+  a.d = d;
+  a.scale = scale;
+  a.dW = dW;
+  a.add = add;
+  if (N == 0) {
+    if (add) return hipSuccess;
+    const size_t elem = dtype == 0 ? 2 : 4;
+    const dim3 grid((unsigned)std::min<int64_t>(1024, ceil_div(V * d * (int64_t)elem, kFillPiece)));
+    if (dtype == 0) hipLaunchKernelGGL(embed_clear_kernel<2>, grid, dim3(kSortThreads), 0, s, a);
+    else hipLaunchKernelGGL(embed_clear_kernel<4>, grid, dim3(kSortThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  const GradPlan p = plan(dtype, V, d, N);
+  const GradSpace sp = space(dtype, V, d, N);
+  char* ws = static_cast<char*>(workspace);
+  a.bits = p.bits;
+  a.passes = p.passes;
+  a.at_bits = p.at_bits;
+  a.tiles = p.tiles;
+  a.count = reinterpret_cast<uint32_t*>(ws + sp.count);
+  for (int i = 0; i < 2; ++i) {
+    a.key[i] = reinterpret_cast<uint32_t*>(ws + sp.key[i]);
+    a.at[i] = reinterpret_cast<uint32_t*>(ws + sp.at[i]);
+  }
+  a.chunk = p.chunk;
+  a.chunks = p.chunks;
+  a.pieces = p.pieces;
+  a.part = reinterpret_cast<float*>(ws + sp.part);
+  return dtype == 0 ? embed_grad<uint16_t>(a, p, s) : embed_grad<float>(a, p, s);
+}
+
+}  // namespace lrh

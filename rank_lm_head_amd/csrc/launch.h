@@ -223,6 +223,52 @@ struct BeamState {
 hipError_t launch_beam_move(const BeamState* states, int n_states, const int32_t* parent, const int32_t* length,
                             int64_t B, int m, int nb, hipStream_t stream);
 
+// ---------------------------------------------------- kernels_sample.hip
+// A token of each row of logits under temperature, top_k, top_p and min_p
+// (an array with one value per row or sequence, or NULL: the value for all),
+// see lrhead_sample.
+struct SampleArgs {
+  int dtype;
+  const void* x;
+  int64_t ld, n;
+  const int32_t* idx;
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all, top_p_all, min_p_all;
+  int top_k_all;
+  int32_t* token;
+  float* prob;
+  float* probs;
+};
+// Drafted tokens of B sequences against s + 1 rows of logits each, see lrhead_verify.
+struct VerifyArgs {
+  int s, k;
+  const int32_t* drafted;
+  const int32_t* list;
+  const float* q;
+  const int32_t* length;
+  int32_t* count;
+};
+bool sample_fits(int64_t rows, int64_t n);
+size_t sample_workspace_bytes(int64_t B, int64_t n);
+hipError_t launch_sample(const SampleArgs& in, int64_t B, void* workspace, hipStream_t stream);
+size_t verify_workspace_bytes(int64_t B, int s, int64_t n);
+hipError_t launch_verify(const SampleArgs& in, const VerifyArgs& v, int64_t B, void* workspace, hipStream_t stream);
+
+// ----------------------------------------------------- kernels_embed.hip
+// out[n] = scale W[token[n]] (zeros for tokens outside [0, V)), and W's
+// gradient, see lrhead_embed and lrhead_embed_grad.
+bool embed_fits(int dtype, int64_t d, int64_t N);
+hipError_t launch_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* token, int64_t N, float scale,
+                        void* out, hipStream_t stream);
+bool embed_grad_fits(int dtype, int64_t V, int64_t d, int64_t N);
+size_t embed_grad_workspace_bytes(int dtype, int64_t V, int64_t d, int64_t N);
+hipError_t launch_embed_grad(int dtype, const void* dY, const int32_t* token, int64_t N, int64_t V, int64_t d,
+                             float scale, bool add, void* dW, void* workspace, hipStream_t stream);
+
 // --------------------------------------------------- kernels_distill.hip
 // Distillation of (Z: N x r, P: V x r) from the teacher places idx / t
 // (N x k), see lrhead_distill. launch_distill writes loss, lse and, unless G

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -58,6 +59,8 @@ constexpr int64_t kDownSplitMaxElems = 65536;   // ... when B * r is above this
 // after a ranking-only merge measured 40.1 us at 64 rows, k = 32.)
 constexpr int64_t kSpeculatePairsBelow = 1024;
 constexpr int64_t kBMaxLimit = int64_t(1) << 20;
+constexpr int64_t kSampleMaxN = int64_t(1) << 24;
+constexpr int kVerifyMaxS = 255;
 
 thread_local char g_err[512] = "";
 
@@ -342,6 +345,55 @@ int check_beam(int dtype, int64_t B, int m, int64_t n, int nb) {
   if (n < 1 || n > INT32_MAX) return fail(LRHEAD_ERANGE, "n = %lld outside [1, 2^31)", (long long)n);
   if (B < 0 || B > kBMaxLimit || !lrh::beam_fits(dtype, B > 0 ? B : 1, m, n))
     return fail(LRHEAD_ERANGE, "B = %lld outside [0, 2^20], or B m n too large for one call", (long long)B);
+  return LRHEAD_OK;
+}
+
+int check_sampling(int dtype, int64_t B, int64_t per, int64_t n) {
+  if (dtype != LRHEAD_BF16 && dtype != LRHEAD_FP32) return fail(LRHEAD_EDTYPE, "unknown dtype %d", dtype);
+  if (n < 1 || n > kSampleMaxN) return fail(LRHEAD_ERANGE, "n = %lld outside [1, 2^24]", (long long)n);
+  if (B < 0 || B > kBMaxLimit / per || !lrh::sample_fits(B * per, n))
+    return fail(LRHEAD_ERANGE, "B = %lld is negative, or too many rows for one call", (long long)B);
+  return LRHEAD_OK;
+}
+
+int check_embed(int dtype, int64_t V, int64_t d, int64_t N) {
+  if (dtype != LRHEAD_BF16 && dtype != LRHEAD_FP32) return fail(LRHEAD_EDTYPE, "unknown dtype %d", dtype);
+  if (V < 1 || V > INT32_MAX) return fail(LRHEAD_ERANGE, "V = %lld outside [1, 2^31)", (long long)V);
+  if (d < 1 || d > LRHEAD_D_MAX) return fail(LRHEAD_ERANGE, "d = %lld outside [1, %d]", (long long)d, LRHEAD_D_MAX);
+  if (N < 0 || N > kBMaxLimit) return fail(LRHEAD_ERANGE, "N = %lld outside [0, 2^20]", (long long)N);
+  if (N > 0 && (!lrh::embed_fits(dtype, d, N) || !lrh::embed_grad_fits(dtype, V, d, N)))
+    return fail(LRHEAD_ERANGE, "N = %lld rows of d = %lld are too many for one call", (long long)N, (long long)d);
+  return LRHEAD_OK;
+}
+
+bool aligned_elem(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) == 0; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an && bn && x < y + bn && y < x + an;
+}
+
+int sample_args(lrh::SampleArgs* a, int dtype, const void* logits, int64_t ld, const float* u,
+                const lrhead_sampling_t* how, int64_t n) {
+  if (!logits || !u || !how) return fail(LRHEAD_EINVAL, "logits, u and how must be non-NULL");
+  if (!aligned_elem(logits, dtype)) return fail(LRHEAD_EALIGN, "logits are not aligned to their elements");
+  if (!aligned4(u) || !aligned4(how->temperature) || !aligned4(how->top_k) || !aligned4(how->top_p) ||
+      !aligned4(how->min_p))
+    return fail(LRHEAD_EALIGN, "u and the settings' arrays must be 4-byte aligned");
+  a->dtype = dtype;
+  a->x = logits;
+  a->ld = ld;
+  a->n = n;
+  a->u = u;
+  a->temperature = how->temperature;
+  a->top_k = how->top_k;
+  a->top_p = how->top_p;
+  a->min_p = how->min_p;
+  a->temperature_all = how->temperature_all;
+  a->top_k_all = how->top_k_all;
+  a->top_p_all = how->top_p_all;
+  a->min_p_all = how->min_p_all;
   return LRHEAD_OK;
 }
 
@@ -672,6 +724,118 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
   }
   LRH_HIP(lrh::launch_beam_move(moves, n_moves, parent, length, B, m, nb, static_cast<hipStream_t>(stream)),
           "state reordering launch");
+  return LRHEAD_OK;
+}
+
+size_t lrhead_sample_workspace_bytes(int dtype, int64_t B, int64_t n) {
+  if (check_sampling(dtype, B, 1, n) != LRHEAD_OK) return 0;
+  return lrh::sample_workspace_bytes(B > 0 ? B : 1, n);
+}
+
+int lrhead_sample(int dtype, const void* logits, int64_t ld, const int32_t* idx, const float* u,
+                  const lrhead_sampling_t* how, int64_t B, int64_t n, int32_t* token, float* prob, float* probs,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  LRH_TRY(check_sampling(dtype, B, 1, n));
+  if (ld < n) return fail(LRHEAD_ERANGE, "ld = %lld below n = %lld", (long long)ld, (long long)n);
+  if (probs && n > LRHEAD_K_MAX) return fail(LRHEAD_ERANGE, "probs with n = %lld above %d", (long long)n, LRHEAD_K_MAX);
+  if (B == 0) return LRHEAD_OK;
+  lrh::SampleArgs a{};
+  LRH_TRY(sample_args(&a, dtype, logits, ld, u, how, n));
+  if (!workspace && n > LRHEAD_K_MAX) return fail(LRHEAD_EINVAL, "workspace is NULL");
+  if (!aligned4(idx) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "idx must be 4-byte aligned, the workspace 16-byte");
+  LRH_TRY(check_out(token, "token", true));
+  LRH_TRY(check_out(prob, "prob", false));
+  LRH_TRY(check_out(probs, "probs", false));
+  const size_t need = lrh::sample_workspace_bytes(B, n);
+  if (workspace && workspace_bytes < need)
+    return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  a.idx = idx;
+  a.token = token;
+  a.prob = prob;
+  a.probs = probs;
+  LRH_HIP(lrh::launch_sample(a, B, workspace, static_cast<hipStream_t>(stream)), "sampling launch");
+  return LRHEAD_OK;
+}
+
+size_t lrhead_verify_workspace_bytes(int dtype, int64_t B, int s, int64_t n) {
+  if (s < 0 || s > kVerifyMaxS || check_sampling(dtype, B, s + 1, n) != LRHEAD_OK) return 0;
+  return lrh::verify_workspace_bytes(B > 0 ? B : 1, s, n);
+}
+
+int lrhead_verify(int dtype, const void* logits, int64_t ld, const int32_t* token, const int32_t* idx,
+                  const float* probs, int k, const int32_t* length, const float* u, const lrhead_sampling_t* how,
+                  int64_t B, int s, int64_t n, int32_t* out_token, int32_t* count, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (s < 0 || s > kVerifyMaxS) return fail(LRHEAD_ERANGE, "s = %d outside [0, %d]", s, kVerifyMaxS);
+  LRH_TRY(check_sampling(dtype, B, s + 1, n));
+  if (ld < n) return fail(LRHEAD_ERANGE, "ld = %lld below n = %lld", (long long)ld, (long long)n);
+  if ((idx == nullptr) != (probs == nullptr)) return fail(LRHEAD_EINVAL, "idx and probs go together");
+  if (idx && (k < 1 || k > LRHEAD_K_MAX)) return fail(LRHEAD_ERANGE, "k = %d outside [1, %d]", k, LRHEAD_K_MAX);
+  if (B == 0) return LRHEAD_OK;
+  lrh::SampleArgs a{};
+  LRH_TRY(sample_args(&a, dtype, logits, ld, u, how, n));
+  if ((!token && s > 0) || !workspace) return fail(LRHEAD_EINVAL, "token and workspace must be non-NULL");
+  if (!aligned4(token) || !aligned4(idx) || !aligned4(probs) || !aligned4(length) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "token, idx, probs and length must be 4-byte aligned, the workspace 16-byte");
+  LRH_TRY(check_out(out_token, "out_token", true));
+  LRH_TRY(check_out(count, "count", true));
+  const size_t need = lrh::verify_workspace_bytes(B, s, n);
+  if (workspace_bytes < need)
+    return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  a.token = out_token;
+  lrh::VerifyArgs v{};
+  v.s = s;
+  v.k = idx ? k : 1;
+  v.drafted = token;
+  v.list = idx;
+  v.q = probs;
+  v.length = length;
+  v.count = count;
+  LRH_HIP(lrh::launch_verify(a, v, B, workspace, static_cast<hipStream_t>(stream)), "verification launch");
+  return LRHEAD_OK;
+}
+
+int lrhead_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* token, int64_t N, float scale,
+                 void* out, void* stream) {
+  LRH_TRY(check_embed(dtype, V, d, N));
+  if (!std::isfinite(scale)) return fail(LRHEAD_ERANGE, "scale is not finite");
+  if (N == 0) return LRHEAD_OK;
+  if (!W || !token || !out) return fail(LRHEAD_EINVAL, "W, token and out must be non-NULL");
+  if (!aligned_elem(W, dtype) || !aligned_elem(out, dtype) || !aligned4(token))
+    return fail(LRHEAD_EALIGN, "W, out and token must be aligned to their elements");
+  const size_t row = size_t(d) * elem_bytes(dtype);
+  if (overlap(out, size_t(N) * row, W, size_t(V) * row) || overlap(out, size_t(N) * row, token, size_t(N) * 4))
+    return fail(LRHEAD_EINVAL, "out overlaps W or token");
+  LRH_HIP(lrh::launch_embed(dtype, W, V, d, token, N, scale, out, static_cast<hipStream_t>(stream)),
+          "embedding launch");
+  return LRHEAD_OK;
+}
+
+size_t lrhead_embed_grad_workspace_bytes(int dtype, int64_t V, int64_t d, int64_t N) {
+  if (check_embed(dtype, V, d, N) != LRHEAD_OK) return 0;
+  return N > 0 ? lrh::embed_grad_workspace_bytes(dtype, V, d, N) : 256;
+}
+
+int lrhead_embed_grad(int dtype, const void* dY, const int32_t* token, int64_t N, int64_t V, int64_t d, float scale,
+                      int add, void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  LRH_TRY(check_embed(dtype, V, d, N));
+  if (!std::isfinite(scale)) return fail(LRHEAD_ERANGE, "scale is not finite");
+  if (!dW || (N > 0 && (!dY || !token || !workspace)))
+    return fail(LRHEAD_EINVAL, "dY, token, dW and workspace must be non-NULL");
+  if (!aligned_elem(dY, dtype) || !aligned_elem(dW, dtype) || !aligned4(token) || !aligned16(workspace))
+    return fail(LRHEAD_EALIGN, "dY, dW and token must be aligned to their elements, the workspace to 16 bytes");
+  const size_t row = size_t(d) * elem_bytes(dtype);
+  if (N > 0) {
+    const size_t need = lrh::embed_grad_workspace_bytes(dtype, V, d, N);
+    if (workspace_bytes < need)
+      return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+    if (overlap(dW, size_t(V) * row, dY, size_t(N) * row) || overlap(dW, size_t(V) * row, token, size_t(N) * 4))
+      return fail(LRHEAD_EINVAL, "dW overlaps dY or token");
+  }
+  LRH_HIP(lrh::launch_embed_grad(dtype, dY, token, N, V, d, scale, add != 0, dW, workspace,
+                                 static_cast<hipStream_t>(stream)),
+          "embedding gradient launch");
   return LRHEAD_OK;
 }
 
