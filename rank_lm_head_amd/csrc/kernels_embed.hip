@@ -82,10 +82,10 @@ constexpr int kEmbedChunks = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
   constexpr int EP = Elems<T>::n;
-  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
-  const int64_t n = w / a.pieces;
+  const uint32_t w = blockIdx.x * kWaves + wave_id(), n32 = w / (uint32_t)a.pieces;   // w < 2^26
+  const int64_t n = n32;
   if (n >= a.N) return;
-  const int64_t c0 = (w % a.pieces) * (kEmbedChunks * kWave * EP) + (threadIdx.x & 63) * EP;
+  const int64_t c0 = (int64_t)(w - n32 * a.pieces) * (kEmbedChunks * kWave * EP) + (threadIdx.x & 63) * EP;
   const int t = a.token[n];
   const bool have = t >= 0 && t < a.V;
   const T* src = static_cast<const T*>(a.W) + (have ? (int64_t)t * a.d : 0);
@@ -446,10 +446,10 @@ constexpr int kAhead = 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(GradArgs a) {
   constexpr int EP = Elems<T>::n;
-  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
-  const int64_t chunk = w / a.pieces;
+  const uint32_t w = blockIdx.x * kWaves + wave_id();   // below 2^26
+  const int64_t chunk = w / (uint32_t)a.pieces;
   if (chunk >= a.chunks) return;
-  const int piece = (int)(w % a.pieces), lane = threadIdx.x & 63;
+  const int piece = (int)(w - (uint32_t)chunk * a.pieces), lane = threadIdx.x & 63;
   const int64_t c = (int64_t)piece * (kWave * EP) + lane * EP;
   const int64_t p0 = chunk * a.chunk, p1 = min(a.N, p0 + a.chunk);
   const uint32_t *keys = a.key[0], *at = a.at[0];
@@ -511,10 +511,10 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(GradArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(GradArgs a) {
   constexpr int EP = Elems<T>::n;
-  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
-  const int64_t chunk = w / a.pieces;
+  const uint32_t w = blockIdx.x * kWaves + wave_id();   // below 2^26
+  const int64_t chunk = w / (uint32_t)a.pieces;
   if (chunk + 1 >= a.chunks) return;   // nothing behind it
-  const int piece = (int)(w % a.pieces), lane = threadIdx.x & 63;
+  const int piece = (int)(w - (uint32_t)chunk * a.pieces), lane = threadIdx.x & 63;
   const int64_t c = (int64_t)piece * (kWave * EP) + lane * EP;
   const uint32_t* keys = a.key[0];
   const int64_t p0 = chunk * a.chunk, p1 = p0 + a.chunk;

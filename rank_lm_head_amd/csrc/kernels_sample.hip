@@ -41,29 +41,42 @@ constexpr int kGroups = kTile / kGroup;     // of a tile
 constexpr int kPer = kTile / kWave;         // columns of a lane
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / kWave;
-constexpr int kBins = 2048;
-constexpr int kBinsPer = kBins / kRowThreads;
-constexpr int kList = 4096;                 // columns that a row's block holds in LDS
-constexpr int kAskGroups = 2 * kRowThreads; // groups looked at a time
+constexpr int kList = 2048;                 // columns that a row's block holds in LDS
+constexpr int kValueBins = 2048;            // of a whole row's logits, even in value
 constexpr double kLog2e = 1.4426950408889634;
-constexpr int kFirstK = 32, kSecondK = 512; // groups' maxima above the bound of top_p's first and second try
+constexpr int kFirstK = 40, kSecondK = 512; // groups' maxima above the bound of top_p's first and second try
 
 // 2^t of -1000 <= t <= 0 to 4e-14: 2^f = 1 + f g(f) for |f| <= 1/2, g by
-// interpolation at the Chebyshev nodes.
-__device__ __forceinline__ double exp2_f64(double t) {
-  t = fmax(t, -1000.0);
-  const double n = rint(t), f = t - n;
-  double g = 1.0203121063391729e-07;
-  g = fma(g, f, 1.3255224878668817e-06);
-  g = fma(g, f, 1.525268684626772e-05);
-  g = fma(g, f, 0.00015403455852453838);
-  g = fma(g, f, 0.0013333558179043112);
-  g = fma(g, f, 0.009618129159402558);
-  g = fma(g, f, 0.055504108664760424);
-  g = fma(g, f, 0.2402265069581299);
-  g = fma(g, f, 0.6931471805599453);
-  return ldexp(fma(g, f, 1.0), (int)n);
-}
+// interpolation at the Chebyshev nodes. The nearest integer comes from the
+// addition of 1.5 2^52, whose low bits hold it, and goes into the exponent as
+// bits: conversions and ldexp of doubles run at a quarter of an addition's
+// rate. The coefficients stand in scalar registers that the compiler knows
+// nothing about; otherwise it copies each into a sum's register first.
+struct Exp2 {
+  double c0, c1, c2, c3, c4, c5, c6, c7, c8;
+  __device__ __forceinline__ Exp2()
+      : c0(1.0203121063391729e-07), c1(1.3255224878668817e-06), c2(1.525268684626772e-05), c3(0.00015403455852453838),
+        c4(0.0013333558179043112), c5(0.009618129159402558), c6(0.055504108664760424), c7(0.2402265069581299),
+        c8(0.6931471805599453) {
+    asm("" : "+v"(c0), "+s"(c1), "+s"(c2), "+s"(c3), "+s"(c4), "+s"(c5), "+s"(c6), "+s"(c7), "+s"(c8));
+  }
+  __device__ __forceinline__ double in_range(double t) const {
+    const double big = 6755399441055744.0;
+    const double r = t + big, f = t - (r - big);
+    double g = fma(c0, f, c1);
+    g = fma(g, f, c2);
+    g = fma(g, f, c3);
+    g = fma(g, f, c4);
+    g = fma(g, f, c5);
+    g = fma(g, f, c6);
+    g = fma(g, f, c7);
+    g = fma(g, f, c8);
+    const uint64_t w = (uint64_t)__double_as_longlong(fma(g, f, 1.0));
+    const uint32_t n = (uint32_t)__double_as_longlong(r);
+    return __longlong_as_double((long long)((uint64_t)((uint32_t)(w >> 32) + (n << 20)) << 32 | (uint32_t)w));
+  }
+  __device__ __forceinline__ double operator()(double t) const { return in_range(fmax(t, -1000.0)); }
+};
 
 // 16 bytes from an address aligned to its elements only.
 __device__ __forceinline__ u32x4 load16_any(const void* p) {
@@ -157,9 +170,6 @@ __device__ __forceinline__ uint64_t to_int(double w, int bits) {   // w 2^bits, 
   return (uint64_t)__double_as_longlong(fma(w, __longlong_as_double((long long)(1023 + bits) << 52), 4503599627370496.0)) &
          0xfffffffffffffull;
 }
-__device__ __forceinline__ uint64_t int_weight(float x, float m, double c, int bits) {
-  return to_int(exp2_f64(log_weight(x, m, c)), bits);
-}
 
 // What the kept mass before a column has to stay below: p of the mass, 1 at least.
 __device__ __forceinline__ uint64_t share_of(uint64_t mass, double p) {
@@ -171,61 +181,92 @@ __device__ __forceinline__ uint64_t place_of(uint64_t mass, float u) {
   return min((uint64_t)t, mass - 1);
 }
 
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t x) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) x += __shfl_xor((unsigned long long)x, o);
-  return x;
+__device__ __forceinline__ uint64_t rl64(uint64_t x, int lane) {
+  return (uint64_t)rl((uint32_t)(x >> 32), lane) << 32 | rl((uint32_t)x, lane);
 }
+template <int Ctrl>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t x) {
+  return (uint64_t)dpp_u32<Ctrl>((uint32_t)(x >> 32)) << 32 | dpp_u32<Ctrl>((uint32_t)x);
+}
+// Sums over a wave, in every lane: rows of 16 lanes by DPP, then the four rows.
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t x) {
+  x += dpp_u64<0xB1>(x);
+  x += dpp_u64<0x4E>(x);
+  x += dpp_u64<0x141>(x);
+  x += dpp_u64<0x140>(x);
+  return (rl64(x, 0) + rl64(x, 16)) + (rl64(x, 32) + rl64(x, 48));
+}
+__device__ __forceinline__ double as_f64(uint64_t x) { return __longlong_as_double((long long)x); }
+__device__ __forceinline__ uint64_t as_u64(double x) { return (uint64_t)__double_as_longlong(x); }
 __device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-  return x;
+  x += as_f64(dpp_u64<0xB1>(as_u64(x)));
+  x += as_f64(dpp_u64<0x4E>(as_u64(x)));
+  x += as_f64(dpp_u64<0x141>(as_u64(x)));
+  x += as_f64(dpp_u64<0x140>(as_u64(x)));
+  return (as_f64(rl64(as_u64(x), 0)) + as_f64(rl64(as_u64(x), 16))) +
+         (as_f64(rl64(as_u64(x), 32)) + as_f64(rl64(as_u64(x), 48)));
+}
+template <int Ctrl>
+__device__ __forceinline__ uint64_t dpp_shr_u64(uint64_t x) {
+  return (uint64_t)dpp_shr_or_0<Ctrl>((uint32_t)(x >> 32)) << 32 | dpp_shr_or_0<Ctrl>((uint32_t)x);
 }
 __device__ __forceinline__ uint64_t wave_incl_scan_u64(uint64_t x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t y = __shfl_up((unsigned long long)x, o);
-    x += lane >= o ? y : 0;
-  }
-  return x;
+  x += dpp_shr_u64<0x111>(x);
+  x += dpp_shr_u64<0x112>(x);
+  x += dpp_shr_u64<0x114>(x);
+  x += dpp_shr_u64<0x118>(x);
+  const int row = (threadIdx.x & 63) >> 4;
+  const uint64_t r0 = rl64(x, 15), r1 = r0 + rl64(x, 31), r2 = r1 + rl64(x, 47);
+  return x + (row == 0 ? 0 : row == 1 ? r0 : row == 2 ? r1 : r2);
 }
 __device__ __forceinline__ float wave_max_f32(float x) {
   return __uint_as_float(order_key_inv(wave_max_u32(order_key(x))));
 }
-__device__ __forceinline__ uint64_t rl64(uint64_t x, int lane) {
-  return (uint64_t)rl((uint32_t)(x >> 32), lane) << 32 | rl((uint32_t)x, lane);
-}
+
+// Waits until the wave's stores and atomics have reached the memory that all
+// compute units see: relaxed atomics of device scope go there without a stop in
+// a cache, so that this wait between two of them, and a barrier between waves,
+// orders them. (A release fence would write back the whole L2: heavy rows took
+// 1100 us with it.)
+__device__ __forceinline__ void wait_memory() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // ---------------------------------------------------------------- the stream
 
-// The tile's columns of a lane: 16-byte chunks, neighbouring lanes on
+// The first column that a tile's wave reads: the last tile of a row is read
+// from as far back as makes it whole, without its neighbour's columns.
+__device__ __forceinline__ int tile_base(const Args& a, int tile) {
+  return a.n < kTile ? 0 : min(tile * kTile, a.n - kTile);
+}
+// A lane's columns from there: 16-byte chunks, neighbouring lanes on
 // neighbouring chunks.
 template <typename T>
-__device__ __forceinline__ int tile_col(int tile, int i) {
+__device__ __forceinline__ int lane_col(int i) {
   constexpr int EP = Elems<T>::n;
-  return tile * kTile + ((i / EP) * kWave + (int)(threadIdx.x & 63)) * EP + i % EP;
+  return ((i / EP) * kWave + (int)(threadIdx.x & 63)) * EP + i % EP;
 }
 template <typename T>
 __device__ __forceinline__ void load_tile(const Args& a, int64_t row, int tile, float (&v)[kPer]) {
   constexpr int EP = Elems<T>::n;
-  const T* x = static_cast<const T*>(a.x) + row * a.ld;
+  const int base = tile_base(a, tile);
+  const T* x = static_cast<const T*>(a.x) + row * a.ld + base;
+  if (a.n >= kTile) {
+    u32x4 w[kPer / EP];
 #pragma unroll
-  for (int i = 0; i < kPer; i += EP) {
-    const int col = tile_col<T>(tile, i);
-    if (col + EP <= a.n) {
-      const u32x4 w = load16_any(x + col);
+    for (int i = 0; i < kPer / EP; ++i) w[i] = load16_any(x + lane_col<T>(i * EP));
 #pragma unroll
-      for (int e = 0; e < EP; ++e) v[i + e] = tame(Elems<T>::get(w, e));
-    } else {
+    for (int i = 0; i < kPer; ++i) v[i] = tame(Elems<T>::get(w[i / EP], i % EP));
+    if (base < tile * kTile) {
 #pragma unroll
-      for (int e = 0; e < EP; ++e) v[i + e] = col + e < a.n ? tame(Elems<T>::one(x + col + e)) : neg_inf();
+      for (int i = 0; i < kPer; ++i) v[i] = base + lane_col<T>(i) < tile * kTile ? neg_inf() : v[i];
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = lane_col<T>(i) < a.n ? tame(Elems<T>::one(x + lane_col<T>(i))) : neg_inf();
   }
   if (a.idx) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int col = tile_col<T>(tile, i);
+      const int col = base + lane_col<T>(i);
       if (col < a.n && a.idx[row * a.n + col] < 0) v[i] = neg_inf();
     }
   }
@@ -234,13 +275,14 @@ __device__ __forceinline__ void load_tile(const Args& a, int64_t row, int tile, 
 template <typename T, bool VERIFY>
 __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
   constexpr int EP = Elems<T>::n, CH = kPer / EP;   // chunks of a lane: one per group of 64 * EP columns
-  const int64_t w = (int64_t)blockIdx.x * kWaves + wave_id();
-  const int64_t row = w / a.tiles;
+  const uint32_t w = blockIdx.x * kWaves + wave_id();   // below 2^26: 32-bit divisions do
+  const uint32_t row32 = w / (uint32_t)a.tiles;
+  const int64_t row = row32;
   if (row >= a.rows) return;
-  const int tile = (int)(w % a.tiles), lane = threadIdx.x & 63;
-  const int64_t seq = row / a.per;
+  const int tile = (int)(w - row32 * a.tiles), lane = threadIdx.x & 63;
+  const int64_t seq = VERIFY ? row32 / (uint32_t)a.per : row32;
   if constexpr (VERIFY) {
-    const int j = (int)(row % a.per);
+    const int j = (int)(row32 - (uint32_t)seq * a.per);
     if (j == 0 && tile == 0 && lane == 0) a.arrived[seq] = 0;
     if (a.length && j > max(a.length[seq], 0)) return;   // no such position
   }
@@ -273,10 +315,16 @@ __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
   if (!h.mass()) return;
   double s = 0.0;
   if (m > neg_inf()) {
+    const Exp2 exp2;
+    const float low = fmaxf((float)((double)m - 990.0 / h.c - fabs((double)m) * 1e-6), -__FLT_MAX__);
+    const double t = log_weight(low, m, h.c);
+    if (t >= -1000.0 && t <= -900.0 && fabs((double)m) * h.c < 4096.0) {   // what is 2^-900 of the maximum and less, -inf among it, counts as nothing
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const double e = exp2_f64(log_weight(fmaxf(v[i], -__FLT_MAX__), m, h.c));
-      s += v[i] > neg_inf() ? e : 0.0;
+      for (int i = 0; i < kPer; ++i) s += exp2.in_range(log_weight(fmaxf(v[i], low), m, h.c));
+    } else {   // temperatures at which the lowest fp32 weighs something, maxima beside which 990 / c is lost
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        s += v[i] > neg_inf() ? exp2(log_weight(fmaxf(v[i], -__FLT_MAX__), m, h.c)) : 0.0;
     }
     s = wave_sum_f64(s);
   }
@@ -308,6 +356,33 @@ struct Less {
   }
 };
 
+// Items of a wave's lanes in LDS: every lane reads each in turn. (The same
+// loops over readlane took six times as long: 64-bit compares with scalars.)
+struct Item {
+  uint64_t key, w;
+};
+__device__ __forceinline__ void wave_put(Item* items, uint64_t key, uint64_t w) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  items[threadIdx.x & 63] = Item{key, w};
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+// How many of the n items have larger keys, and their weight.
+__device__ __forceinline__ uint64_t wave_before(const Item* items, int n, uint64_t key, int& rank) {
+  uint64_t before = 0;
+  rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const Item it = items[j];
+    const bool first = it.key > key;
+    rank += first;
+    before += first ? it.w : 0;
+  }
+  return before;
+}
+
 // One wave, a column per lane: what is kept of the keys.
 struct Kept {
   uint64_t w;       // the lane's weight, 0 where it is not kept
@@ -315,20 +390,15 @@ struct Kept {
 };
 // n: lanes that hold keys. all: the row's mass if top_p goes by it (no
 // top_k), else 0.
-__device__ __forceinline__ Kept wave_keep(uint64_t key, float m, const How& h, int bits, int n, uint64_t all) {
+__device__ __forceinline__ Kept wave_keep(uint64_t key, float m, const How& h, int bits, int n, uint64_t all,
+                                          Item* items) {
   const double t = log_weight(key ? key_score(key) : m, m, h.c);
-  uint64_t w = key ? to_int(exp2_f64(t), bits) : 0;
+  const uint64_t w = key ? to_int(Exp2()(t), bits) : 0;
   bool in = key != 0;
   if (h.top_k || h.top_p < 1.0) {
-    int rank = 0;
-    uint64_t before = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t kj = rl64(key, j), wj = rl64(w, j);
-      if (kj > key) {
-        ++rank;
-        before += wj;
-      }
-    }
+    wave_put(items, key, w);
+    int rank;
+    const uint64_t before = wave_before(items, n, key, rank);
     if (h.top_k) in = in && rank < h.top_k;
     if (h.top_p < 1.0) {
       const uint64_t mass = all ? all : wave_sum_u64(in ? w : 0);
@@ -342,15 +412,12 @@ __device__ __forceinline__ Kept wave_keep(uint64_t key, float m, const How& h, i
   return k;
 }
 // The lane whose column holds u's place in the mass (> 0), columns in the
-// order of col.
-__device__ __forceinline__ int wave_draw(uint64_t w, uint64_t mass, int col, float u, int n) {
+// order of col; columns are distinct.
+__device__ __forceinline__ int wave_draw(uint64_t w, uint64_t mass, int col, float u, int n, Item* items) {
   const uint64_t at = place_of(mass, u);
-  uint64_t before = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint64_t wj = rl64(w, j);
-    const int cj = (int)rl((uint32_t)col, j);
-    if (cj < col) before += wj;
-  }
+  wave_put(items, ~(uint64_t)(uint32_t)col, w);
+  int rank;
+  const uint64_t before = wave_before(items, n, ~(uint64_t)(uint32_t)col, rank);
   const unsigned long long hit = __ballot(before <= at && at - before < w);
   return __ffsll(hit) - 1;
 }
@@ -358,8 +425,10 @@ __device__ __forceinline__ int wave_draw(uint64_t w, uint64_t mass, int col, flo
 // Rows of at most 64 columns: a wave per row, a lane per column.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_lists_kernel(Args a) {
+  __shared__ Item lds[kWaves][kWave];
   const int64_t row = (int64_t)blockIdx.x * kWaves + wave_id();
   if (row >= a.rows) return;
+  Item* items = lds[wave_id()];
   const int lane = threadIdx.x & 63;
   const How h = how_of(a, row);
   float x = lane < a.n ? tame(Elems<T>::one(static_cast<const T*>(a.x) + row * a.ld + lane)) : neg_inf();
@@ -370,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) sample_lists_kernel(Args a) {
   }
   const float m = wave_max_f32(x);
   const bool none = !(m > neg_inf());
-  Kept k = wave_keep(key_of(x, lane), none ? 0.f : m, h, a.bits, a.n, 0);
+  Kept k = wave_keep(key_of(x, lane), none ? 0.f : m, h, a.bits, a.n, 0, items);
   if (none) k.w = 0;
   if (a.probs && lane < a.n) a.probs[row * a.n + lane] = none ? 0.f : (float)((double)k.w / (double)k.mass);
   if (none) {
@@ -380,31 +449,34 @@ __global__ void __launch_bounds__(kThreads) sample_lists_kernel(Args a) {
     }
     return;
   }
-  const int at = wave_draw(k.w, k.mass, lane, a.u[row * a.u_ld], a.n);
+  const int at = wave_draw(k.w, k.mass, lane, a.u[row * a.u_ld], a.n, items);
   if (lane == at) {
     a.token[row] = id;
     if (a.prob) a.prob[row] = (float)((double)k.w / (double)k.mass);
   }
 }
 
+// A block runs most of what follows once, from cold instruction caches, so
+// that loops stay rolled and each part stands in the code once: unrolled, the
+// same steps took two to four times as long (256 rows under top_k 200: 105 us).
 struct Lds {
-  uint64_t mass[kBins];
-  uint32_t count[kBins];
-  uint64_t list[kList];
-  uint64_t few[kWave];
-  uint64_t sum[kRowWaves + 2];
+  uint64_t key[kList], w[kList];   // the list, and its weights
+  uint64_t mass[kRowThreads];
+  uint32_t count[kValueBins];
+  Item items[kWave];
+  uint64_t sum[kRowWaves];
   uint64_t out[4];
-  int ask[kAskGroups];
-  int n_ask, n_list, n_few, pick;
+  int ask[2 * kRowThreads];
+  int n_ask, n_list, pick;
   int32_t id[64];
   float q[64];
   int tile[64];             // of the list's tokens, and what they take from it
   uint64_t gone[64];
 };
 
+// A barrier has to lie between a call of either and the next.
 __device__ __forceinline__ uint64_t block_sum(uint64_t x, Lds& s) {
   x = wave_sum_u64(x);
-  __syncthreads();
   if ((threadIdx.x & 63) == 0) s.sum[wave_id()] = x;
   __syncthreads();
   uint64_t all = 0;
@@ -415,7 +487,6 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t x, Lds& s) {
 // Exclusive prefix over the threads; all: the total.
 __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t& all, Lds& s) {
   const uint64_t incl = wave_incl_scan_u64(x);
-  __syncthreads();
   if ((threadIdx.x & 63) == 63) s.sum[wave_id()] = incl;
   __syncthreads();
   uint64_t before = incl - x;
@@ -423,164 +494,153 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t& all, Lds& s
   const int wave = wave_id();
 #pragma unroll
   for (int w = 0; w < kRowWaves; ++w) {
-    if (w < wave) before += s.sum[w];
-    all += s.sum[w];
+    const uint64_t y = s.sum[w];
+    before += w < wave ? y : 0;
+    all += y;
   }
   return before;
 }
 
-// Of elements (key, weight) the last, in descending order of distinct keys
-// from hi to lo, before which less than `target` (> 0) weight lies.
-// each(lo, hi, f) calls f(key, weight) for the calling thread's elements with
-// a weight above 0 in [lo, hi]; at least one there is. Halves the range of keys
-// by 2^11 a step until at most `most` elements are left; these are put into
-// `list` and n is their number (0: the element was found, its key is lo).
+// Part of an order of distinct 64-bit keys, larger first: those in [lo, hi],
+// and how much weight may lie before the last one sought, `target` > 0 of it.
 struct Range {
   uint64_t lo, hi, target;
   int n;
 };
-template <typename Each>
-__device__ __forceinline__ Range block_narrow(const Each& each, Range r, int most, uint64_t* list, int* n_list, Lds& s) {
+// One step towards the last key before which less than `target` weight lies:
+// the range is cut into 512 bins whose weights and counts are in s.mass and
+// s.count, and becomes the bin that holds it, with n keys.
+__device__ __forceinline__ int shift_of(const Range& r) { return max(0, 64 - __clzll((long long)(r.hi - r.lo)) - 9); }
+__device__ __forceinline__ void bins_begin(Lds& s) {
+  __syncthreads();
+  s.mass[threadIdx.x] = 0;
+  s.count[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    s.pick = -1;
+    s.n_ask = 0;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void bins_add(uint64_t key, uint64_t w, const Range& r, int shift, Lds& s) {
+  const int bin = (int)((r.hi - key) >> shift);
+  atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[bin]), (unsigned long long)w);
+  atomicAdd(&s.count[bin], 1u);
+}
+__device__ __forceinline__ Range bins_pick(Range r, int shift, Lds& s) {
   const int tid = threadIdx.x;
-  for (;;) {
-    const uint64_t span = r.hi - r.lo;
-    if (!span) {
-      r.n = 0;
-      return r;
+  __syncthreads();
+  uint64_t all;
+  const uint64_t before = block_scan(s.mass[tid], all, s);
+  const uint32_t c = s.count[tid];
+  if (c && before < r.target) atomicMax(&s.pick, tid);
+  __syncthreads();
+  const int pick = s.pick;
+  if (tid == pick) {
+    s.out[0] = before;
+    s.out[1] = c;
+  }
+  __syncthreads();
+  if (pick < 0) {   // no key with weight: not by any call here
+    r.lo = r.hi;
+    r.n = 1;
+    return r;
+  }
+  const uint64_t top = r.hi - ((uint64_t)pick << shift), width = (1ull << shift) - 1;
+  r.lo = top - r.lo > width ? top - width : r.lo;
+  r.hi = top;
+  r.target -= s.out[0];
+  r.n = (int)s.out[1];
+  return r;
+}
+
+// The last key & mask of the list's n before which less than the target lies,
+// by weight or, with `ones`, by count; keys of weight 0 do not count.
+__device__ __forceinline__ uint64_t list_find(Range r, int n, uint64_t mask, bool ones, Lds& s) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  do {
+    if (r.lo >= r.hi) return r.lo;
+    const int shift = shift_of(r);
+    bins_begin(s);
+#pragma unroll 1
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t k = s.key[i] & mask, w = ones ? 1 : s.w[i];
+      if (w && k >= r.lo && k <= r.hi) bins_add(k, w, r, shift, s);
     }
-    const int shift = max(0, 64 - __clzll((long long)span) - 11);
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kRowThreads) {
-      s.mass[i] = 0;
-      s.count[i] = 0;
-    }
-    if (tid == 0) s.pick = -1;
-    __syncthreads();
-    each(r.lo, r.hi, [&](uint64_t key, uint64_t w) {
-      const int bin = (int)((r.hi - key) >> shift);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[bin]), (unsigned long long)w);
-      atomicAdd(&s.count[bin], 1u);
-    });
-    __syncthreads();
-    uint64_t w[kBinsPer], mine = 0, all;
-    uint32_t c[kBinsPer];
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) {
-      w[i] = s.mass[tid * kBinsPer + i];
-      c[i] = s.count[tid * kBinsPer + i];
-      mine += w[i];
-    }
-    uint64_t before = block_scan(mine, all, s);
-    int last = -1;
-    uint64_t last_before = 0;
-    uint32_t last_count = 0;
-#pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) {
-      if (c[i] && before < r.target) {
-        last = tid * kBinsPer + i;
-        last_before = before;
-        last_count = c[i];
-      }
-      before += w[i];
-    }
-    if (last >= 0) atomicMax(&s.pick, last);
-    __syncthreads();
-    if (last >= 0 && s.pick == last) {
-      s.out[0] = last_before;
-      s.out[1] = last_count;
-    }
-    __syncthreads();
-    if (s.pick < 0) {   // no element: not by any call here
-      r.lo = r.hi;
-      r.n = 0;
-      return r;
-    }
-    const uint64_t top = r.hi - ((uint64_t)s.pick << shift);
-    const uint64_t width = (1ull << shift) - 1;
-    r.lo = top - r.lo > width ? top - width : r.lo;
-    r.hi = top;
-    r.target -= s.out[0];
-    const int n = (int)s.out[1];
-    if (n <= most) {
-      if (tid == 0) *n_list = 0;
-      __syncthreads();
-      each(r.lo, r.hi, [&](uint64_t key, uint64_t) {
-        const int at = atomicAdd(n_list, 1);
-        if (at < most) list[at] = key;
-      });
-      __syncthreads();
-      r.n = n;
-      return r;
+    r = bins_pick(r, shift, s);
+  } while (r.n > kWave);
+#pragma unroll 1
+  for (int i = tid; i < n; i += kRowThreads) {
+    const uint64_t k = s.key[i] & mask;
+    if (k >= r.lo && k <= r.hi && (ones || s.w[i])) {
+      const int at = atomicAdd(&s.n_ask, 1);
+      if (at < kWave) s.ask[at] = i;
     }
   }
-}
-// The element itself, of keys in LDS.
-template <typename Each, typename Weight>
-__device__ __forceinline__ uint64_t block_find(const Each& each, const Weight& weight, Range r, Lds& s) {
-  r = block_narrow(each, r, kWave, s.few, &s.n_few, s);
-  if (!r.n) return r.lo;
+  __syncthreads();
   if (wave_id() == 0) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t key = lane < r.n ? s.few[lane] : 0;
-    const uint64_t w = key ? weight(key) : 0;
-    uint64_t before = 0;
-    int rank = 0;
-    for (int j = 0; j < r.n; ++j) {
-      const uint64_t kj = rl64(key, j), wj = rl64(w, j);
-      if (kj > key) {
-        before += wj;
-        ++rank;
-      }
-    }
-    const int kept = wave_count(key && before < r.target);
-    if (key && rank == kept - 1) s.out[2] = key;
+    const int few = min(r.n, s.n_ask);
+    const bool have = lane < few;
+    const int i = have ? s.ask[lane] : 0;
+    const uint64_t k = have ? s.key[i] & mask : 0, w = have ? (ones ? 1 : s.w[i]) : 0;
+    wave_put(s.items, k, w);
+    int rank;
+    const uint64_t before = wave_before(s.items, few, k, rank);
+    const int kept = wave_count(have && before < r.target);
+    if (have && rank == kept - 1) s.out[2] = k;
   }
   __syncthreads();
   return s.out[2];
 }
 
-// A bound that at least k of the groups' maxima reach, as an order key: lane
-// by lane every 64th group (the largest of several where there are more than
-// 64 * kHeld). 0 where there are not so many. Every wave finds the same.
-constexpr int kHeld = 16;
-__device__ __forceinline__ uint32_t group_bound(const float* gmax, int groups, int k) {
-  const int lane = threadIdx.x & 63;
+// The groups' maxima of a row as order keys (0: no candidate), in every wave:
+// lane by lane every 64th. Of more groups than kHeldGroups, the largest of
+// several.
+constexpr int kHeld = 16, kHeldGroups = kHeld * kWave;
+struct GroupMax {
   uint32_t v[kHeld];
-  uint32_t lo = ~0u, hi = 0;
-#pragma unroll
-  for (int e = 0; e < kHeld; ++e) v[e] = 0;
-  for (int g0 = 0; g0 < groups; g0 += kWave * kHeld) {
+  __device__ __forceinline__ void load(const float* gmax, int g0, int groups) {
+    float x[kHeld];
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
-      const int g = g0 + e * kWave + lane;
-      const float x = g < groups ? gmax[g] : neg_inf();
-      if (x > neg_inf()) v[e] = max(v[e], order_key(x));
+      const int g = g0 + e * kWave + (threadIdx.x & 63);
+      x[e] = g < groups ? gmax[g] : neg_inf();
     }
-  }
-  int have = 0;
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e) {
-    have += wave_count(v[e] != 0);
-    hi = max(hi, v[e]);
-    if (v[e]) lo = min(lo, v[e]);
+    for (int e = 0; e < kHeld; ++e) v[e] = x[e] > neg_inf() ? order_key(x[e]) : 0;
   }
-  if (have < k) return 0;
-  lo = wave_min_u32(lo);
-  hi = wave_max_u32(hi);
-  while (lo < hi) {   // count(>= lo) >= k
-    const uint32_t mid = lo + (hi - lo + 1) / 2;
-    int c = 0;
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) c += wave_count(v[e] >= mid);
-    if (c >= k) {
-      lo = mid;
-      if (c <= k + k / 4) break;
-    } else {
-      hi = mid - 1;
+    for (int e = 0; e < kHeld; ++e) m = max(m, v[e]);
+    return wave_max_u32(m);
+  }
+  // A bound that at least k of them reach, and few more. 0 where there are not so many.
+  __device__ __forceinline__ uint32_t bound(int k, uint32_t hi) const {
+    uint32_t lo = ~0u;
+    int have = 0;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      have += wave_count(v[e] != 0);
+      lo = min(lo, v[e] ? v[e] : ~0u);
     }
+    if (have < k) return 0;
+    lo = wave_min_u32(lo);
+#pragma unroll 1
+    while (lo < hi) {   // count(>= lo) >= k
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) c += wave_count(v[e] >= mid);
+      if (c >= k) {
+        lo = mid;
+        if (c <= k + k / 4) break;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    return lo;
   }
-  return lo;
-}
+};
 
 template <typename T>
 struct RowCtx {
@@ -589,208 +649,346 @@ struct RowCtx {
   int64_t row;
   How h;
   float m;
+  Exp2 exp2;
   uint64_t thr;     // kept: keys from here on, of weight h.least at least
   uint64_t mass;    // kept, in all
+  uint64_t own;     // the mass of the tile of the thread's number, as the stream left it
 
+  // N columns; those that are not (col out of [from, end)) are no candidates.
+  // All loads are on their way before the first is looked at.
+  template <int N>
+  __device__ __forceinline__ void load(const int (&col)[N], int from, int end, float (&x)[N]) const {
+    const T* p = static_cast<const T*>(a.x) + row * a.ld;
+    T raw[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) raw[q] = p[min(col[q], a.n - 1)];
+    int id[N];
+    if (a.idx) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) id[q] = a.idx[row * a.n + min(col[q], a.n - 1)];
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      x[q] = tame(Elems<T>::one(&raw[q]));
+      if (col[q] < from || col[q] >= end || (a.idx && id[q] < 0)) x[q] = neg_inf();
+    }
+  }
   __device__ __forceinline__ float at(int col) const {
-    if (a.idx && a.idx[row * a.n + col] < 0) return neg_inf();
-    return tame(Elems<T>::one(static_cast<const T*>(a.x) + row * a.ld + col));
+    const int c[1] = {col};
+    float x[1];
+    load(c, 0, a.n, x);
+    return x[0];
   }
   __device__ __forceinline__ uint64_t key_at(int col) const { return key_of(at(col), col); }
-  __device__ __forceinline__ uint64_t weight(uint64_t key) const { return int_weight(key_score(key), m, h.c, a.bits); }
+  __device__ __forceinline__ uint64_t weight(uint64_t key) const {
+    return to_int(exp2(log_weight(key_score(key), m, h.c)), a.bits);
+  }
   // the kept weight, 0 of what is not kept
   __device__ __forceinline__ uint64_t kept(uint64_t key) const {
     if (!key || key < thr) return 0;
     const double t = log_weight(key_score(key), m, h.c);
-    return t >= h.least ? to_int(exp2_f64(t), a.bits) : 0;
+    return t >= h.least ? to_int(exp2(t), a.bits) : 0;
   }
-
-  // f(key) for all columns, a tile a wave
-  template <typename F>
-  __device__ __forceinline__ void each_col(const F& f) const {
-    for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
-      float v[kPer];
-      load_tile<T>(a, row, tile, v);
+  // Four neighbouring columns from each col[4 q] on, all of them there; no ids.
+  template <int N>
+  __device__ __forceinline__ void load4(const int (&col)[4 * N], float (&x)[4 * N]) const {
+    struct Raw {
+      T v[4];
+    } raw[N];
+    const T* p = static_cast<const T*>(a.x) + row * a.ld;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (v[i] > neg_inf()) f(cand_key(v[i], tile_col<T>(tile, i)));
+    for (int q = 0; q < N; ++q) __builtin_memcpy(&raw[q], p + col[4 * q], sizeof(Raw));
+#pragma unroll
+    for (int q = 0; q < 4 * N; ++q) x[q] = tame(Elems<T>::one(&raw[q / 4].v[q % 4]));
+  }
+  // f(x, col) for the calling lane's candidates in a tile of its wave's
+  template <typename F>
+  __device__ __forceinline__ void each_of_tile(int tile, const F& f) const {
+    const int end = min(a.n, (tile + 1) * kTile), lane = threadIdx.x & 63;
+#pragma unroll 1
+    for (int c0 = tile * kTile; c0 < end; c0 += 8 * kWave) {
+      int col[8];
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) col[q] = c0 + q / 4 * 4 * kWave + lane * 4 + q % 4;
+      if (c0 + 8 * kWave <= end && !a.idx) {
+        load4<2>(col, x);
+      } else {
+        load(col, 0, end, x);
       }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (x[q] > neg_inf()) f(x[q], col[q]);
     }
   }
 
   // LDS list of the columns that reach the bound, as keys; its length may be
-  // above kList, then the list is not whole.
-  __device__ __forceinline__ int gather(uint32_t bound) {
+  // above kList, then the list is not whole. A wave reads eight groups at a time.
+  __device__ __forceinline__ int gather(GroupMax& g, uint32_t bound) {
+    constexpr int kEach = kGroup / kWave, kAtOnce = 8;
     const int groups = a.tiles * kGroups;
-    const float* gmax = a.gmax + row * groups;
     const float least = bound ? __uint_as_float(order_key_inv(bound)) : -__FLT_MAX__;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const uint32_t key = max(bound, 1u);
+    const int lane = threadIdx.x & 63, wave = wave_id();
     __syncthreads();
-    if (tid == 0) s.n_list = 0;
-    for (int g0 = 0; g0 < groups; g0 += kAskGroups) {
+    if (threadIdx.x == 0) s.n_list = 0;
+#pragma unroll 1
+    for (int g0 = 0; g0 < groups; g0 += kHeldGroups) {
+      if (groups > kHeldGroups) g.load(a.gmax + row * groups, g0, groups);
+      if (threadIdx.x == 0) s.n_ask = 0;
       __syncthreads();
-      if (tid == 0) s.n_ask = 0;
-      __syncthreads();
-      for (int g = g0 + tid; g < min(groups, g0 + kAskGroups); g += kRowThreads)
-        if (gmax[g] >= least) s.ask[atomicAdd(&s.n_ask, 1)] = g;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) {
+        if (e % kRowWaves != wave) continue;
+        if (g.v[e] >= key) s.ask[atomicAdd(&s.n_ask, 1)] = g0 + e * kWave + lane;
+      }
       __syncthreads();
       const int n = s.n_ask;
-      for (int i = wave_id(); i < n; i += kRowWaves) {
-        const int c0 = s.ask[i] * kGroup + lane;
-        float v[kGroup / kWave];
+#pragma unroll 1
+      for (int i = wave * kAtOnce; i < n; i += kRowWaves * kAtOnce) {
+        int col[kAtOnce * kEach], from[kAtOnce];
+        float v[kAtOnce * kEach];
 #pragma unroll
-        for (int j = 0; j < kGroup / kWave; ++j) v[j] = c0 + j * kWave < a.n ? at(c0 + j * kWave) : neg_inf();
+        for (int q = 0; q < kAtOnce; ++q) {
+          const int grp = s.ask[min(i + q, n - 1)], tile = grp / kGroups;
+          const int c = tile_base(a, tile) + grp % kGroups * kGroup + lane * kEach;
+          from[q] = i + q < n ? tile * kTile : a.n;
 #pragma unroll
-        for (int j = 0; j < kGroup / kWave; ++j) {
-          if (v[j] >= least) {
-            const int p = atomicAdd(&s.n_list, 1);
-            if (p < kList) s.list[p] = cand_key(v[j], c0 + j * kWave);
+          for (int e = 0; e < kEach; ++e) col[q * kEach + e] = c + e;
+        }
+        if (a.n >= kTile && !a.idx) load4<kAtOnce>(col, v);   // whole groups
+        else load(col, 0, a.n, v);
+#pragma unroll
+        for (int q = 0; q < kAtOnce * kEach; ++q) v[q] = col[q] >= from[q / kEach] ? v[q] : neg_inf();
+        int some = 0;
+#pragma unroll
+        for (int q = 0; q < kAtOnce * kEach; ++q) some += v[q] >= least;
+        if (some) {
+          int p = atomicAdd(&s.n_list, some);
+#pragma unroll
+          for (int q = 0; q < kAtOnce * kEach; ++q) {
+            if (v[q] >= least) {
+              if (p < kList) s.key[p] = cand_key(v[q], col[q]);
+              ++p;
+            }
           }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
     return s.n_list;
   }
-
-  // thr and mass of the list, which holds all that may be kept. all: the
-  // row's mass for top_p without top_k.
-  __device__ __forceinline__ void keep_list(int n, uint32_t bound, uint64_t all) {
-    const auto ones = [&](uint64_t lo, uint64_t hi, auto f) {
-      for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const uint64_t k = s.list[i];
-        if (k >= lo && k <= hi) f(k, (uint64_t)1);
-      }
-    };
-    const auto weights = [&](uint64_t lo, uint64_t hi, auto f) {
-      for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const uint64_t k = s.list[i];
-        if (k >= lo && k <= hi) {
-          const uint64_t w = weight(k);
-          if (w) f(k, w);
-        }
-      }
-    };
-    const uint64_t hi = cand_key(m, 0);
-    thr = max((uint64_t)bound << 32, (uint64_t)1);
-    if (h.top_k && n > h.top_k)
-      thr = block_find(ones, [](uint64_t) { return (uint64_t)1; }, Range{thr, hi, (uint64_t)h.top_k, 0}, s);
-    if (h.top_p < 1.0) {
-      if (!all) {
-        uint64_t mine = 0;
-        weights(thr, hi, [&](uint64_t, uint64_t w) { mine += w; });
-        all = block_sum(mine, s);
-      }
-      const uint64_t p = block_find(weights, [&](uint64_t k) { return weight(k); },
-                                    Range{thr, hi, share_of(all, h.top_p), 0}, s);
-      thr = max(thr, p);
-    }
+  __device__ __forceinline__ uint64_t weigh_list(int n) const {   // the calling thread's share
     uint64_t mine = 0;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) mine += kept(s.list[i]);
-    mass = block_sum(mine, s);
-  }
-  __device__ __forceinline__ int draw_list(int n, float u, Less less) {
-    const auto weights = [&](uint64_t lo, uint64_t hi, auto f) {
-      for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const uint64_t k = (uint32_t)s.list[i];   // lower columns are larger
-        if (k >= lo && k <= hi) {
-          const uint64_t w = less.rest(kept(s.list[i]), key_id(s.list[i]));
-          if (w) f(k, w);
-        }
-      }
-    };
-    uint64_t total = mass;
-    if (less.k) {
-      uint64_t mine = 0;
-      weights(0, ~0ull, [&](uint64_t, uint64_t w) { mine += w; });
-      total = block_sum(mine, s);
-      if (!total) {
-        less.k = 0;
-        total = mass;
-      }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kRowThreads) {
+      const uint64_t w = weight(s.key[i]);
+      s.w[i] = w;
+      mine += w;
     }
-    const uint64_t k = block_find(weights, [&](uint64_t low) {
-      const int col = (int)(0xFFFFFFFFu - (uint32_t)low);
-      return less.rest(kept(key_at(col)), col);
-    }, Range{0xFFFFFFFFu - (uint32_t)(a.n - 1), 0xFFFFFFFFu, place_of(total, u) + 1, 0}, s);
-    return (int)(0xFFFFFFFFu - (uint32_t)k);
+    return mine;
   }
 
-  // The row as a whole: thr, mass, and the tiles' kept masses.
-  __device__ __forceinline__ void keep_row(uint64_t all) {
-    const uint64_t hi = cand_key(m, 0);
-    const auto ones = [&](uint64_t lo, uint64_t up, auto f) {
-      each_col([&](uint64_t k) {
-        if (k >= lo && k <= up) f(k, (uint64_t)1);
-      });
-    };
-    const auto weights = [&](uint64_t lo, uint64_t up, auto f) {
-      each_col([&](uint64_t k) {
-        if (k >= lo && k <= up) {
-          const uint64_t w = weight(k);
-          if (w) f(k, w);
+  // A tile's mass from the stream's sums, relative to the tile's maximum.
+  __device__ __forceinline__ uint64_t tile_mass(float t, double sum) const {
+    if (!(t > neg_inf())) return 0;
+    return (uint64_t)rint(sum * exp2(log_weight(t, m, h.c)) * (double)(1ull << a.bits));
+  }
+  __device__ __forceinline__ uint64_t tile_mass(int tile) const {
+    if (tile == (int)threadIdx.x) return own;
+    return tile_mass(a.tmax[row * a.tiles + tile], a.tsum[row * a.tiles + tile]);
+  }
+  // A tile's kept mass as an integer, where keep_row or split_row have put it.
+  __device__ __forceinline__ uint64_t* tile_ints() const {
+    return reinterpret_cast<uint64_t*>(a.tsum) + row * a.tiles;
+  }
+  __device__ __forceinline__ uint64_t tile_int(int tile) const {
+    return __hip_atomic_load(tile_ints() + tile, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+
+  // Whole rows under top_p alone. What is kept has a weight of (1 - p) / n of
+  // the mass at least, as all lighter columns together have less than 1 - p of
+  // it. Between that and the maximum, columns are counted in bins even in
+  // value, along with where in its bin each stands; that gives a bin's mass to
+  // about a millionth, and so the few bins in which the border must lie. A
+  // second pass sums what is above these, tile by tile, and lists what is in
+  // them, which also shows whether the border is there. False where it is not,
+  // where that is too much for the list, or min_p leaves more out; else thr and
+  // mass are known, and the tiles' ints.
+  __device__ __forceinline__ bool keep_row(uint64_t all) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const uint64_t share = share_of(all, h.top_p);
+    const double least = log2((1.0 - h.top_p) / a.n) * 1.001;   // the mass is 1 at least
+    const float f = (float)((double)kValueBins / least * -h.c);   // bins per unit of logit
+    if (!(f > 0.f && f < 1e30f) || h.least > -__builtin_inf()) return false;
+    const auto bin_of = [&](float x) { return (m - x) * f; };
+    uint64_t* bins = s.w;   // count << 40 | places in the bin, in 2^-16
+    static_assert(kValueBins == kList, "the bins stand where the list's weights will");
+    __syncthreads();
+    for (int i = tid; i < kValueBins; i += kRowThreads) bins[i] = 0;
+    if (tid == 0) {
+      s.n_list = 0;
+      s.pick = kValueBins - 1;
+      s.n_ask = kValueBins - 1;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
+      each_of_tile(tile, [&](float x, int) {
+        const float b = bin_of(x);
+        if (b < (float)kValueBins) {
+          const int i = (int)b;
+          atomicAdd(reinterpret_cast<unsigned long long*>(&bins[i]),
+                    1ull << 40 | (unsigned long long)((b - (float)i) * 65535.f));
         }
       });
-    };
-    int n = 0;
-    const auto list_ones = [&](uint64_t lo, uint64_t up, auto f) {
-      for (int i = threadIdx.x; i < n; i += kRowThreads)
-        if (s.list[i] >= lo && s.list[i] <= up) f(s.list[i], (uint64_t)1);
-    };
-    const auto list_weights = [&](uint64_t lo, uint64_t up, auto f) {
-      for (int i = threadIdx.x; i < n; i += kRowThreads)
-        if (s.list[i] >= lo && s.list[i] <= up) f(s.list[i], weight(s.list[i]));
-    };
-    thr = 1;
-    if (h.top_k) {
-      const Range r = block_narrow(ones, Range{1, hi, (uint64_t)h.top_k, 0}, kList, s.list, &s.n_list, s);
-      n = r.n;
-      thr = n ? block_find(list_ones, [](uint64_t) { return (uint64_t)1; }, r, s) : r.lo;
-    }
-    if (h.top_p < 1.0) {
-      if (!all) {
-        uint64_t mine = 0;
-        weights(thr, hi, [&](uint64_t, uint64_t w) { mine += w; });
-        all = block_sum(mine, s);
-      }
-      const Range r = block_narrow(weights, Range{thr, hi, share_of(all, h.top_p), 0}, kList, s.list, &s.n_list, s);
-      n = r.n;
-      thr = max(thr, n ? block_find(list_weights, [&](uint64_t k) { return weight(k); }, r, s) : r.lo);
-    }
-    uint64_t* sums = reinterpret_cast<uint64_t*>(a.tsum) + row * a.tiles;
-    uint64_t mine = 0;
-    for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
-      float v[kPer];
-      load_tile<T>(a, row, tile, v);
-      uint64_t w = 0;
+    __syncthreads();
+    // the bins through which the mass, off by 2^-13 of itself either way, reaches the share
+    constexpr int kEach = kValueBins / kRowThreads;
+    const double step = least / kValueBins;   // log2 of weight per bin
+    uint64_t w[kEach], mine = 0, total;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) w += kept(key_of(v[i], tile_col<T>(tile, i)));
+    for (int i = 0; i < kEach; ++i) {
+      const uint64_t b = bins[tid * kEach + i];
+      const double count = (double)(uint32_t)(b >> 40), place = (double)(b & 0xffffffffffull) * (1.0 / 65535.0);
+      // 2^(step x) = 1 + y x + (y x)^2 / 2 with y = step ln 2, the square's mean as of places spread evenly
+      const double y = step * 0.6931471805599453;
+      w[i] = (uint64_t)((count * (1.0 + y * y * (1.0 / 6.0)) + y * place) * exp2(step * (tid * kEach + i)) *
+                        (double)(1ull << a.bits));
+      mine += w[i];
+    }
+    const uint64_t before = block_scan(mine, total, s);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      uint64_t through = before;
+      const uint64_t at = side ? share + (share >> 13) : share - (share >> 13);
+      if (through < at && through + mine >= at) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          if (through < at && through + w[i] >= at) (side ? s.n_ask : s.pick) = tid * kEach + i;
+          through += w[i];
+        }
+      }
+    }
+    __syncthreads();
+    const float lo = (float)s.pick, hi = (float)(s.n_ask + 1);
+    mine = 0;
+    for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
+      uint64_t w = 0;
+      each_of_tile(tile, [&](float x, int col) {
+        const float b = bin_of(x);
+        if (b < lo) {
+          w += weight(cand_key(x, col));
+        } else if (b < hi) {
+          const int p = atomicAdd(&s.n_list, 1);
+          if (p < kList) s.key[p] = cand_key(x, col);
+        }
+      });
       w = wave_sum_u64(w);
-      if ((threadIdx.x & 63) == 0) {
-        sums[tile] = w;
+      if (lane == 0) {
+        __hip_atomic_store(tile_ints() + tile, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         mine += w;
       }
     }
+    wait_memory();
+    __syncthreads();
+    const int n = s.n_list;
+    const uint64_t above = block_sum(mine, s);
+    if (n > kList || n < 1 || above >= share) return false;
+    __syncthreads();
+    const uint64_t listed = block_sum(weigh_list(n), s);
+    if (above + listed < share && hi < (float)kValueBins) return false;
+    if (!listed) return false;
+    thr = list_find(Range{1, cand_key(m, 0), share - above, 0}, n, ~0ull, false, s);
+    mine = 0;
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t k = s.key[i];
+      if (k < thr) continue;
+      mine += s.w[i];
+      __hip_atomic_fetch_add(tile_ints() + key_id(k) / kTile, s.w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    wait_memory();
+    __syncthreads();
+    mass = above + block_sum(mine, s);
+    return true;
+  }
+
+  // Any row: the order of its keys is cut into bins until what is left of it
+  // fits the list, for top_k and for top_p, then the tiles' kept masses are summed.
+  __device__ __forceinline__ void split_row(uint64_t all) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const uint64_t hi = cand_key(m, 0);
+    thr = 1;
+#pragma unroll 1
+    for (int stage = 0; stage < 3; ++stage) {
+      // 0: top_k, 1: its mass, 2: top_p
+      if (stage == 0 ? !h.top_k : !(h.top_p < 1.0) || (stage == 1 && all)) continue;
+      const bool ones = stage == 0;
+      Range r{thr, hi, stage == 0 ? (uint64_t)h.top_k : stage == 2 ? share_of(all, h.top_p) : 1, kList + 1};
+      uint64_t mine = 0;
+      do {
+        const int shift = shift_of(r);
+        bins_begin(s);
+#pragma unroll 1
+        for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
+          each_of_tile(tile, [&](float x, int col) {
+            const uint64_t k = cand_key(x, col);
+            if (k < r.lo || k > r.hi) return;
+            const uint64_t w = ones ? 1 : weight(k);
+            if (stage == 1) mine += w;
+            else if (w) bins_add(k, w, r, shift, s);
+          });
+        if (stage == 1) break;
+        r = bins_pick(r, shift, s);
+      } while (r.n > kList && r.lo < r.hi);
+      if (stage == 1) {
+        __syncthreads();
+        all = block_sum(mine, s);
+        continue;
+      }
+      __syncthreads();
+      if (tid == 0) s.n_list = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
+        each_of_tile(tile, [&](float x, int col) {
+          const uint64_t k = cand_key(x, col);
+          if (k < r.lo || k > r.hi || (!ones && !weight(k))) return;
+          const int p = atomicAdd(&s.n_list, 1);
+          if (p < kList) s.key[p] = k;
+        });
+      __syncthreads();
+      const int n = min(s.n_list, kList);
+      weigh_list(n);
+      __syncthreads();
+      thr = max(thr, list_find(r, n, ~0ull, ones, s));
+    }
+    uint64_t mine = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
+      uint64_t w = 0;
+      each_of_tile(tile, [&](float x, int col) { w += kept(cand_key(x, col)); });
+      w = wave_sum_u64(w);
+      if (lane == 0) {
+        __hip_atomic_store(tile_ints() + tile, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        mine += w;
+      }
+    }
+    wait_memory();
+    __syncthreads();
     mass = block_sum(mine, s);
   }
 
-  // A tile's kept mass: an integer (keep_row), or of the sum relative to the tile's maximum.
-  __device__ __forceinline__ uint64_t tile_mass(int tile, bool ints) const {
-    const int64_t i = row * a.tiles + tile;
-    if (ints) return reinterpret_cast<const uint64_t*>(a.tsum)[i];
-    const float t = a.tmax[i];
-    if (!(t > neg_inf())) return 0;
-    return (uint64_t)rint(a.tsum[i] * exp2_f64(log_weight(t, m, h.c)) * (double)(1ull << a.bits));
-  }
-
-  // The draw over the tiles' masses, then inside the tile. The masses may be
-  // off by roundings; whatever they say, a column of weight 0 is never drawn.
+  // The draw over the tiles' masses (ints: those of keep_row and split_row),
+  // then inside the tile. The masses may be off by roundings; whatever they
+  // say, a column of weight 0 is never drawn.
   __device__ __forceinline__ int draw_tiles(bool ints, float u, Less less) {
     const int tid = threadIdx.x;
     const int each = (a.tiles + kRowThreads - 1) / kRowThreads;
     for (;;) {
+      __syncthreads();
       if (less.k) {   // what the list takes from its tokens' tiles
-        __syncthreads();
         if (tid < less.k) {
           const int col = less.id[tid];
           bool first = col >= 0 && col < a.n;
@@ -807,41 +1005,48 @@ struct RowCtx {
       }
       uint64_t mine = 0, total;
       const auto mass_of = [&](int tile) {
-        uint64_t w = tile_mass(tile, ints), gone = 0;
+        uint64_t w = ints ? tile_int(tile) : tile_mass(tile), gone = 0;
         for (int j = 0; j < less.k; ++j) gone += s.tile[j] == tile ? s.gone[j] : 0;
         return w > gone ? w - gone : 0;
       };
+      uint64_t one = 0;
       for (int i = 0; i < each; ++i) {
         const int tile = tid * each + i;
-        if (tile < a.tiles) mine += mass_of(tile);
+        one = tile < a.tiles ? mass_of(tile) : 0;
+        mine += one;
       }
       const uint64_t before = block_scan(mine, total, s);
+      uint64_t left = 0;
+      int tile = a.tiles;
       if (total) {
         const uint64_t at = place_of(total, u);
         if (before <= at && at - before < mine) {
           uint64_t b = before;
           for (int i = 0; i < each; ++i) {
-            const int tile = tid * each + i;
-            const uint64_t w = tile < a.tiles ? mass_of(tile) : 0;
+            const int t = tid * each + i;
+            const uint64_t w = each == 1 ? one : t < a.tiles ? mass_of(t) : 0;
             if (b <= at && at - b < w) {
-              s.pick = tile;
+              s.pick = t;
               s.out[0] = at - b;
             }
             b += w;
           }
         }
         __syncthreads();
-        uint64_t left = s.out[0];
-        for (int tile = s.pick; tile < a.tiles; ++tile) {
-          const int col = in_tile(tile, left, less, false);
-          if (col >= 0) return col;
-        }
+        left = s.out[0];
+        tile = s.pick;
       }
-      // a place behind all of them: the last column with weight
-      uint64_t none = 0;
-      for (int tile = a.tiles - 1; tile >= 0; --tile) {
-        const int col = in_tile(tile, none, less, true);
+      // forwards to the column that holds the place; from behind the last tile,
+      // backwards to the last column with weight
+      bool last = false;
+      while (tile >= 0) {
+        if (tile == a.tiles) {
+          last = true;
+          if (--tile < 0) break;
+        }
+        const int col = in_tile(tile, left, less, last);
         if (col >= 0) return col;
+        tile += last ? -1 : 1;
       }
       if (!less.k) return -1;   // only of a row without candidates
       less.k = 0;               // the list covers the target: the target itself
@@ -852,16 +1057,18 @@ struct RowCtx {
   __device__ __forceinline__ int in_tile(int tile, uint64_t& left, const Less& less, bool last) {
     constexpr int kEach = kTile / kRowThreads;
     const int tid = threadIdx.x;
+    int col[kEach];
+    float x[kEach];
     uint64_t w[kEach], mine = 0, total;
 #pragma unroll
+    for (int e = 0; e < kEach; ++e) col[e] = tile * kTile + tid * kEach + e;
+    load(col, 0, a.n, x);
+#pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const int col = tile * kTile + tid * kEach + e;
-      w[e] = 0;
-      if (col < a.n) {
-        w[e] = less.rest(kept(key_at(col)), col);
-      }
+      w[e] = less.rest(kept(key_of(x[e], col[e])), col[e]);
       mine += w[e];
     }
+    __syncthreads();
     const uint64_t before = block_scan(mine, total, s);
     if (!total) return -1;
     if (last) left = total - 1;
@@ -869,17 +1076,16 @@ struct RowCtx {
       left -= total;
       return -1;
     }
-    __syncthreads();
     if (before <= left && left - before < mine) {
       uint64_t b = before;
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        if (b <= left && left - b < w[e]) s.pick = tile * kTile + tid * kEach + e;
+        if (b <= left && left - b < w[e]) s.n_ask = col[e];
         b += w[e];
       }
     }
     __syncthreads();
-    return s.pick;
+    return s.n_ask;
   }
 };
 
@@ -888,12 +1094,11 @@ struct RowCtx {
 __device__ __forceinline__ void finish_sequence(const Args& a, int64_t seq, int drafted, Lds& s) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    s.pick = __hip_atomic_fetch_add(&a.arrived[seq], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)drafted;
+    wait_memory();
+    s.pick = __hip_atomic_fetch_add(&a.arrived[seq], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)drafted;
   }
   __syncthreads();
   if (!s.pick || wave_id() != 0) return;
-  __threadfence();
   const int lane = threadIdx.x & 63;
   const int32_t* state = a.state + seq * a.per;
   int taken = drafted;
@@ -917,26 +1122,33 @@ template <typename T, bool VERIFY>
 __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
   __shared__ Lds s;
   const int64_t row = blockIdx.x;
-  const int64_t seq = row / a.per;
-  const int j = (int)(row % a.per), tid = threadIdx.x, lane = tid & 63;
+  const int64_t seq = VERIFY ? blockIdx.x / (uint32_t)a.per : blockIdx.x;
+  const int j = VERIFY ? (int)(blockIdx.x - (uint32_t)seq * a.per) : 0, tid = threadIdx.x, lane = tid & 63;
   int drafted = a.per - 1;
   if constexpr (VERIFY) {
     if (a.length) drafted = min(max(a.length[seq], 0), a.per - 1);
     if (j > drafted) return;
   }
-  RowCtx<T> r{a, s, row, how_of(a, seq), neg_inf(), 1, 0};
+  // the row's maximum
+  const int groups = a.tiles * kGroups;
+  const float u = a.u[seq * a.u_ld + (VERIFY ? a.per - 1 : 0)];
+  const int64_t own = row * a.tiles + min(tid, a.tiles - 1);
+  const float own_max = a.tmax[own];
+  const double own_sum = a.tsum[own];
+  GroupMax g;
+  g.load(a.gmax + row * groups, 0, groups);
+  RowCtx<T> r{a, s, row, how_of(a, seq), neg_inf(), Exp2(), 1, 0, 0};
   const How& h = r.h;
-
-  // the row's maximum and mass
-  float m = neg_inf();
-  for (int t = tid; t < a.tiles; t += kRowThreads) m = fmaxf(m, a.tmax[row * a.tiles + t]);
-  m = wave_max_f32(m);
-  if (lane == 0) s.sum[wave_id()] = __float_as_uint(m);
-  __syncthreads();
+#pragma unroll 1
+  for (int g0 = kHeldGroups; g0 < groups; g0 += kHeldGroups) {
+    GroupMax more;
+    more.load(a.gmax + row * groups, g0, groups);
 #pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) m = fmaxf(m, __uint_as_float((uint32_t)s.sum[w]));
-  __syncthreads();
-  const bool none = !(m > neg_inf());
+    for (int e = 0; e < kHeld; ++e) g.v[e] = max(g.v[e], more.v[e]);
+  }
+  const uint32_t top = g.most();
+  const bool none = !top;
+  const float m = none ? neg_inf() : __uint_as_float(order_key_inv(top));
   r.m = m;
 
   // the list of a drafted position
@@ -959,17 +1171,18 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
       qx = less.of(x);
     }
   }
-  const float u = a.u[seq * a.u_ld + (VERIFY ? a.per - 1 : 0)];
 
   // what is kept: by one wave's lanes (way 0), by a list (1), by tiles (2: as
-  // read, 3: as integers)
+  // the stream left them, 3: as integers)
   int way = 2, n = 0;
   uint32_t bound = 0;
   uint64_t all = 0;
   if (!none) {
     if (h.mass()) {
-      uint64_t mine = 0;
-      for (int t = tid; t < a.tiles; t += kRowThreads) mine += r.tile_mass(t, false);
+      if (tid < a.tiles) r.own = r.tile_mass(own_max, own_sum);
+      uint64_t mine = r.own;
+#pragma unroll 1
+      for (int t = tid + kRowThreads; t < a.tiles; t += kRowThreads) mine += r.tile_mass(t);
       all = block_sum(mine, s);
     }
     if (h.whole()) {
@@ -982,18 +1195,17 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         const double f = (double)m + h.least / h.c;   // c = 0: -inf or NaN
         if (f > -(double)__FLT_MAX__) floor_key = order_key((float)(f - (fabs(f) + fabs((double)m)) * 1e-6));
       }
-      const int groups = a.tiles * kGroups;
+#pragma unroll 1
       for (int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : groups + 1;; k = kSecondK) {
-        bound = group_bound(a.gmax + row * groups, groups, k);
+        bound = g.bound(k, top);
         // all that can be kept is in a list that reaches down to top_k columns or to min_p
         bool enough = h.top_k || !bound || bound <= floor_key;
         if (!(h.top_k && h.top_p < 1.0)) bound = max(bound, floor_key);
-        n = r.gather(bound);
+        n = r.gather(g, bound);
         if (n > kList) break;
-        if (!enough) {   // or to top_p of the mass
-          uint64_t mine = 0;
-          for (int i = tid; i < n; i += kRowThreads) mine += r.weight(s.list[i]);
-          enough = block_sum(mine, s) >= share_of(all, h.top_p);
+        if (n > kWave || !enough) {
+          const uint64_t listed = block_sum(r.weigh_list(n), s);
+          enough = enough || listed >= share_of(all, h.top_p);   // or to top_p of the mass
         }
         if (enough) {
           way = n <= kWave ? 0 : 1;
@@ -1001,8 +1213,7 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         }
         if (k >= kSecondK) break;
       }
-      if (way == 1) r.keep_list(n, bound, all);
-      if (way == 3) r.keep_row(all);
+      if (way == 3 && !(h.mass() && r.keep_row(all))) r.split_row(all);
     }
   }
 
@@ -1013,8 +1224,8 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
     // nothing to draw
   } else if (way == 0) {
     if (wave_id() == 0) {
-      const uint64_t key = lane < n ? s.list[lane] : 0;
-      Kept k = wave_keep(key, m, h, a.bits, n, all);
+      const uint64_t key = lane < n ? s.key[lane] : 0;
+      Kept k = wave_keep(key, m, h, a.bits, n, all, s.items);
       const int col = key ? key_id(key) : a.n + lane;
       if (check) {
         const unsigned long long hit = __ballot(key && col == x);
@@ -1031,23 +1242,73 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
             mass = sum;
           }
         }
-        const int at = wave_draw(w, mass, col, u, n);
+        const int at = wave_draw(w, mass, col, u, n, s.items);
         drawn = __builtin_amdgcn_readlane(col, at);
         kept_x = (double)rl64(k.w, at);
       }
       r.mass = k.mass;
     }
   } else {
-    if (check) {
-      const bool real = x >= 0 && x < a.n;
-      const double wx = real ? (double)r.kept(r.key_at(x)) : 0.0;
-      accepted = (double)ux * qx * (double)r.mass < wx;
-      less.mass = (double)r.mass;
+    // the list: top_k's border, top_p's, and the column drawn, each by
+    // list_find; the tiles' borders are known
+#pragma unroll 1
+    for (int stage = way == 1 ? 0 : 2; stage < 3; ++stage) {
+      Range f{max((uint64_t)bound << 32, (uint64_t)1), cand_key(m, 0), 0, 0};
+      if (stage == 0) {
+        if (!h.top_k || n <= h.top_k) continue;
+        f.target = h.top_k;
+      } else if (stage == 1) {
+        if (!(h.top_p < 1.0)) continue;
+        uint64_t mine = 0;
+#pragma unroll 1
+        for (int i = tid; i < n; i += kRowThreads)
+          if (s.key[i] >= r.thr) mine += s.w[i];
+        __syncthreads();
+        const uint64_t listed = block_sum(mine, s);
+        f.lo = max(f.lo, r.thr);
+        f.target = share_of(all ? all : listed, h.top_p);
+      } else {
+        if (way == 1) {
+          uint64_t mine = 0;
+#pragma unroll 1
+          for (int i = tid; i < n; i += kRowThreads) {
+            const uint64_t w = r.kept(s.key[i]);
+            s.w[i] = w;
+            mine += w;
+          }
+          __syncthreads();
+          r.mass = block_sum(mine, s);
+        }
+        if (check) {
+          const double wx = x >= 0 && x < a.n ? (double)r.kept(r.key_at(x)) : 0.0;
+          accepted = (double)ux * qx * (double)r.mass < wx;
+          less.mass = (double)r.mass;
+          if (accepted) break;
+        }
+        if (way != 1) {
+          drawn = r.draw_tiles(way == 3, u, less);
+          break;
+        }
+        uint64_t total = r.mass;
+        if (check) {
+          uint64_t mine = 0;
+#pragma unroll 1
+          for (int i = tid; i < n; i += kRowThreads) mine += less.rest(s.w[i], key_id(s.key[i]));
+          __syncthreads();
+          const uint64_t rest = block_sum(mine, s);
+          if (rest) {
+            total = rest;
+#pragma unroll 1
+            for (int i = tid; i < n; i += kRowThreads) s.w[i] = less.rest(s.w[i], key_id(s.key[i]));
+          }
+        }
+        f = Range{0xFFFFFFFFu - (uint32_t)(a.n - 1), 0xFFFFFFFFu, place_of(total, u) + 1, 0};
+      }
+      const uint64_t k = list_find(f, n, stage == 2 ? 0xFFFFFFFFull : ~0ull, stage == 0, s);
+      if (stage < 2) r.thr = max(r.thr, k);
+      else drawn = (int)(0xFFFFFFFFu - (uint32_t)k);
     }
-    if (!accepted) {
-      drawn = way == 1 ? r.draw_list(n, u, less) : r.draw_tiles(way == 3, u, less);
-      kept_x = drawn >= 0 ? (double)r.kept(r.key_at(drawn)) : 0.0;
-    }
+    if (!accepted) kept_x = drawn >= 0 ? (double)r.kept(r.key_at(drawn)) : 0.0;
   }
   if (tid == 0) {   // wave 0 knows in every case
     if (!VERIFY) {
