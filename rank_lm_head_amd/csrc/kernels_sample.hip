@@ -78,6 +78,45 @@ struct Exp2 {
   __device__ __forceinline__ double operator()(double t) const { return in_range(fmax(t, -1000.0)); }
 };
 
+// 2^(j / 32), and 2^f = 1 + f q(f) for |f| <= 1/64 to 2e-13 with three
+// multiplications: what the stream sums. (x - m) c is rounded to 1/32 by the
+// addition of 1.5 2^47, and the rest formed by one fma without rounding; the
+// maximum's weight is 1, without an error, so that ties have equal masses
+// whatever their tile. Per column this takes 11 64-bit instructions instead of
+// 16, which bound rows that need their mass (256 x 151936 bf16: 39 us with the polynomial of
+// degree 9).
+__constant__ const double kPow32[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002,
+};
+struct TileExp {
+  const double* pow;   // kPow32 in LDS
+  double m, c;
+  double a1, a2, a3, a4;
+  __device__ __forceinline__ TileExp(const double* p, double m_, double c_)
+      : pow(p), m(m_), c(c_), a1(0.693147180550011), a2(0.24022650695795306), a3(0.055504434191939005),
+        a4(0.009618166713972776) {
+    asm("" : "+s"(a1), "+s"(a2), "+s"(a3), "+v"(a4));
+  }
+  __device__ __forceinline__ double operator()(float x) const {
+    const double big = 211106232532992.0, d = (double)x - m;
+    const double r = fma(d, c, big), f = fma(d, c, -(r - big));
+    const uint32_t n = (uint32_t)__double_as_longlong(r);   // 32 (x - m) c, rounded
+    const uint64_t t = (uint64_t)__double_as_longlong(pow[n & 31]);
+    const double p = __longlong_as_double((long long)((t & 0xffffffffull) | (uint64_t)((uint32_t)(t >> 32) + ((n & ~31u) << 15)) << 32));
+    double q = fma(a4, f, a3);
+    q = fma(q, f, a2);
+    q = fma(q, f, a1);
+    return fma(p * f, q, p);
+  }
+};
+
 // 16 bytes from an address aligned to its elements only.
 __device__ __forceinline__ u32x4 load16_any(const void* p) {
   u32x4 v;
@@ -119,6 +158,7 @@ struct Args {
   int tiles;
   int per;                  // rows of a sequence
   int bits;                 // S
+  bool sums;                // whether a row may need its mass
   float* gmax;              // [row][tile][kGroups]
   float* tmax;              // [row][tile]
   double* tsum;             // [row][tile]; a block may put integers of the kept mass there
@@ -275,6 +315,11 @@ __device__ __forceinline__ void load_tile(const Args& a, int64_t row, int tile, 
 template <typename T, bool VERIFY>
 __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
   constexpr int EP = Elems<T>::n, CH = kPer / EP;   // chunks of a lane: one per group of 64 * EP columns
+  __shared__ double pow[32];
+  if (a.sums) {
+    if (threadIdx.x < 32) pow[threadIdx.x] = kPow32[threadIdx.x];
+    __syncthreads();
+  }
   const uint32_t w = blockIdx.x * kWaves + wave_id();   // below 2^26: 32-bit divisions do
   const uint32_t row32 = w / (uint32_t)a.tiles;
   const int64_t row = row32;
@@ -312,19 +357,19 @@ __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
   const float m = wave_max_f32(t);
   if (lane == 0) a.tmax[row * a.tiles + tile] = m;
   const How h = how_of(a, seq);
-  if (!h.mass()) return;
+  if (!a.sums || !h.mass()) return;
   double s = 0.0;
   if (m > neg_inf()) {
-    const Exp2 exp2;
     const float low = fmaxf((float)((double)m - 990.0 / h.c - fabs((double)m) * 1e-6), -__FLT_MAX__);
     const double t = log_weight(low, m, h.c);
-    if (t >= -1000.0 && t <= -900.0 && fabs((double)m) * h.c < 4096.0) {   // what is 2^-900 of the maximum and less, -inf among it, counts as nothing
+    if (t >= -1000.0 && t <= -900.0) {   // what is 2^-900 of the maximum and less, -inf among it, counts as nothing
+      const TileExp ex(pow, m, h.c);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) s += exp2.in_range(log_weight(fmaxf(v[i], low), m, h.c));
+      for (int i = 0; i < kPer; ++i) s += ex(fmaxf(v[i], low));
     } else {   // temperatures at which the lowest fp32 weighs something, maxima beside which 990 / c is lost
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        s += v[i] > neg_inf() ? exp2(log_weight(fmaxf(v[i], -__FLT_MAX__), m, h.c)) : 0.0;
+        s += v[i] > neg_inf() ? Exp2()(log_weight(fmaxf(v[i], -__FLT_MAX__), m, h.c)) : 0.0;
     }
     s = wave_sum_f64(s);
   }
@@ -633,7 +678,7 @@ struct GroupMax {
       for (int e = 0; e < kHeld; ++e) c += wave_count(v[e] >= mid);
       if (c >= k) {
         lo = mid;
-        if (c <= k + k / 4) break;
+        if (c <= k + max(k / 4, 4)) break;
       } else {
         hi = mid - 1;
       }
@@ -723,60 +768,97 @@ struct RowCtx {
   }
 
   // LDS list of the columns that reach the bound, as keys; its length may be
-  // above kList, then the list is not whole. A wave reads eight groups at a time.
+  // above kList, then the list is not whole. First the places of four
+  // neighbouring columns in which one does, a wave on eight groups at a time,
+  // then these one by one: few lanes of a group find any.
   __device__ __forceinline__ int gather(GroupMax& g, uint32_t bound) {
-    constexpr int kEach = kGroup / kWave, kAtOnce = 8;
+    constexpr int kAtOnce = 8, kOfLast = 1 << 30;
+    static_assert(kGroup == 4 * kWave, "a lane has four columns of a group");
     const int groups = a.tiles * kGroups;
     const float least = bound ? __uint_as_float(order_key_inv(bound)) : -__FLT_MAX__;
     const uint32_t key = max(bound, 1u);
-    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+    int* fours = reinterpret_cast<int*>(s.count);
     __syncthreads();
-    if (threadIdx.x == 0) s.n_list = 0;
-#pragma unroll 1
-    for (int g0 = 0; g0 < groups; g0 += kHeldGroups) {
-      if (groups > kHeldGroups) g.load(a.gmax + row * groups, g0, groups);
-      if (threadIdx.x == 0) s.n_ask = 0;
+    if (tid == 0) {
+      s.n_list = 0;
+      s.pick = 0;
+    }
+    if (a.n < kTile) {   // all of them
       __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kHeld; ++e) {
-        if (e % kRowWaves != wave) continue;
-        if (g.v[e] >= key) s.ask[atomicAdd(&s.n_ask, 1)] = g0 + e * kWave + lane;
-      }
-      __syncthreads();
-      const int n = s.n_ask;
+      fours[tid] = tid * 4;
+      if (tid == 0) s.pick = (a.n + 3) / 4;
+    } else {
 #pragma unroll 1
-      for (int i = wave * kAtOnce; i < n; i += kRowWaves * kAtOnce) {
-        int col[kAtOnce * kEach], from[kAtOnce];
-        float v[kAtOnce * kEach];
+      for (int g0 = 0; g0 < groups; g0 += kHeldGroups) {
+        if (groups > kHeldGroups) g.load(a.gmax + row * groups, g0, groups);
+        if (tid == 0) s.n_ask = 0;
+        __syncthreads();
 #pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-          const int grp = s.ask[min(i + q, n - 1)], tile = grp / kGroups;
-          const int c = tile_base(a, tile) + grp % kGroups * kGroup + lane * kEach;
-          from[q] = i + q < n ? tile * kTile : a.n;
-#pragma unroll
-          for (int e = 0; e < kEach; ++e) col[q * kEach + e] = c + e;
+        for (int e = 0; e < kHeld; ++e) {
+          if (e % kRowWaves != wave) continue;
+          if (g.v[e] >= key) s.ask[atomicAdd(&s.n_ask, 1)] = g0 + e * kWave + lane;
         }
-        if (a.n >= kTile && !a.idx) load4<kAtOnce>(col, v);   // whole groups
-        else load(col, 0, a.n, v);
+        __syncthreads();
+        const int n = s.n_ask;
+#pragma unroll 1
+        for (int i = wave * kAtOnce; i < n; i += kRowWaves * kAtOnce) {
+          int c[kAtOnce * 4], flag[kAtOnce];
+          float v[kAtOnce * 4];
 #pragma unroll
-        for (int q = 0; q < kAtOnce * kEach; ++q) v[q] = col[q] >= from[q / kEach] ? v[q] : neg_inf();
-        int some = 0;
+          for (int q = 0; q < kAtOnce; ++q) {
+            const int grp = s.ask[min(i + q, n - 1)];
+            c[q * 4] = tile_base(a, grp / kGroups) + grp % kGroups * kGroup + lane * 4;
+            flag[q] = grp / kGroups == a.tiles - 1 ? kOfLast : 0;
+          }
+          load4<kAtOnce>(c, v);
+          uint32_t found = 0;
 #pragma unroll
-        for (int q = 0; q < kAtOnce * kEach; ++q) some += v[q] >= least;
-        if (some) {
-          int p = atomicAdd(&s.n_list, some);
+          for (int q = 0; q < kAtOnce; ++q) {
+            const float most = fmaxf(fmaxf(v[q * 4], v[q * 4 + 1]), fmaxf(v[q * 4 + 2], v[q * 4 + 3]));
+            found |= most >= least && i + q < n ? 1u << q : 0u;
+          }
+          if (found) {
+            int p = atomicAdd(&s.pick, __popc(found));
 #pragma unroll
-          for (int q = 0; q < kAtOnce * kEach; ++q) {
-            if (v[q] >= least) {
-              if (p < kList) s.key[p] = cand_key(v[q], col[q]);
-              ++p;
+            for (int q = 0; q < kAtOnce; ++q) {
+              if (found >> q & 1) {
+                if (p < kList) fours[p] = c[q * 4] | flag[q];
+                ++p;
+              }
             }
           }
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
-    return s.n_list;
+    __syncthreads();
+    const int n = s.pick;
+#pragma unroll 1
+    for (int i = tid; i < min(n, kList); i += kRowThreads) {
+      const int c = fours[i] & ~kOfLast;
+      int col[4];
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) col[q] = c + q;
+      // the last tile's groups begin among its neighbour's columns, which are in the neighbour's
+      load(col, fours[i] & kOfLast ? (a.tiles - 1) * kTile : 0, a.n, v);
+      int some = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) some += v[q] >= least;
+      if (some) {
+        int p = atomicAdd(&s.n_list, some);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (v[q] >= least) {
+            if (p < kList) s.key[p] = cand_key(v[q], col[q]);
+            ++p;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    return n > kList ? kList + 1 : s.n_list;
   }
   __device__ __forceinline__ uint64_t weigh_list(int n) const {   // the calling thread's share
     uint64_t mine = 0;
@@ -1361,6 +1443,10 @@ Args make_args(const SampleArgs& in, int64_t seqs, int per, void* workspace) {
   int log = 0;
   while ((int64_t(1) << log) < in.n) ++log;
   a.bits = std::min(51, 62 - log);
+  // as How::mass() goes by them, where they are known here
+  const bool some_k = !in.top_k && in.top_k_all > 0 && in.top_k_all < in.n, greedy = !in.temperature && !(in.temperature_all > 0.f);
+  const bool only_min_p = !in.top_p && !(in.top_p_all < 1.f) && !in.min_p && in.min_p_all > 0.f;
+  a.sums = !(some_k || greedy || only_min_p);
   a.token = in.token;
   a.prob = in.prob;
   a.probs = in.probs;
