@@ -44,7 +44,8 @@ constexpr int kRowWaves = kRowThreads / kWave;
 constexpr int kList = 2048;                 // columns that a row's block holds in LDS
 constexpr int kValueBins = 2048;            // of a whole row's logits, even in value
 constexpr double kLog2e = 1.4426950408889634;
-constexpr int kFirstK = 40, kSecondK = 512; // groups' maxima above the bound of top_p's first and second try
+constexpr int kFirstK = 40, kSecondK = 128, kThirdK = 512;   // groups' maxima above the bounds that top_p tries
+constexpr int kMostMore = 1000;             // columns that the last of these may add
 
 // 2^t of -1000 <= t <= 0 to 4e-14: 2^f = 1 + f g(f) for |f| <= 1/2, g by
 // interpolation at the Chebyshev nodes. The nearest integer comes from the
@@ -160,6 +161,8 @@ struct Args {
   int bits;                 // S
   bool sums;                // whether a row may need its mass
   float* gmax;              // [row][tile][kGroups]
+  float* gsecond;           // its largest chunk of 16 bytes apart, and the lane of that chunk
+  int32_t* gat;
   float* tmax;              // [row][tile]
   double* tsum;             // [row][tile]; a block may put integers of the kept mass there
   int32_t* token;
@@ -333,30 +336,74 @@ __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
   }
   float v[kPer];
   load_tile<T>(a, row, tile, v);
-  // chunk by chunk the maxima of rows of 16 lanes; lane i of a row keeps chunk i's
-  float t = neg_inf();
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    float m = v[i * EP];
-#pragma unroll
-    for (int e = 1; e < EP; ++e) m = fmaxf(m, v[i * EP + e]);
-    m = fmaxf(m, dpp<0xB1>(m));
-    m = fmaxf(m, dpp<0x4E>(m));
-    m = fmaxf(m, dpp<0x141>(m));
-    m = fmaxf(m, dpp<0x140>(m));
-    t = (lane & 15) == i ? m : t;
-  }
-  t = fmaxf(t, __shfl_xor(t, 16));
-  float* g = a.gmax + (row * a.tiles + tile) * kGroups;
-  if constexpr (EP == 4) {   // a chunk is a group
-    t = fmaxf(t, __shfl_xor(t, 32));
-    if (lane < kGroups) g[lane] = t;
-  } else {                   // a chunk is two groups, of 32 lanes each
-    if ((lane & 31) < CH) g[(lane & 31) * 2 + (lane >> 5)] = t;
-  }
-  const float m = wave_max_f32(t);
-  if (lane == 0) a.tmax[row * a.tiles + tile] = m;
   const How h = how_of(a, seq);
+  const int64_t g0 = (row * a.tiles + tile) * kGroups;
+  float m;
+  if (h.whole()) {   // the maximum alone
+    m = v[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, v[i]);
+    m = wave_max_f32(m);
+    if (lane < kGroups) a.gmax[g0 + lane] = lane ? neg_inf() : m;
+  } else {
+    // of the chunks of a group the two largest maxima, over rows of 16 lanes
+    // by DPP; lane i of a row keeps those of its i-th chunks, then the rows join
+    float chunk[CH], t1 = neg_inf(), t2 = neg_inf();
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float m1 = v[i * EP];
+#pragma unroll
+      for (int e = 1; e < EP; ++e) m1 = fmaxf(m1, v[i * EP + e]);
+      chunk[i] = m1;
+      float o = dpp<0xB1>(m1), m2 = fminf(m1, o);
+      m1 = fmaxf(m1, o);
+      o = dpp<0x4E>(m1);
+      m2 = fmaxf(fmaxf(m2, dpp<0x4E>(m2)), fminf(m1, o));
+      m1 = fmaxf(m1, o);
+      o = dpp<0x141>(m1);
+      m2 = fmaxf(fmaxf(m2, dpp<0x141>(m2)), fminf(m1, o));
+      m1 = fmaxf(m1, o);
+      o = dpp<0x140>(m1);
+      m2 = fmaxf(fmaxf(m2, dpp<0x140>(m2)), fminf(m1, o));
+      m1 = fmaxf(m1, o);
+      t1 = (lane & 15) == i ? m1 : t1;
+      t2 = (lane & 15) == i ? m2 : t2;
+    }
+    const auto join = [&](int lanes) {
+      const float o1 = __shfl_xor(t1, lanes), o2 = __shfl_xor(t2, lanes);
+      t2 = fmaxf(fmaxf(t2, o2), fminf(t1, o1));
+      t1 = fmaxf(t1, o1);
+    };
+    join(16);
+    int at = 0;   // the lane whose chunk has the largest
+    if constexpr (EP == 4) {   // a chunk is a group
+      join(32);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int l = __ffsll((unsigned long long)__ballot(chunk[i] == readlane_f(t1, i))) - 1;
+        at = lane == i ? l : at;
+      }
+      if (lane < kGroups) {
+        a.gmax[g0 + lane] = t1;
+        a.gsecond[g0 + lane] = t2;
+        a.gat[g0 + lane] = at;
+      }
+    } else {                   // a chunk is two groups, of 32 lanes each
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const unsigned long long k = __ballot(chunk[i] == (lane < 32 ? readlane_f(t1, i) : readlane_f(t1, 32 + i)));
+        at = lane == i ? __ffs((int)(uint32_t)k) - 1 : lane == 32 + i ? __ffs((int)(uint32_t)(k >> 32)) + 31 : at;
+      }
+      if ((lane & 31) < CH) {
+        const int64_t g = g0 + (lane & 31) * 2 + (lane >> 5);
+        a.gmax[g] = t1;
+        a.gsecond[g] = t2;
+        a.gat[g] = at;
+      }
+    }
+    m = wave_max_f32(t1);
+  }
+  if (lane == 0) a.tmax[row * a.tiles + tile] = m;
   if (!a.sums || !h.mass()) return;
   double s = 0.0;
   if (m > neg_inf()) {
@@ -506,13 +553,16 @@ __global__ void __launch_bounds__(kThreads) sample_lists_kernel(Args a) {
 // same steps took two to four times as long (256 rows under top_k 200: 105 us).
 struct Lds {
   uint64_t key[kList], w[kList];   // the list, and its weights
-  uint64_t mass[kRowThreads];
-  uint32_t count[kValueBins];
+  uint64_t mass[kRowThreads];      // bins, all 0 between their uses
+  uint32_t count[kRowThreads];
+  int four[kList];                 // places of four columns to look at
+  int ask[2 * kRowThreads];        // groups to read
   Item items[kWave];
   uint64_t sum[kRowWaves];
-  uint64_t out[4];
-  int ask[2 * kRowThreads];
-  int n_ask, n_list, pick;
+  uint64_t win_before[kRowWaves];
+  int win_bin[kRowWaves], win_count[kRowWaves];
+  uint64_t out;
+  int n_ask, n_four, n_list, n_few, pick;
   int32_t id[64];
   float q[64];
   int tile[64];             // of the list's tokens, and what they take from it
@@ -553,59 +603,55 @@ struct Range {
   int n;
 };
 // One step towards the last key before which less than `target` weight lies:
-// the range is cut into 512 bins whose weights and counts are in s.mass and
-// s.count, and becomes the bin that holds it, with n keys.
+// the range is cut into 512 bins, whose weights and counts the threads add up
+// (bins_add), and becomes the bin that holds it, with n keys.
 __device__ __forceinline__ int shift_of(const Range& r) { return max(0, 64 - __clzll((long long)(r.hi - r.lo)) - 9); }
-__device__ __forceinline__ void bins_begin(Lds& s) {
-  __syncthreads();
-  s.mass[threadIdx.x] = 0;
-  s.count[threadIdx.x] = 0;
-  if (threadIdx.x == 0) {
-    s.pick = -1;
-    s.n_ask = 0;
-  }
-  __syncthreads();
-}
 __device__ __forceinline__ void bins_add(uint64_t key, uint64_t w, const Range& r, int shift, Lds& s) {
   const int bin = (int)((r.hi - key) >> shift);
   atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[bin]), (unsigned long long)w);
   atomicAdd(&s.count[bin], 1u);
 }
 __device__ __forceinline__ Range bins_pick(Range r, int shift, Lds& s) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, wave = wave_id();
   __syncthreads();
-  uint64_t all;
-  const uint64_t before = block_scan(s.mass[tid], all, s);
+  const uint64_t w = s.mass[tid];
   const uint32_t c = s.count[tid];
-  if (c && before < r.target) atomicMax(&s.pick, tid);
-  __syncthreads();
-  const int pick = s.pick;
-  if (tid == pick) {
-    s.out[0] = before;
-    s.out[1] = c;
+  s.mass[tid] = 0;
+  s.count[tid] = 0;
+  if (tid == 0) s.n_few = 0;
+  uint64_t all;
+  const uint64_t before = block_scan(w, all, s);
+  const unsigned long long in = __ballot(c && before < r.target);   // the last of these
+  if ((tid & 63) == (in ? 63 - __clzll((long long)in) : 0)) {
+    s.win_bin[wave] = in ? tid : -1;
+    s.win_count[wave] = (int)c;
+    s.win_before[wave] = before;
   }
   __syncthreads();
-  if (pick < 0) {   // no key with weight: not by any call here
+  int win = -1;
+#pragma unroll
+  for (int v = 0; v < kRowWaves; ++v) win = s.win_bin[v] >= 0 ? v : win;
+  if (win < 0) {   // no key with weight: not by any call here
     r.lo = r.hi;
     r.n = 1;
     return r;
   }
-  const uint64_t top = r.hi - ((uint64_t)pick << shift), width = (1ull << shift) - 1;
+  const uint64_t top = r.hi - ((uint64_t)s.win_bin[win] << shift), width = (1ull << shift) - 1;
   r.lo = top - r.lo > width ? top - width : r.lo;
   r.hi = top;
-  r.target -= s.out[0];
-  r.n = (int)s.out[1];
+  r.target -= s.win_before[win];
+  r.n = s.win_count[win];
   return r;
 }
 
 // The last key & mask of the list's n before which less than the target lies,
-// by weight or, with `ones`, by count; keys of weight 0 do not count.
+// by weight or, with `ones`, by count; keys of weight 0 do not count. A barrier
+// has to lie between the writing of the list and this.
 __device__ __forceinline__ uint64_t list_find(Range r, int n, uint64_t mask, bool ones, Lds& s) {
   const int tid = threadIdx.x, lane = tid & 63;
   do {
     if (r.lo >= r.hi) return r.lo;
     const int shift = shift_of(r);
-    bins_begin(s);
 #pragma unroll 1
     for (int i = tid; i < n; i += kRowThreads) {
       const uint64_t k = s.key[i] & mask, w = ones ? 1 : s.w[i];
@@ -615,26 +661,20 @@ __device__ __forceinline__ uint64_t list_find(Range r, int n, uint64_t mask, boo
   } while (r.n > kWave);
 #pragma unroll 1
   for (int i = tid; i < n; i += kRowThreads) {
-    const uint64_t k = s.key[i] & mask;
-    if (k >= r.lo && k <= r.hi && (ones || s.w[i])) {
-      const int at = atomicAdd(&s.n_ask, 1);
-      if (at < kWave) s.ask[at] = i;
+    const uint64_t k = s.key[i] & mask, w = ones ? 1 : s.w[i];
+    if (w && k >= r.lo && k <= r.hi) {
+      const int at = atomicAdd(&s.n_few, 1);
+      if (at < kWave) s.items[at] = Item{k, w};
     }
   }
   __syncthreads();
-  if (wave_id() == 0) {
-    const int few = min(r.n, s.n_ask);
-    const bool have = lane < few;
-    const int i = have ? s.ask[lane] : 0;
-    const uint64_t k = have ? s.key[i] & mask : 0, w = have ? (ones ? 1 : s.w[i]) : 0;
-    wave_put(s.items, k, w);
-    int rank;
-    const uint64_t before = wave_before(s.items, few, k, rank);
-    const int kept = wave_count(have && before < r.target);
-    if (have && rank == kept - 1) s.out[2] = k;
-  }
-  __syncthreads();
-  return s.out[2];
+  const int few = min(s.n_few, kWave);
+  const Item it = lane < few ? s.items[lane] : Item{0, 0};
+  int rank;
+  const uint64_t before = wave_before(s.items, few, it.key, rank);
+  const int kept = wave_count(it.w && before < r.target);
+  const unsigned long long hit = __ballot(it.w && rank == kept - 1);
+  return hit ? rl64(it.key, __ffsll(hit) - 1) : r.lo;
 }
 
 // The groups' maxima of a row as order keys (0: no candidate), in every wave:
@@ -642,13 +682,23 @@ __device__ __forceinline__ uint64_t list_find(Range r, int n, uint64_t mask, boo
 // several.
 constexpr int kHeld = 16, kHeldGroups = kHeld * kWave;
 struct GroupMax {
+  static constexpr int kOwn = kHeld / kRowWaves;
   uint32_t v[kHeld];
-  __device__ __forceinline__ void load(const float* gmax, int g0, int groups) {
+  float second[kOwn];   // of the groups that are this wave's to look at: every kRowWaves-th 64
+  int at[kOwn];
+  __device__ __forceinline__ void load(const Args& a, int64_t row, int g0, int groups) {
+    const float* gmax = a.gmax + row * groups;
     float x[kHeld];
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
       const int g = g0 + e * kWave + (threadIdx.x & 63);
       x[e] = g < groups ? gmax[g] : neg_inf();
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int64_t g = row * groups + min(g0 + (i * kRowWaves + wave_id()) * kWave + (int)(threadIdx.x & 63), groups - 1);
+      second[i] = a.gsecond[g];
+      at[i] = a.gat[g];
     }
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) v[e] = x[e] > neg_inf() ? order_key(x[e]) : 0;
@@ -768,36 +818,49 @@ struct RowCtx {
   }
 
   // LDS list of the columns that reach the bound, as keys; its length may be
-  // above kList, then the list is not whole. First the places of four
-  // neighbouring columns in which one does, a wave on eight groups at a time,
-  // then these one by one: few lanes of a group find any.
+  // above kList, then the list is not whole. A group whose second chunk stays
+  // below the bound has its candidates in the chunk of its maximum; the others
+  // are read, a wave on eight of them at a time. That gives the places of four
+  // neighbouring columns with one that reaches the bound, or nearly only
+  // these, which are then looked at one by one.
   __device__ __forceinline__ int gather(GroupMax& g, uint32_t bound) {
-    constexpr int kAtOnce = 8, kOfLast = 1 << 30;
+    constexpr int kAtOnce = 8, kOfLast = 1 << 30, EP = Elems<T>::n;
     static_assert(kGroup == 4 * kWave, "a lane has four columns of a group");
     const int groups = a.tiles * kGroups;
     const float least = bound ? __uint_as_float(order_key_inv(bound)) : -__FLT_MAX__;
     const uint32_t key = max(bound, 1u);
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-    int* fours = reinterpret_cast<int*>(s.count);
     __syncthreads();
     if (tid == 0) {
       s.n_list = 0;
-      s.pick = 0;
+      s.n_four = a.n < kTile ? (a.n + 3) / 4 : 0;
+      s.n_ask = 0;
     }
     if (a.n < kTile) {   // all of them
-      __syncthreads();
-      fours[tid] = tid * 4;
-      if (tid == 0) s.pick = (a.n + 3) / 4;
+      s.four[tid] = tid * 4;
     } else {
 #pragma unroll 1
       for (int g0 = 0; g0 < groups; g0 += kHeldGroups) {
-        if (groups > kHeldGroups) g.load(a.gmax + row * groups, g0, groups);
-        if (tid == 0) s.n_ask = 0;
+        if (groups > kHeldGroups) g.load(a, row, g0, groups);
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kHeld; ++e) {
-          if (e % kRowWaves != wave) continue;
-          if (g.v[e] >= key) s.ask[atomicAdd(&s.n_ask, 1)] = g0 + e * kWave + lane;
+        for (int i = 0; i < GroupMax::kOwn; ++i) {
+          uint32_t v = 0;   // of the wave's i-th 64 groups
+#pragma unroll
+          for (int e = 0; e < kHeld; ++e) v = e == i * kRowWaves + wave ? g.v[e] : v;
+          if (v >= key) {
+            const int grp = g0 + (i * kRowWaves + wave) * kWave + lane, tile = grp / kGroups, in = grp % kGroups;
+            if (g.second[i] >= least) {
+              s.ask[atomicAdd(&s.n_ask, 1)] = grp;
+            } else {
+              const int p = atomicAdd(&s.n_four, EP / 4);
+              const int c = (tile_base(a, tile) + in / (EP / 4) * (kWave * EP) + g.at[i] * EP) |
+                            (tile == a.tiles - 1 ? kOfLast : 0);
+#pragma unroll
+              for (int q = 0; q < EP / 4; ++q)
+                if (p + q < kList) s.four[p + q] = c + 4 * q;
+            }
+          }
         }
         __syncthreads();
         const int n = s.n_ask;
@@ -819,30 +882,33 @@ struct RowCtx {
             found |= most >= least && i + q < n ? 1u << q : 0u;
           }
           if (found) {
-            int p = atomicAdd(&s.pick, __popc(found));
+            int p = atomicAdd(&s.n_four, __popc(found));
 #pragma unroll
             for (int q = 0; q < kAtOnce; ++q) {
               if (found >> q & 1) {
-                if (p < kList) fours[p] = c[q * 4] | flag[q];
+                if (p < kList) s.four[p] = c[q * 4] | flag[q];
                 ++p;
               }
             }
           }
         }
-        __syncthreads();
+        if (groups > kHeldGroups) {
+          __syncthreads();
+          if (tid == 0) s.n_ask = 0;
+        }
       }
     }
     __syncthreads();
-    const int n = s.pick;
+    const int n = s.n_four;
 #pragma unroll 1
     for (int i = tid; i < min(n, kList); i += kRowThreads) {
-      const int c = fours[i] & ~kOfLast;
+      const int c = s.four[i] & ~kOfLast;
       int col[4];
       float v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) col[q] = c + q;
       // the last tile's groups begin among its neighbour's columns, which are in the neighbour's
-      load(col, fours[i] & kOfLast ? (a.tiles - 1) * kTile : 0, a.n, v);
+      load(col, s.four[i] & kOfLast ? (a.tiles - 1) * kTile : 0, a.n, v);
       int some = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) some += v[q] >= least;
@@ -979,6 +1045,7 @@ struct RowCtx {
     if (n > kList || n < 1 || above >= share) return false;
     __syncthreads();
     const uint64_t listed = block_sum(weigh_list(n), s);
+    __syncthreads();
     if (above + listed < share && hi < (float)kValueBins) return false;
     if (!listed) return false;
     thr = list_find(Range{1, cand_key(m, 0), share - above, 0}, n, ~0ull, false, s);
@@ -1010,7 +1077,7 @@ struct RowCtx {
       uint64_t mine = 0;
       do {
         const int shift = shift_of(r);
-        bins_begin(s);
+        __syncthreads();
 #pragma unroll 1
         for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
           each_of_tile(tile, [&](float x, int col) {
@@ -1109,13 +1176,13 @@ struct RowCtx {
             const uint64_t w = each == 1 ? one : t < a.tiles ? mass_of(t) : 0;
             if (b <= at && at - b < w) {
               s.pick = t;
-              s.out[0] = at - b;
+              s.out = at - b;
             }
             b += w;
           }
         }
         __syncthreads();
-        left = s.out[0];
+        left = s.out;
         tile = s.pick;
       }
       // forwards to the column that holds the place; from behind the last tile,
@@ -1211,6 +1278,8 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
     if (a.length) drafted = min(max(a.length[seq], 0), a.per - 1);
     if (j > drafted) return;
   }
+  s.mass[tid] = 0;
+  s.count[tid] = 0;
   // the row's maximum
   const int groups = a.tiles * kGroups;
   const float u = a.u[seq * a.u_ld + (VERIFY ? a.per - 1 : 0)];
@@ -1218,13 +1287,13 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
   const float own_max = a.tmax[own];
   const double own_sum = a.tsum[own];
   GroupMax g;
-  g.load(a.gmax + row * groups, 0, groups);
+  g.load(a, row, 0, groups);
   RowCtx<T> r{a, s, row, how_of(a, seq), neg_inf(), Exp2(), 1, 0, 0};
   const How& h = r.h;
 #pragma unroll 1
   for (int g0 = kHeldGroups; g0 < groups; g0 += kHeldGroups) {
     GroupMax more;
-    more.load(a.gmax + row * groups, g0, groups);
+    more.load(a, row, g0, groups);
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) g.v[e] = max(g.v[e], more.v[e]);
   }
@@ -1277,23 +1346,31 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         const double f = (double)m + h.least / h.c;   // c = 0: -inf or NaN
         if (f > -(double)__FLT_MAX__) floor_key = order_key((float)(f - (fabs(f) + fabs((double)m)) * 1e-6));
       }
+      int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : groups + 1;
 #pragma unroll 1
-      for (int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : groups + 1;; k = kSecondK) {
+      for (;;) {
         bound = g.bound(k, top);
         // all that can be kept is in a list that reaches down to top_k columns or to min_p
         bool enough = h.top_k || !bound || bound <= floor_key;
         if (!(h.top_k && h.top_p < 1.0)) bound = max(bound, floor_key);
         n = r.gather(g, bound);
         if (n > kList) break;
+        double more = 0.0;
         if (n > kWave || !enough) {
           const uint64_t listed = block_sum(r.weigh_list(n), s);
-          enough = enough || listed >= share_of(all, h.top_p);   // or to top_p of the mass
+          if (!enough) {   // or to top_p of the mass
+            const uint64_t share = share_of(all, h.top_p);
+            enough = listed >= share;
+            // else at least so many more columns, as the others weigh less than the bound
+            if (!enough) more = (double)(share - listed) / ((double)r.weight((uint64_t)bound << 32) + 1.0);
+          }
         }
         if (enough) {
           way = n <= kWave ? 0 : 1;
           break;
         }
-        if (k >= kSecondK) break;
+        if (k >= kThirdK || more > kMostMore) break;
+        k = k == kFirstK && more < kFirstK ? kSecondK : kThirdK;
       }
       if (way == 3 && !(h.mass() && r.keep_row(all))) r.split_row(all);
     }
@@ -1407,13 +1484,15 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Space {
-  size_t gmax, tmax, tsum, state, arrived, total;
+  size_t gmax, gsecond, gat, tmax, tsum, state, arrived, total;
 };
 Space space(int64_t rows, int64_t seqs, int64_t n) {
   const size_t tiles = (size_t)rows * ceil_div(n, kTile);
   Space s{};
   s.gmax = 0;
-  s.tmax = align256(tiles * kGroups * 4);
+  s.gsecond = align256(tiles * kGroups * 4);
+  s.gat = 2 * s.gsecond;
+  s.tmax = 3 * s.gsecond;
   s.tsum = s.tmax + align256(tiles * 4);
   s.state = s.tsum + align256(tiles * 8);
   s.arrived = s.state + align256((size_t)rows * 4);
@@ -1454,6 +1533,8 @@ Args make_args(const SampleArgs& in, int64_t seqs, int per, void* workspace) {
     const Space s = space(a.rows, seqs, in.n);
     char* ws = static_cast<char*>(workspace);
     a.gmax = reinterpret_cast<float*>(ws + s.gmax);
+    a.gsecond = reinterpret_cast<float*>(ws + s.gsecond);
+    a.gat = reinterpret_cast<int32_t*>(ws + s.gat);
     a.tmax = reinterpret_cast<float*>(ws + s.tmax);
     a.tsum = reinterpret_cast<double*>(ws + s.tsum);
     a.state = reinterpret_cast<int32_t*>(ws + s.state);
