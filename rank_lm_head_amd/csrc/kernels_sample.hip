@@ -45,7 +45,7 @@ constexpr int kList = 2048;                 // columns that a row's block holds 
 constexpr int kValueBins = 2048;            // of a whole row's logits, even in value
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kFirstK = 40, kSecondK = 128, kThirdK = 512;   // groups' maxima above the bounds that top_p tries
-constexpr int kMostMore = 1000;             // columns that the last of these may add
+constexpr int kMostMore = 250;              // columns missing at least from which on none of them is worth it
 
 // 2^t of -1000 <= t <= 0 to 4e-14: 2^f = 1 + f g(f) for |f| <= 1/2, g by
 // interpolation at the Chebyshev nodes. The nearest integer comes from the
@@ -428,22 +428,19 @@ __global__ void __launch_bounds__(kThreads) sample_tiles_kernel(Args a) {
 // The order of a row's columns: cand_key of logit and column, larger first.
 __device__ __forceinline__ uint64_t key_of(float x, int col) { return x > neg_inf() ? cand_key(x, col) : 0; }
 
-// What a drafted list takes from the weights of its tokens: q of them.
+// What a drafted list takes from the weights of its tokens: q of them, as
+// integers, each token once.
+constexpr int kMapWords = 64;
 struct Less {
-  const int32_t* id;   // LDS
-  const float* q;
-  int k;               // 0: nothing
-  double mass;         // the kept mass of the target row
-  __device__ __forceinline__ double of(int col) const {
-    double s = 0.0;
-    for (int j = 0; j < k; ++j) s += id[j] == col ? (double)q[j] : 0.0;
-    return s;
-  }
+  const int32_t* id;     // LDS; -1: none
+  const uint64_t* q;
+  const uint32_t* map;   // a bit for each id, modulo 2048
+  int k;                 // 0: nothing
   __device__ __forceinline__ uint64_t rest(uint64_t w, int col) const {
-    if (!k || !w) return w;
-    const double s = of(col);
-    if (!(s > 0.0)) return w;
-    const uint64_t gone = (uint64_t)rint(fmin(s * mass, 9e18));
+    if (!k || !w || !(map[col >> 5 & (kMapWords - 1)] >> (col & 31) & 1)) return w;
+    uint64_t gone = 0;
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) gone = id[j] == col ? q[j] : gone;
     return w > gone ? w - gone : 0;
   }
 };
@@ -453,13 +450,15 @@ struct Less {
 struct Item {
   uint64_t key, w;
 };
-__device__ __forceinline__ void wave_put(Item* items, uint64_t key, uint64_t w) {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  items[threadIdx.x & 63] = Item{key, w};
+__device__ __forceinline__ void wave_sync() {   // LDS writes before it are there for the wave's lanes behind it
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+__device__ __forceinline__ void wave_put(Item* items, uint64_t key, uint64_t w) {
+  wave_sync();
+  items[threadIdx.x & 63] = Item{key, w};
+  wave_sync();
 }
 // How many of the n items have larger keys, and their weight.
 __device__ __forceinline__ uint64_t wave_before(const Item* items, int n, uint64_t key, int& rank) {
@@ -563,10 +562,11 @@ struct Lds {
   int win_bin[kRowWaves], win_count[kRowWaves];
   uint64_t out;
   int n_ask, n_four, n_list, n_few, pick;
-  int32_t id[64];
-  float q[64];
-  int tile[64];             // of the list's tokens, and what they take from it
-  uint64_t gone[64];
+  int32_t id[kWave];        // a drafted list
+  uint64_t q[kWave];
+  uint32_t map[kMapWords];
+  int tile[kWave];          // its tokens' tiles, and what they take from them
+  uint64_t gone[kWave];
 };
 
 // A barrier has to lie between a call of either and the next.
@@ -1137,24 +1137,11 @@ struct RowCtx {
     const int each = (a.tiles + kRowThreads - 1) / kRowThreads;
     for (;;) {
       __syncthreads();
-      if (less.k) {   // what the list takes from its tokens' tiles
-        if (tid < less.k) {
-          const int col = less.id[tid];
-          bool first = col >= 0 && col < a.n;
-          for (int j = 0; j < tid && first; ++j) first = less.id[j] != col;
-          uint64_t w = 0;
-          if (first) {
-            w = kept(key_at(col));
-            w -= less.rest(w, col);
-          }
-          s.tile[tid] = first ? col / kTile : -1;
-          s.gone[tid] = w;
-        }
-        __syncthreads();
-      }
       uint64_t mine = 0, total;
       const auto mass_of = [&](int tile) {
-        uint64_t w = ints ? tile_int(tile) : tile_mass(tile), gone = 0;
+        const uint64_t w = ints ? tile_int(tile) : tile_mass(tile);
+        uint64_t gone = 0;
+#pragma unroll 4
         for (int j = 0; j < less.k; ++j) gone += s.tile[j] == tile ? s.gone[j] : 0;
         return w > gone ? w - gone : 0;
       };
@@ -1283,6 +1270,21 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
   // the row's maximum
   const int groups = a.tiles * kGroups;
   const float u = a.u[seq * a.u_ld + (VERIFY ? a.per - 1 : 0)];
+  const bool check = VERIFY && j < drafted;
+  int x = -1, id = -2, list_k = 1;
+  float ux = 0.f, q = 0.f;
+  if constexpr (VERIFY) {
+    if (check) {   // in every wave, a lane per entry of the list
+      const int64_t at = seq * (a.per - 1) + j;
+      x = a.drafted[at];
+      ux = a.u[seq * a.u_ld + j];
+      list_k = a.list ? a.k : 1;
+      if (lane < list_k) {
+        id = a.list ? a.list[at * a.k + lane] : x;
+        q = a.list ? fmaxf(a.q[at * a.k + lane], 0.f) : 1.f;   // NaN: 0
+      }
+    }
+  }
   const int64_t own = row * a.tiles + min(tid, a.tiles - 1);
   const float own_max = a.tmax[own];
   const double own_sum = a.tsum[own];
@@ -1302,26 +1304,37 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
   const float m = none ? neg_inf() : __uint_as_float(order_key_inv(top));
   r.m = m;
 
-  // the list of a drafted position
-  Less less{s.id, s.q, 0, 0.0};
-  int x = -1;
-  float ux = 0.f;
+  // the logits of a drafted position's token and list
   double qx = 0.0;
-  const bool check = VERIFY && j < drafted;
+  float logit_x = neg_inf(), logit = neg_inf();
   if constexpr (VERIFY) {
     if (check) {
-      const int64_t at = seq * (a.per - 1) + j;
-      x = a.drafted[at];
-      ux = a.u[seq * a.u_ld + j];
-      less.k = a.list ? a.k : 1;
-      if (tid < less.k) {
-        s.id[tid] = a.list ? a.list[at * a.k + tid] : x;
-        s.q[tid] = a.list ? fmaxf(a.q[at * a.k + tid], 0.f) : 1.f;
-      }
-      __syncthreads();
-      qx = less.of(x);
+      qx = wave_sum_f64(id == x ? (double)q : 0.0);
+      if (x >= 0 && x < a.n) logit_x = r.at(x);
+      if (id < 0 || id >= a.n) id = -1;
+      if (wave_id() == 0 && id >= 0) logit = r.at(id);
     }
   }
+  Less less{s.id, s.q, s.map, 0};
+  // by wave 0, when the row's kept mass is known: what its list takes
+  const auto take = [&](uint64_t mass) {
+    double sum = 0.0;
+    bool again = false;
+    s.map[lane] = 0;
+#pragma unroll 1
+    for (int j = 0; j < list_k; ++j) {   // an id that occurs twice counts twice, at its first place
+      const bool same = (int)rl((uint32_t)id, j) == id;
+      sum += same ? (double)readlane_f(q, j) : 0.0;
+      again = again || (same && j < lane);
+    }
+    const bool real = id >= 0 && !again && sum > 0.0;
+    const uint64_t gone = real ? (uint64_t)rint(fmin(sum * (double)mass, 9e18)) : 0;
+    if (real) atomicOr(&s.map[id >> 5 & (kMapWords - 1)], 1u << (id & 31));
+    s.id[lane] = real ? id : -1;
+    s.q[lane] = gone;
+    s.tile[lane] = real ? id / kTile : -1;
+    s.gone[lane] = real ? min(r.kept(key_of(logit, id)), gone) : 0;
+  };
 
   // what is kept: by one wave's lanes (way 0), by a list (1), by tiles (2: as
   // the stream left them, 3: as integers)
@@ -1390,11 +1403,13 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         const unsigned long long hit = __ballot(key && col == x);
         const double wx = hit ? (double)rl64(k.w, __ffsll(hit) - 1) : 0.0;
         accepted = (double)ux * qx * (double)k.mass < wx;
-        less.mass = (double)k.mass;
       }
       if (!accepted) {
         uint64_t w = k.w, mass = k.mass;
         if (check) {
+          take(mass);
+          less.k = list_k;
+          wave_sync();
           const uint64_t rest = less.rest(w, col), sum = wave_sum_u64(rest);
           if (sum) {
             w = rest;
@@ -1439,10 +1454,11 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
           r.mass = block_sum(mine, s);
         }
         if (check) {
-          const double wx = x >= 0 && x < a.n ? (double)r.kept(r.key_at(x)) : 0.0;
-          accepted = (double)ux * qx * (double)r.mass < wx;
-          less.mass = (double)r.mass;
+          accepted = (double)ux * qx * (double)r.mass < (double)r.kept(key_of(logit_x, x));
           if (accepted) break;
+          if (wave_id() == 0) take(r.mass);
+          less.k = list_k;
+          __syncthreads();
         }
         if (way != 1) {
           drawn = r.draw_tiles(way == 3, u, less);
@@ -1452,15 +1468,19 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         if (check) {
           uint64_t mine = 0;
 #pragma unroll 1
-          for (int i = tid; i < n; i += kRowThreads) mine += less.rest(s.w[i], key_id(s.key[i]));
-          __syncthreads();
-          const uint64_t rest = block_sum(mine, s);
-          if (rest) {
-            total = rest;
+          for (int i = tid; i < n; i += kRowThreads) {
+            const uint64_t w = less.rest(s.w[i], key_id(s.key[i]));
+            s.w[i] = w;
+            mine += w;
+          }
+          total = block_sum(mine, s);
+          if (!total) {   // the list covers the target: the target itself
+            total = r.mass;
 #pragma unroll 1
-            for (int i = tid; i < n; i += kRowThreads) s.w[i] = less.rest(s.w[i], key_id(s.key[i]));
+            for (int i = tid; i < n; i += kRowThreads) s.w[i] = r.kept(s.key[i]);
           }
         }
+        __syncthreads();
         f = Range{0xFFFFFFFFu - (uint32_t)(a.n - 1), 0xFFFFFFFFu, place_of(total, u) + 1, 0};
       }
       const uint64_t k = list_find(f, n, stage == 2 ? 0xFFFFFFFFull : ~0ull, stage == 0, s);
