@@ -111,7 +111,7 @@ def check_grad(got, dY, t, V, scale, dtype, old=None):
 
 @pytest.mark.parametrize("N,V,d", [(1, 1, 1), (1, 50, 8), (2, 3, 7), (16, 100, 64), (17, 100, 513), (333, 4096, 256),
                                    (1000, 20, 33), (4096, 999, 40), (1023, 511, 520), (5000, 512, 16),
-                                   (16384, 3000, 24), (2048, 70000, 16)])
+                                   (16384, 3000, 24), (2048, 70000, 16), (512, 5000, 12), (513, 5000, 12), (511, 9001, 3)])
 @pytest.mark.parametrize("kind", ["zipf", "even", "one", "two", "some"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_gradient(N, V, d, kind, dtype):
@@ -127,7 +127,7 @@ def test_gradient(N, V, d, kind, dtype):
 
 
 @pytest.mark.parametrize("N,V,d", [(16385, 700, 16), (40000, 151936, 16), (70001, 2 ** 20 + 1, 8), (131072, 9, 24),
-                                   (300, 2 ** 27 - 5, 1), (16384, 2 ** 18 + 1, 8), (600001, 30000, 8)])
+                                   (300, 2 ** 27 - 5, 1), (90, 2 ** 24, 2), (90, 2 ** 24 + 1, 2), (3000, 2 ** 20 - 3, 4), (16384, 2 ** 18 + 1, 8), (600001, 30000, 8)])
 @pytest.mark.parametrize("kind", ["zipf", "some"])
 def test_gradient_of_many_rows(N, V, d, kind):
     """The sort over several blocks: more places than one block sorts, or tokens and places past one word."""
