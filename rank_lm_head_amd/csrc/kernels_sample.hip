@@ -24,6 +24,7 @@
 // What bounds a large call is the one read of the logits; a small one, the
 // two launches.
 #include <algorithm>
+#include <climits>
 
 #include "device.h"
 #include "launch.h"
@@ -45,7 +46,7 @@ constexpr int kList = 2048;                 // columns that a row's block holds 
 constexpr int kValueBins = 2048;            // of a whole row's logits, even in value
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int kFirstK = 40, kSecondK = 128, kThirdK = 512;   // groups' maxima above the bounds that top_p tries
-constexpr int kMostMore = 250;              // columns missing at least from which on none of them is worth it
+constexpr int kMostMore = 128;              // columns missing at least, or a third of the mass: none of them is worth it
 
 // 2^t of -1000 <= t <= 0 to 4e-14: 2^f = 1 + f g(f) for |f| <= 1/2, g by
 // interpolation at the Chebyshev nodes. The nearest integer comes from the
@@ -556,11 +557,13 @@ struct Lds {
   uint32_t count[kRowThreads];
   int four[kList];                 // places of four columns to look at
   int ask[2 * kRowThreads];        // groups to read
+  uint32_t set[2 * kRowThreads];   // maxima of strided sets of columns
   Item items[kWave];
   uint64_t sum[kRowWaves];
   uint64_t win_before[kRowWaves];
   int win_bin[kRowWaves], win_count[kRowWaves];
   uint64_t out;
+  double pow[32];
   int n_ask, n_four, n_list, n_few, pick;
   int32_t id[kWave];        // a drafted list
   uint64_t q[kWave];
@@ -709,16 +712,18 @@ struct GroupMax {
     for (int e = 0; e < kHeld; ++e) m = max(m, v[e]);
     return wave_max_u32(m);
   }
+  __device__ __forceinline__ int some() const {
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) n += wave_count(v[e] != 0);
+    return n;
+  }
   // A bound that at least k of them reach, and few more. 0 where there are not so many.
   __device__ __forceinline__ uint32_t bound(int k, uint32_t hi) const {
     uint32_t lo = ~0u;
-    int have = 0;
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) {
-      have += wave_count(v[e] != 0);
-      lo = min(lo, v[e] ? v[e] : ~0u);
-    }
-    if (have < k) return 0;
+    for (int e = 0; e < kHeld; ++e) lo = min(lo, v[e] ? v[e] : ~0u);
+    if (some() < k) return 0;
     lo = wave_min_u32(lo);
 #pragma unroll 1
     while (lo < hi) {   // count(>= lo) >= k
@@ -796,7 +801,7 @@ struct RowCtx {
 #pragma unroll
     for (int q = 0; q < 4 * N; ++q) x[q] = tame(Elems<T>::one(&raw[q / 4].v[q % 4]));
   }
-  // f(x, col) for the calling lane's candidates in a tile of its wave's
+  // f(x, col) for the calling lane's columns in a tile of its wave's; x is -inf where there is no candidate
   template <typename F>
   __device__ __forceinline__ void each_of_tile(int tile, const F& f) const {
     const int end = min(a.n, (tile + 1) * kTile), lane = threadIdx.x & 63;
@@ -812,9 +817,36 @@ struct RowCtx {
         load(col, 0, end, x);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (x[q] > neg_inf()) f(x[q], col[q]);
+      for (int q = 0; q < 8; ++q) f(x[q], col[q]);
     }
+  }
+
+  // The bound that at least k columns reach, where there are not as many
+  // groups: the row's columns in kHeldGroups strided sets, their maxima in LDS.
+  __device__ __forceinline__ uint32_t fine_bound(int k, uint32_t top, bool& made) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    if (!made) {
+      made = true;
+      static_assert(kHeldGroups == 2 * kRowThreads, "two sets a thread");
+      float m[2] = {neg_inf(), neg_inf()};
+#pragma unroll 1
+      for (int c0 = tid; c0 < a.n; c0 += 4 * kHeldGroups) {
+        int col[8];
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) col[q] = c0 + q * kRowThreads;
+        load(col, 0, a.n, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m[q & 1] = fmaxf(m[q & 1], x[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) s.set[tid + q * kRowThreads] = m[q] > neg_inf() ? order_key(m[q]) : 0;
+      __syncthreads();
+    }
+    GroupMax g;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) g.v[e] = s.set[e * kWave + lane];
+    return g.bound(k, top);
   }
 
   // LDS list of the columns that reach the bound, as keys; its length may be
@@ -974,6 +1006,7 @@ struct RowCtx {
     static_assert(kValueBins == kList, "the bins stand where the list's weights will");
     __syncthreads();
     for (int i = tid; i < kValueBins; i += kRowThreads) bins[i] = 0;
+    if (tid < 32) s.pow[tid] = kPow32[tid];
     if (tid == 0) {
       s.n_list = 0;
       s.pick = kValueBins - 1;
@@ -983,7 +1016,7 @@ struct RowCtx {
 #pragma unroll 1
     for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
       each_of_tile(tile, [&](float x, int) {
-        const float b = bin_of(x);
+        const float b = bin_of(x);   // inf of -inf
         if (b < (float)kValueBins) {
           const int i = (int)b;
           atomicAdd(reinterpret_cast<unsigned long long*>(&bins[i]),
@@ -1020,14 +1053,16 @@ struct RowCtx {
     }
     __syncthreads();
     const float lo = (float)s.pick, hi = (float)(s.n_ask + 1);
+    const TileExp ex(s.pow, m, h.c);
     mine = 0;
+#pragma unroll 1
     for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
       uint64_t w = 0;
       each_of_tile(tile, [&](float x, int col) {
         const float b = bin_of(x);
-        if (b < lo) {
-          w += weight(cand_key(x, col));
-        } else if (b < hi) {
+        const uint64_t one = to_int(ex(b < lo ? x : m), a.bits);   // no branch: in a flat row some lane takes it
+        w += b < lo ? one : 0;
+        if (b >= lo && b < hi) {
           const int p = atomicAdd(&s.n_list, 1);
           if (p < kList) s.key[p] = cand_key(x, col);
         }
@@ -1081,7 +1116,7 @@ struct RowCtx {
 #pragma unroll 1
         for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
           each_of_tile(tile, [&](float x, int col) {
-            const uint64_t k = cand_key(x, col);
+            const uint64_t k = key_of(x, col);   // 0 of -inf, below every range
             if (k < r.lo || k > r.hi) return;
             const uint64_t w = ones ? 1 : weight(k);
             if (stage == 1) mine += w;
@@ -1101,7 +1136,7 @@ struct RowCtx {
 #pragma unroll 1
       for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves)
         each_of_tile(tile, [&](float x, int col) {
-          const uint64_t k = cand_key(x, col);
+          const uint64_t k = key_of(x, col);
           if (k < r.lo || k > r.hi || (!ones && !weight(k))) return;
           const int p = atomicAdd(&s.n_list, 1);
           if (p < kList) s.key[p] = k;
@@ -1117,7 +1152,7 @@ struct RowCtx {
 #pragma unroll 1
     for (int tile = wave_id(); tile < a.tiles; tile += kRowWaves) {
       uint64_t w = 0;
-      each_of_tile(tile, [&](float x, int col) { w += kept(cand_key(x, col)); });
+      each_of_tile(tile, [&](float x, int col) { w += kept(key_of(x, col)); });
       w = wave_sum_u64(w);
       if (lane == 0) {
         __hip_atomic_store(tile_ints() + tile, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -1254,8 +1289,13 @@ __device__ __forceinline__ void finish_sequence(const Args& a, int64_t seq, int 
   if (lane == 0) a.count[seq] = taken + (drawn >= 0);
 }
 
-template <typename T, bool VERIFY>
-__global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
+// More rows than CUs run two to a CU, in half the registers (BLOCKS 2: 1024
+// rows of 32003 columns, bf16, top_k 20: 46 -> 32 us, top_p 0.9: 53 -> 36); a
+// spill then costs a lone row 0.7 to 2 us, so up to 256 rows keep them all.
+constexpr int kCus = 256;
+
+template <typename T, bool VERIFY, int BLOCKS>
+__global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_rows_kernel(Args a) {
   __shared__ Lds s;
   const int64_t row = blockIdx.x;
   const int64_t seq = VERIFY ? blockIdx.x / (uint32_t)a.per : blockIdx.x;
@@ -1359,31 +1399,47 @@ __global__ void __launch_bounds__(kRowThreads) sample_rows_kernel(Args a) {
         const double f = (double)m + h.least / h.c;   // c = 0: -inf or NaN
         if (f > -(double)__FLT_MAX__) floor_key = order_key((float)(f - (fabs(f) + fabs((double)m)) * 1e-6));
       }
-      int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : groups + 1;
+      int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : INT_MAX;   // of min_p alone: no bound but its own
+      const int held = min(groups, kHeldGroups);
+      const bool full = g.some() >= held - held / 8 - kGroups;   // but for the last tile's
+      bool made = false;
 #pragma unroll 1
       for (;;) {
         bound = g.bound(k, top);
+        // Few groups give no bound, or a list past a wave's lanes: finer maxima
+        // (256 rows of 5000 columns, bf16, top_p 0.9: 31 -> 19 us; 64 of 1000, top_k 20: 19 -> 12;
+        // 1024 of 32003, top_k 200: 256 -> 71). Of mostly empty groups a list
+        // may hold all candidates, and is tried first.
+        const bool finer = (!bound || (held < 2 * k && k <= kWave)) && k < INT_MAX && a.n > kWave;
+        if (finer && full) bound = r.fine_bound(k, top, made);
         // all that can be kept is in a list that reaches down to top_k columns or to min_p
         bool enough = h.top_k || !bound || bound <= floor_key;
         if (!(h.top_k && h.top_p < 1.0)) bound = max(bound, floor_key);
         n = r.gather(g, bound);
+        if (n > kList && finer && !full && !bound) {
+          bound = r.fine_bound(k, top, made);
+          n = r.gather(g, bound);
+          enough = enough && h.top_k;
+        }
         if (n > kList) break;
-        double more = 0.0;
+        bool flat = false, few = false;
         if (n > kWave || !enough) {
           const uint64_t listed = block_sum(r.weigh_list(n), s);
           if (!enough) {   // or to top_p of the mass
             const uint64_t share = share_of(all, h.top_p);
             enough = listed >= share;
-            // else at least so many more columns, as the others weigh less than the bound
-            if (!enough) more = (double)(share - listed) / ((double)r.weight((uint64_t)bound << 32) + 1.0);
+            // of a flat row longer lists do not have it either: the others weigh less than the bound
+            const double more = (double)(share - min(listed, share)) / ((double)r.weight((uint64_t)bound << 32) + 1.0);
+            flat = more > kMostMore || listed < share / 3 * 2;
+            few = more < kFirstK;
           }
         }
         if (enough) {
           way = n <= kWave ? 0 : 1;
           break;
         }
-        if (k >= kThirdK || more > kMostMore) break;
-        k = k == kFirstK && more < kFirstK ? kSecondK : kThirdK;
+        if (k >= kThirdK || flat) break;
+        k = k == kFirstK && few ? kSecondK : kThirdK;
       }
       if (way == 3 && !(h.mass() && r.keep_row(all))) r.split_row(all);
     }
@@ -1567,7 +1623,8 @@ template <typename T, bool VERIFY>
 hipError_t launch_rows(const Args& a, hipStream_t s) {
   const dim3 tiles((unsigned)ceil_div(a.rows * a.tiles, kWaves));
   hipLaunchKernelGGL((sample_tiles_kernel<T, VERIFY>), tiles, dim3(kThreads), 0, s, a);
-  hipLaunchKernelGGL((sample_rows_kernel<T, VERIFY>), dim3((unsigned)a.rows), dim3(kRowThreads), 0, s, a);
+  const auto rows = a.rows > kCus ? sample_rows_kernel<T, VERIFY, 2> : sample_rows_kernel<T, VERIFY, 1>;
+  hipLaunchKernelGGL(rows, dim3((unsigned)a.rows), dim3(kRowThreads), 0, s, a);
   return hipGetLastError();
 }
 

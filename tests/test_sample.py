@@ -305,3 +305,36 @@ def test_no_rows():
     token, prob, probs = lr.sample(torch.zeros(0, 32, device=DEV), torch.zeros(0, device=DEV), want_probs=True)
     assert token.shape == (0,) and prob.shape == (0,) and probs.shape == (0, 32)
     assert lr.sample(torch.zeros(0, 3200, device=DEV), torch.zeros(0, device=DEV))[0].shape == (0,)
+
+
+def of_each_row(hows):
+    col = lambda key, other, dt: torch.tensor([h.get(key, other) for h in hows], dtype=dt, device=DEV)  # noqa: E731
+    f = torch.float32
+    return dict(temperature=col("T", 1.0, f), top_k=col("k", 0, torch.int32), top_p=col("p", 1.0, f),
+                min_p=col("m", 0.0, f))
+
+
+@pytest.mark.parametrize("kind", ["noise", "model", "masked", "rising", "wide"])
+@pytest.mark.parametrize("n", [2049, 5000, 20001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_more_kept_columns_than_groups_of_columns(n, kind, dtype):
+    rng = np.random.default_rng(17)
+    hows = [dict(k=40), dict(k=200, p=0.98, T=1.2), dict(k=900), dict(p=0.9, T=0.7), dict(p=0.98, m=0.02),
+            dict(k=1023, m=0.01), dict(k=1024), dict(k=2049)]
+    B = len(hows)
+    x = values(kind, B, n, dtype, rng)
+    u = torch.from_numpy(rng.random(B).astype(np.float32))
+    got = lr.sample(x.to(DEV), u.to(DEV), **of_each_row(hows))[:2]
+    assert check(x, u.numpy(), got, hows) <= 2
+
+
+@pytest.mark.parametrize("left", [3, 60, 300, 3000])
+def test_candidates_in_few_groups_only(left):
+    rng = np.random.default_rng(23)
+    hows = [dict(k=40), dict(k=500, p=0.95), dict(p=0.9), dict(k=2500)]
+    B, n = len(hows), 40003
+    x = torch.full((B, n), -float("inf"))
+    x[:, n - 10000:n - 10000 + left] = values("noise", B, left, "fp32", rng)
+    u = torch.from_numpy(rng.random(B).astype(np.float32))
+    got = lr.sample(x.to(DEV), u.to(DEV), **of_each_row(hows))[:2]
+    assert check(x, u.numpy(), got, hows) <= 1
