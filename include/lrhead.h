@@ -348,16 +348,18 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
  * [0, 1], and a column of weight 0 is never drawn. A logit that is NaN or
  * -inf, or has a negative id, is no candidate; +inf counts as the largest
  * finite fp32. A row without candidates gives token -1 and probabilities 0.
- * Weights are good to 4e-14 and sums to 1e-12 of the mass at n = 2^17 (half
- * a unit of 2^-51, or of 2^(ceil(log2 n) - 62) for n above 2^11, per weight),
- * and do not vary from call to call.
+ * Weights are good to 2e-13 of themselves and half a unit of 2^-51, or of
+ * 2^(ceil(log2 n) - 62) for n above 2^11 (2^-46 at 2^17 columns, 2^-39 at
+ * 2^24, where the largest weighs 1); equal logits weigh the same, sums of
+ * weights are exact, and nothing varies from call to call.
  * Each setting is one value for all rows or, where its pointer is not NULL, an
  * array of B device values.
  * Requirements: 1 <= n <= 2^24, ld >= n, 0 <= B <= 2^20 and B rows of n
  * columns less than 2^37 in all (ERANGE), inputs aligned to their
  * elements, outputs and workspace to 16 bytes; the workspace has at least
  * lrhead_sample_workspace_bytes bytes (0: invalid sizes), or is NULL where
- * n <= 64, which needs none. `prob` may be NULL.
+ * n <= 64, which needs none. `prob` may be NULL. No output may overlap an input,
+ * the workspace or another output (EINVAL; the logits from the first to the last).
  */
 typedef struct {
   const float* temperature;   /* arrays, or NULL */
@@ -400,8 +402,9 @@ int lrhead_sample(int dtype, const void* logits, int64_t ld, const int32_t* idx,
  * count[b]: how many there are in all. A row without candidates accepts
  * nothing and draws -1, which count leaves out.
  * Requirements: 0 <= s <= 255, 1 <= k <= 64, n, ld and alignment as for
- * lrhead_sample, with B (s+1) rows in its place of B <= 2^20; the workspace
- * has at least lrhead_verify_workspace_bytes bytes (0: invalid sizes).
+ * lrhead_sample, with B (s+1) rows in its place of B <= 2^20, and so for
+ * overlaps; the workspace has at least lrhead_verify_workspace_bytes bytes
+ * (0: invalid sizes).
  */
 size_t lrhead_verify_workspace_bytes(int dtype, int64_t B, int s, int64_t n);
 int lrhead_verify(int dtype, const void* logits, int64_t ld, const int32_t* token,
@@ -421,13 +424,13 @@ int lrhead_verify(int dtype, const void* logits, int64_t ld, const int32_t* toke
  *                       with `add` added to the rows of tokens that occur, the
  *                       others left as they were.
  * W, dW: V x d; out, dY: N x d, all in `dtype`, token: N int32. Products and
- * sums are fp32 and rounded once; the sums' order goes by N and the tokens
- * alone, so the results do not vary from call to call. scale is finite.
+ * sums are fp32 and rounded once; the sums' order goes by the sizes and the
+ * tokens alone, so the results do not vary from call to call. scale is finite.
  * Requirements: 1 <= V < 2^31, 1 <= d <= 65536, 0 <= N <= 2^20 and N d < 2^35
- * (more may be refused, ERANGE); every pointer aligned to its elements, the workspace to 16
- * bytes, with at least lrhead_embed_grad_workspace_bytes bytes (0: invalid
- * sizes). N == 0 writes no row, but dW (zeros) unless `add`. out may not
- * overlap W, nor dW dY.
+ * (more may be refused, ERANGE); every pointer aligned to its elements, the
+ * workspace to 16 bytes, with at least lrhead_embed_grad_workspace_bytes bytes
+ * (0: invalid sizes). N == 0 writes no row, but dW (zeros) unless `add`. No
+ * output may overlap an input, nor dW the workspace (EINVAL).
  */
 int lrhead_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* token, int64_t N,
                  float scale, void* out, void* stream);

@@ -13,6 +13,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 
@@ -372,6 +373,19 @@ bool aligned_elem(const void* p, int dtype) { return reinterpret_cast<uintptr_t>
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return an && bn && x < y + bn && y < x + an;
+}
+
+// Whether one of `outs` shares a byte with another of them or with one of `ins`.
+struct Span {
+  const void* p;
+  size_t n;   // bytes; none where p is NULL
+};
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    const auto meets = [&](const Span& i) { return o->p && i.p && overlap(o->p, o->n, i.p, i.n); };
+    if (std::any_of(o + 1, outs.end(), meets) || std::any_of(ins.begin(), ins.end(), meets)) return true;
+  }
+  return false;
 }
 
 int sample_args(lrh::SampleArgs* a, int dtype, const void* logits, int64_t ld, const float* u,
@@ -750,6 +764,11 @@ int lrhead_sample(int dtype, const void* logits, int64_t ld, const int32_t* idx,
   const size_t need = lrh::sample_workspace_bytes(B, n);
   if (workspace && workspace_bytes < need)
     return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t rows = size_t(B) * 4, all = rows * size_t(n);
+  if (clash({{token, rows}, {prob, rows}, {probs, all}, {workspace, need}},
+            {{logits, (size_t(B - 1) * size_t(ld) + size_t(n)) * elem_bytes(dtype)}, {idx, all}, {u, rows},
+             {how->temperature, rows}, {how->top_k, rows}, {how->top_p, rows}, {how->min_p, rows}}))
+    return fail(LRHEAD_EINVAL, "an output or the workspace overlaps an input or another output");
   a.idx = idx;
   a.token = token;
   a.prob = prob;
@@ -783,6 +802,12 @@ int lrhead_verify(int dtype, const void* logits, int64_t ld, const int32_t* toke
   const size_t need = lrh::verify_workspace_bytes(B, s, n);
   if (workspace_bytes < need)
     return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t seqs = size_t(B) * 4, rows = seqs * size_t(s + 1), places = seqs * size_t(s);
+  if (clash({{out_token, rows}, {count, seqs}, {workspace, need}},
+            {{logits, ((size_t(B) * size_t(s + 1) - 1) * size_t(ld) + size_t(n)) * elem_bytes(dtype)},
+             {token, places}, {idx, places * size_t(k)}, {probs, places * size_t(k)}, {length, seqs}, {u, rows},
+             {how->temperature, seqs}, {how->top_k, seqs}, {how->top_p, seqs}, {how->min_p, seqs}}))
+    return fail(LRHEAD_EINVAL, "an output or the workspace overlaps an input or another output");
   a.token = out_token;
   lrh::VerifyArgs v{};
   v.s = s;
@@ -805,7 +830,7 @@ int lrhead_embed(int dtype, const void* W, int64_t V, int64_t d, const int32_t* 
   if (!aligned_elem(W, dtype) || !aligned_elem(out, dtype) || !aligned4(token))
     return fail(LRHEAD_EALIGN, "W, out and token must be aligned to their elements");
   const size_t row = size_t(d) * elem_bytes(dtype);
-  if (overlap(out, size_t(N) * row, W, size_t(V) * row) || overlap(out, size_t(N) * row, token, size_t(N) * 4))
+  if (clash({{out, size_t(N) * row}}, {{W, size_t(V) * row}, {token, size_t(N) * 4}}))
     return fail(LRHEAD_EINVAL, "out overlaps W or token");
   LRH_HIP(lrh::launch_embed(dtype, W, V, d, token, N, scale, out, static_cast<hipStream_t>(stream)),
           "embedding launch");
@@ -830,8 +855,8 @@ int lrhead_embed_grad(int dtype, const void* dY, const int32_t* token, int64_t N
     const size_t need = lrh::embed_grad_workspace_bytes(dtype, V, d, N);
     if (workspace_bytes < need)
       return fail(LRHEAD_EWORKSPACE, "workspace holds %zu bytes, needs %zu", workspace_bytes, need);
-    if (overlap(dW, size_t(V) * row, dY, size_t(N) * row) || overlap(dW, size_t(V) * row, token, size_t(N) * 4))
-      return fail(LRHEAD_EINVAL, "dW overlaps dY or token");
+    if (clash({{dW, size_t(V) * row}, {workspace, need}}, {{dY, size_t(N) * row}, {token, size_t(N) * 4}}))
+      return fail(LRHEAD_EINVAL, "dW or the workspace overlaps dY or token, or each other");
   }
   LRH_HIP(lrh::launch_embed_grad(dtype, dY, token, N, V, d, scale, add != 0, dW, workspace,
                                  static_cast<hipStream_t>(stream)),

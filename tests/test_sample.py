@@ -338,3 +338,23 @@ def test_candidates_in_few_groups_only(left):
     u = torch.from_numpy(rng.random(B).astype(np.float32))
     got = lr.sample(x.to(DEV), u.to(DEV), **of_each_row(hows))[:2]
     assert check(x, u.numpy(), got, hows) <= 1
+
+
+@pytest.mark.parametrize("how", ["whole", "k300", "p90", "m05", "greedy"])
+def test_the_longest_rows(how):
+    """2^24 columns, a token every 2^-24 of the mass: the draw lies where u says to the sums' accuracy."""
+    rng = np.random.default_rng(31)
+    n, how = 1 << 24, SETTINGS[how]
+    x = torch.from_numpy(rng.standard_normal((2, n), dtype=np.float32) * 2.5).to(torch.bfloat16)
+    x[1, :n // 2] = -float("inf")
+    u = torch.tensor([0.37, 0.9])
+    token, prob, _ = lr.sample(x.to(DEV), u.to(DEV), **settings_args(how))
+    for b in range(2):
+        w, _ = weights(x[b].float().double().numpy(), **how)
+        c, t = np.cumsum(w), int(token[b])
+        # half a unit of 2^-38 for each weight, on both sides of a border, and 64-bit sums over 2^24 columns; as much
+        # again, of 0.9 of the mass, for the border of top_p
+        off = 2 * (2 * n * 2.0 ** -39 / c[-1] + 1e-8) / 0.9
+        place = float(u[b])
+        assert w[t] > 0 and c[t] / c[-1] >= place - off and (c[t] - w[t]) / c[-1] <= place + off
+        assert abs(float(prob[b]) - w[t] / c[-1]) <= w[t] / c[-1] * (2.0 ** -24 + off) + 2.0 ** -39 / c[-1]

@@ -96,7 +96,8 @@ def test_workspace_bytes_are_host_arithmetic():
     assert lib.lrhead_sample_workspace_bytes(BF16, 1, 0) == 0 and lib.lrhead_sample_workspace_bytes(5, 1, 9) == 0
     assert lib.lrhead_verify_workspace_bytes(BF16, 4, 255, 151936) > lib.lrhead_verify_workspace_bytes(BF16, 4, 0, 151936) > 0
     assert lib.lrhead_verify_workspace_bytes(BF16, 4, 256, 100) == 0 and lib.lrhead_verify_workspace_bytes(BF16, -1, 2, 9) == 0
-    assert lib.lrhead_embed_grad_workspace_bytes(FP32, 100, 8, 50) > 50 * 8
+    assert lib.lrhead_embed_grad_workspace_bytes(FP32, 100, 8, 5000) > 5000 * 8
+    assert lib.lrhead_embed_grad_workspace_bytes(FP32, 100, 8, 50) > 0
     assert lib.lrhead_embed_grad_workspace_bytes(FP32, 100, 0, 50) == 0 and lib.lrhead_embed_grad_workspace_bytes(FP32, 9, 8, 0) > 0
 
 
@@ -156,3 +157,41 @@ def test_bindings_refuse_what_does_not_fit_together():
                 dict(out=f(8, 5).t()), dict(dY=f(8, 3).t()), dict(dY=f(3, 8).half()), dict(scale=float("inf"))]:
         with pytest.raises(ValueError):
             lr.embed_grad(bad.pop("dY", y), bad.pop("token", i(3)), bad.pop("V", 5), **bad)
+
+
+APART = [0x1000000 * (i + 1) for i in range(16)]   # stand-ins with 16 MiB between them
+
+
+@pytest.mark.parametrize("a,b", [(o, i) for o in ("token", "prob", "probs", "ws") for i in
+                                 ("logits", "idx", "u", "temperature", "top_k", "top_p", "min_p", "token", "prob", "probs",
+                                  "ws") if o != i])
+def test_sample_refuses_outputs_over_inputs(a, b):
+    names = ["logits", "idx", "u", "temperature", "top_k", "top_p", "min_p", "token", "prob", "probs", "ws"]
+    at = dict(zip(names, APART))
+    at[a] = at[b]
+    settings = {k: at.pop(k) for k in ("temperature", "top_k", "top_p", "min_p")}
+    assert sample(**at, n=64, ld=64, B=9, how=how(**settings)) == EINVAL
+
+
+def test_sample_refuses_an_output_among_the_last_row_s_logits():
+    at = dict(logits=APART[0], u=APART[1], token=APART[2], prob=APART[3], ws=APART[4])
+    assert sample(**{**at, "token": APART[0] + 4 * (2 * 2000 + 996)}, ld=2000, B=3, n=1000) == EINVAL
+    assert sample(**{**at, "ws": APART[0] + 4 * (2 * 2000 + 996)}, ld=2000, B=3, n=1000) == EINVAL
+
+
+@pytest.mark.parametrize("a,b", [(o, i) for o in ("out", "count", "ws") for i in
+                                 ("logits", "token", "idx", "probs", "length", "u", "temperature", "top_k", "top_p", "min_p",
+                                  "out", "count", "ws") if o != i])
+def test_verify_refuses_outputs_over_inputs(a, b):
+    names = ["logits", "token", "idx", "probs", "length", "u", "temperature", "top_k", "top_p", "min_p", "out", "count", "ws"]
+    at = dict(zip(names, APART))
+    at[a] = at[b]
+    settings = {k: at.pop(k) for k in ("temperature", "top_k", "top_p", "min_p")}
+    assert verify(**at, B=9, how=how(**settings)) == EINVAL
+
+
+@pytest.mark.parametrize("a,b", [("dW", "dY"), ("dW", "token"), ("dW", "ws"), ("ws", "dY"), ("ws", "token")])
+def test_embed_grad_refuses_outputs_over_inputs(a, b):
+    at = dict(zip(["dY", "token", "dW", "ws"], APART))
+    at[a] = at[b]
+    assert embed_grad(**at) == EINVAL
