@@ -348,10 +348,10 @@ int lrhead_reorder(const lrhead_state_t* states, int n_states, const int32_t* pa
  * [0, 1], and a column of weight 0 is never drawn. A logit that is NaN or
  * -inf, or has a negative id, is no candidate; +inf counts as the largest
  * finite fp32. A row without candidates gives token -1 and probabilities 0.
- * Weights are good to 2e-13 of themselves and half a unit of 2^-51, or of
- * 2^(ceil(log2 n) - 62) for n above 2^11 (2^-46 at 2^17 columns, 2^-39 at
- * 2^24, where the largest weighs 1); equal logits weigh the same, sums of
- * weights are exact, and nothing varies from call to call.
+ * With a largest weight of 1, weights and their sums are good to 2e-13 of
+ * themselves and half a unit of 2^-51, or of 2^(ceil(log2 n) - 62) for n above
+ * 2^11 (2^-45 at 2^17 columns, 2^-38 at 2^24), per weight; equal logits weigh
+ * the same, and nothing varies from call to call.
  * Each setting is one value for all rows or, where its pointer is not NULL, an
  * array of B device values.
  * Requirements: 1 <= n <= 2^24, ld >= n, 0 <= B <= 2^20 and B rows of n

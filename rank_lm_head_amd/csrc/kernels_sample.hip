@@ -11,18 +11,22 @@
 //
 // Weights are held in 64 bits: as doubles where sums have no common reference
 // yet, and otherwise as integers, w 2^S rounded, whose sums do not depend on
-// their order. A polynomial of degree 9 gives 2^f to 4e-14, so that a random
-// number, which falls between two sums, is held against sums good to 1e-13.
+// their order. A single weight is good to 4e-14, the stream's sums to 2e-13 (a
+// shorter exponential, since they are what a large call computes most of).
 //
 // sample_tiles_kernel reads the logits once: a wave takes 2048 columns and
-// leaves their largest logit, those of the tile's eight groups of 256, and,
-// where the row's settings need the whole mass, their sum of weights.
+// leaves their largest logit, of each of the tile's groups of 256 columns the
+// largest logit, its place and that of the next best chunk of 16 bytes, and,
+// where the row's settings need the whole mass, the sum of weights.
 // sample_rows_kernel has a block per row. With a bound that at least k groups'
-// maxima reach, it reads again only the groups that hold what passes the
+// maxima reach, it reads again only the chunks that hold what passes the
 // bound. Where that does not settle the row (flat rows under top_p, long
 // top_k), it splits the whole row by value until the border is known.
-// What bounds a large call is the one read of the logits; a small one, the
-// two launches.
+// What bounds a large call is the one read of the logits and, for rows that
+// need their mass, the 64-bit exponentials (half rate); a small one, the
+// chain of dependent steps in a row's block. 256 rows of 151936 columns, bf16,
+// tiles / rows in us: top_k 20 16 / 13, top_k 200 18 / 23, top_p 0.9 38 / 15,
+// no setting 32 / 7, a flat row's top_p 38 / 129.
 #include <algorithm>
 #include <climits>
 
