@@ -358,3 +358,24 @@ def test_the_longest_rows(how):
         place = float(u[b])
         assert w[t] > 0 and c[t] / c[-1] >= place - off and (c[t] - w[t]) / c[-1] <= place + off
         assert abs(float(prob[b]) - w[t] / c[-1]) <= w[t] / c[-1] * (2.0 ** -24 + off) + 2.0 ** -39 / c[-1]
+
+
+@pytest.mark.parametrize("kind", ["model", "noise", "flat", "masked", "ties"])
+@pytest.mark.parametrize("n,dtype", [(700, "fp32"), (9001, "bf16"), (9001, "fp32"), (40003, "bf16")])
+def test_large_batches_give_what_small_ones_do(n, dtype, kind):
+    """More rows than compute units, under every setting, against the same rows by themselves; some against the formula."""
+    rng = np.random.default_rng(41)
+    names = list(SETTINGS)
+    B = 20 * len(names)
+    hows = [SETTINGS[names[b % len(names)]] for b in range(B)]
+    x = values(kind, B, n, dtype, rng)
+    u = torch.from_numpy(rng.random(B).astype(np.float32))
+    args = of_each_row(hows)
+    got = lr.sample(x.to(DEV), u.to(DEV), **args)[:2]
+    for b0 in range(0, B, 100):
+        part = lr.sample(x[b0:b0 + 100].to(DEV), u[b0:b0 + 100].to(DEV), **{k: v[b0:b0 + 100].clone() for k, v in args.items()})
+        for whole, one in zip(got, part):
+            assert torch.equal(whole[b0:b0 + 100], one)
+    first = len(names)   # a row of each; flat rows and ties lie on borders by themselves
+    undecided = check(x[:first], u[:first].numpy(), [t[:first] for t in got], hows[:first])
+    assert undecided <= (first // 2 if kind in ("flat", "ties") else 2)

@@ -255,3 +255,29 @@ def test_a_drafter_s_loop():
     after = lr.embed(E, got[0])                           # empty slots give rows of zeros
     assert after.shape == (B, s + 1, d) and after[got[0] < 0].abs().sum() == 0
     head.close()
+
+
+@pytest.mark.parametrize("n,dtype", [(700, "fp32"), (9001, "bf16"), (20001, "fp32")])
+def test_large_batches_give_what_small_ones_do(n, dtype):
+    """More rows than compute units, under every setting, against the same sequences a few at a time."""
+    rng = np.random.default_rng(43)
+    names = list(SETTINGS)
+    B, s, each = 5 * len(names), 4, 20
+    x = values("model", B * (s + 1), n, dtype, rng).view(B, s + 1, n)
+    token, ids, q = drafts(x, 16, rng)
+    u = rng.random((B, s + 1)).astype(np.float32)
+    length = rng.integers(0, s + 1, B).astype(np.int32)
+    how = [SETTINGS[names[b % len(names)]] for b in range(B)]
+    col = lambda key, other, dt: torch.tensor([h.get(key, other) for h in how], dtype=dt, device=DEV)  # noqa: E731
+    f = torch.float32
+    args = dict(temperature=col("T", 1.0, f), top_k=col("k", 0, torch.int32), top_p=col("p", 1.0, f),
+                min_p=col("m", 0.0, f))
+    got = run(x, token, ids, q, u, length, args)
+    for b0 in range(0, B, each):
+        b = slice(b0, b0 + each)
+        part = run(x[b], token[b].copy(), ids[b].copy(), q[b].copy(), u[b].copy(), length[b].copy(),
+                   {k: v[b].clone() for k, v in args.items()})
+        assert torch.equal(got[0][b], part[0]) and torch.equal(got[1][b], part[1])
+    first = slice(0, len(names))
+    assert check(x[first], token[first], ids[first], q[first], u[first], length[first], [t[first] for t in got],
+                 how[first]) <= 2
