@@ -251,3 +251,22 @@ def test_autograd_refuses_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, torch.zeros(3, 8, device=DEV))
+
+
+@pytest.mark.parametrize("N", [3, 300, 900, 17000])
+def test_gradient_past_32_bits(N):
+    """A matrix of 2.9e9 elements, 5.7 GB, which held other values."""
+    V, d = 72000, 40000
+    rng = np.random.default_rng(N)
+    dY = torch.from_numpy(rng.standard_normal((min(N, 64), d)).astype(np.float32)).bfloat16().to(DEV)
+    dY = dY.repeat(-(-N // len(dY)), 1)[:N].contiguous()
+    t = rng.choice(V, N, replace=False).astype(np.int32)
+    t[0] = V - 1 if V - 1 not in t else t[0]
+    torch.full((V, d), 7.0, dtype=torch.bfloat16, device=DEV)      # freed: the result may take its place
+    dW = lr.embed_grad(dY, torch.from_numpy(t).to(DEV), V)
+    at = torch.from_numpy(t).long().to(DEV)
+    for i in range(0, N, 2000):
+        assert torch.equal(dW[at[i:i + 2000]], dY[i:i + 2000])     # one row a token: the row itself
+        dW[at[i:i + 2000]] = 0
+    for v in range(0, V, 8000):
+        assert not dW[v:v + 8000].any()

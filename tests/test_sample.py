@@ -379,3 +379,16 @@ def test_large_batches_give_what_small_ones_do(n, dtype, kind):
     first = len(names)   # a row of each; flat rows and ties lie on borders by themselves
     undecided = check(x[:first], u[:first].numpy(), [t[:first] for t in got], hows[:first])
     assert undecided <= (first // 2 if kind in ("flat", "ties") else 2)
+
+
+def test_rows_past_32_bits():
+    """Rows more than 2^31 elements apart, and settings that read them again."""
+    n, ld = 50000, (1 << 31) + 5
+    rng = np.random.default_rng(47)
+    x = values("noise", 3, n, "bf16", rng)
+    big = torch.empty(2 * ld + n, dtype=torch.bfloat16, device=DEV).as_strided((3, n), (ld, 1))
+    big.copy_(x.to(DEV))
+    u = torch.from_numpy(rng.random(3).astype(np.float32)).to(DEV)
+    for how in SETTINGS.values():
+        for far, near in zip(lr.sample(big, u, **settings_args(how))[:2], lr.sample(x.to(DEV), u, **settings_args(how))[:2]):
+            assert torch.equal(far, near)
