@@ -684,8 +684,11 @@ __device__ __forceinline__ uint64_t list_find(Range r, int n, uint64_t mask, boo
   return hit ? rl64(it.key, __ffsll(hit) - 1) : r.lo;
 }
 
-// The groups' maxima of a row as order keys (0: no candidate), in every wave:
-// lane by lane every 64th. Of more groups than kHeldGroups, the largest of
+// A maximum as an order key: 0 without a candidate, and one key for -0 and +0, which tie.
+__device__ __forceinline__ uint32_t max_key(float m) { return m > neg_inf() ? order_key(m + 0.0f) : 0; }
+
+// The groups' maxima of a row as max_key has them, in every wave: lane by lane
+// every 64th. Of more groups than kHeldGroups, the largest of
 // several.
 constexpr int kHeld = 16, kHeldGroups = kHeld * kWave;
 struct GroupMax {
@@ -708,7 +711,7 @@ struct GroupMax {
       at[i] = a.gat[g];
     }
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) v[e] = x[e] > neg_inf() ? order_key(x[e]) : 0;
+    for (int e = 0; e < kHeld; ++e) v[e] = max_key(x[e]);
   }
   __device__ __forceinline__ uint32_t most() const {
     uint32_t m = 0;
@@ -844,7 +847,7 @@ struct RowCtx {
         for (int q = 0; q < 8; ++q) m[q & 1] = fmaxf(m[q & 1], x[q]);
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) s.set[tid + q * kRowThreads] = m[q] > neg_inf() ? order_key(m[q]) : 0;
+      for (int q = 0; q < 2; ++q) s.set[tid + q * kRowThreads] = max_key(m[q]);
       __syncthreads();
     }
     GroupMax g;
@@ -1397,11 +1400,11 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
       r.mass = all;
     } else {
       way = 3;
-      // least logit that min_p can leave in, a little below
+      // least logit that min_p can leave in, a little below; the largest logit reaches it
       uint32_t floor_key = 0;
       if (h.least > -__builtin_inf()) {
         const double f = (double)m + h.least / h.c;   // c = 0: -inf or NaN
-        if (f > -(double)__FLT_MAX__) floor_key = order_key((float)(f - (fabs(f) + fabs((double)m)) * 1e-6));
+        if (f > -(double)__FLT_MAX__) floor_key = min(max_key((float)(f - (fabs(f) + fabs((double)m)) * 1e-6)), top);
       }
       int k = h.top_k ? h.top_k : h.top_p < 1.0 ? kFirstK : INT_MAX;   // of min_p alone: no bound but its own
       const int held = min(groups, kHeldGroups);
@@ -1477,8 +1480,10 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
           }
         }
         const int at = wave_draw(w, mass, col, u, n, s.items);
-        drawn = __builtin_amdgcn_readlane(col, at);
-        kept_x = (double)rl64(k.w, at);
+        if (at >= 0) {   // the largest logit has weight
+          drawn = __builtin_amdgcn_readlane(col, at);
+          kept_x = (double)rl64(k.w, at);
+        }
       }
       r.mass = k.mass;
     }
