@@ -1489,7 +1489,10 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
     }
   } else {
     // the list: top_k's border, top_p's, and the column drawn, each by
-    // list_find; the tiles' borders are known
+    // list_find; the tiles' borders are known. What is kept is in the list, and
+    // so not below its bound, also where top_k leaves the whole list in: a
+    // drafted token need not be in it.
+    if (way == 1) r.thr = max(r.thr, (uint64_t)bound << 32);
 #pragma unroll 1
     for (int stage = way == 1 ? 0 : 2; stage < 3; ++stage) {
       Range f{max((uint64_t)bound << 32, (uint64_t)1), cand_key(m, 0), 0, 0};
