@@ -394,10 +394,11 @@ int lrhead_sample(int dtype, const void* logits, int64_t ld, const int32_t* idx,
  *   where that has no mass) takes its place, and the sequence ends;
  *   after length[b] accepted ones, the token drawn from p of the next row is
  *   added.
- * Draws go by u[b, s] and by column order, as in lrhead_sample (u: B x (s+1)
- * fp32). idx == NULL and probs == NULL (k ignored): the drafted token had
- * probability 1 (greedy drafting). length (B int32, held to [0, s]; NULL: s):
- * the drafted tokens that there are; rows behind row length[b] are not read.
+ * Draws go by u[b, s] and by column order, as in lrhead_sample. u (B x (s+1)
+ * fp32) is held to [0, 1] everywhere, NaN to 0: 0 accepts any token that p has.
+ * idx == NULL and probs == NULL (k ignored): the drafted token had probability
+ * 1 (greedy drafting). length (B int32, held to [0, s]; NULL: s): the drafted
+ * tokens that there are; rows behind row length[b] are not read.
  * out_token (B x (s+1)): the accepted tokens, the drawn one, and -1 behind it;
  * count[b]: how many there are in all. A row without candidates accepts
  * nothing and draws -1, which count leaves out.

@@ -223,9 +223,10 @@ __device__ __forceinline__ uint64_t to_int(double w, int bits) {   // w 2^bits, 
 __device__ __forceinline__ uint64_t share_of(uint64_t mass, double p) {
   return max((uint64_t)ceil(p * (double)mass), (uint64_t)1);
 }
+__device__ __forceinline__ float hold(float u) { return fminf(fmaxf(u, 0.f), 1.f); }   // NaN: 0
 // The place of u in the mass.
 __device__ __forceinline__ uint64_t place_of(uint64_t mass, float u) {
-  const double t = (double)fminf(fmaxf(u, 0.f), 1.f) * (double)mass;   // NaN: 0
+  const double t = (double)hold(u) * (double)mass;
   return min((uint64_t)t, mass - 1);
 }
 
@@ -1324,7 +1325,7 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
     if (check) {   // in every wave, a lane per entry of the list
       const int64_t at = seq * (a.per - 1) + j;
       x = a.drafted[at];
-      ux = a.u[seq * a.u_ld + j];
+      ux = hold(a.u[seq * a.u_ld + j]);
       list_k = a.list ? a.k : 1;
       if (lane < list_k) {
         id = a.list ? a.list[at * a.k + lane] : x;

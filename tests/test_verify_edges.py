@@ -1,11 +1,12 @@
-"""Verification where a drafted token is one that the target's settings leave out."""
+"""Verification at its edges: drafted tokens that the target's settings leave out, u outside [0, 1)."""
 import numpy as np
 import pytest
 import torch
 
 import rank_lm_head_amd as lr
 from sampling_ref import weights
-from test_sample import DEV, DT, settings_args, values
+from test_sample import DEV, DT, SETTINGS, settings_args, values
+from test_verify import check, drafts, run
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,40 @@ def test_tokens_behind_top_k_are_refused(n, dtype):
             for b in range(B):
                 w, _ = weights(x[b, 0].float().double().numpy(), k=int(ks[b]), **how)
                 assert w[int(out[b, 0])] > 0 and out[b, 0] != int(token[b, 0])
+
+
+OUTSIDE = [0.0, -0.0, -3.0, -float("inf"), float("nan"), 1.0, 2.0, float("inf")]
+
+
+@pytest.mark.parametrize("how", ["whole", "greedy", "k20p", "k300", "p90", "p999", "m05"])
+@pytest.mark.parametrize("n", [30, 3000, 20011])
+@pytest.mark.parametrize("lists", [False, True])
+def test_the_ends_of_the_acceptance_numbers(n, how, lists):
+    """u below 0 and NaN accept as 0 does: what has weight, and no token left out, masked or outside the vocabulary."""
+    rng = np.random.default_rng(n)
+    B, s = len(OUTSIDE), 7
+    x = values("noise", B * (s + 1), n, "fp32", rng).view(B, s + 1, n)
+    x[:, :, 5] = -float("inf")
+    order = np.argsort(-x.numpy(), axis=2, kind="stable")
+    token, ids, q = drafts(x, 16, rng)
+    token[:, 0] = order[:, 0, 0]                       # accepted, unless u q passes p
+    for b in range(B):                                 # what must not be accepted, at each of the places behind
+        j = 1 + b % 3
+        token[b, j] = (5, -1, n)[b % 3]
+        ids[b, j, 0] = token[b, j]
+    token[:, 4] = order[:, 4, n - 2]                   # the least one
+    ids[:, 4, 0] = token[:, 4]
+    u = rng.random((B, s + 1)).astype(np.float32)
+    u[:, :s] = np.array(OUTSIDE, np.float32)[:, None]
+    if not lists:
+        ids = q = None
+    got = run(x, token, ids, q, u, None, settings_args(SETTINGS[how]))
+    held = u.copy()
+    held[:, :s] = np.clip(np.nan_to_num(held[:, :s], nan=0.0), 0.0, 1.0)
+    # three rows have u = 1, and greedy ones without lists p = q = 1: 1 < 1 lies on the border itself, and refuses
+    undecided = 3 if how == "greedy" and not lists else 2
+    assert check(x, token, ids, q, held, None, got, SETTINGS[how]) <= undecided
+    if undecided == 3:
+        assert got[1][5:].tolist() == [1, 1, 1] and np.array_equal(got[0][5:, 0].cpu().numpy(), token[5:, 0])
+    for b in range(B):                                 # none passes the place that has no chance
+        assert got[1][b] <= 2 + b % 3
