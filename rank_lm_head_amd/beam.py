@@ -5,6 +5,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .head import _DTYPES, _on
@@ -84,10 +85,11 @@ def reorder(states, parent: torch.Tensor, *, length: torch.Tensor | None = None,
         raise ValueError("parent must be a contiguous int32 device tensor [B, nb]")
     dev = parent.device
     B, nb = parent.shape
+    given = ()
     if out is None:
         out = [None] * len(states)
     else:
-        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        given = out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != len(states):
             raise ValueError("out must have one tensor per state")
     if length is not None and (length.device != dev or length.dtype != torch.int32 or length.shape != (B,)
@@ -121,4 +123,6 @@ def reorder(states, parent: torch.Tensor, *, length: torch.Tensor | None = None,
                                             None if length is None else length.data_ptr(), B, m, nb, stream)
             if rc:
                 _lib.check(rc, "lrhead_reorder")
+            if given:
+                increment_version(given)   # so that autograd knows of the change
     return out[0] if single else out

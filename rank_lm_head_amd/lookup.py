@@ -5,6 +5,7 @@ import math
 
 import torch
 from torch.autograd.forward_ad import unpack_dual
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .head import _DTYPES, _on
@@ -72,6 +73,8 @@ def embed_grad(dY: torch.Tensor, token: torch.Tensor, V: int, *, scale: float = 
                                    dW.data_ptr(), None if ws is None else ws.data_ptr(), nbytes, stream)
         if rc:
             _lib.check(rc, "lrhead_embed_grad")
+    if out is not None:
+        increment_version(out)   # so that autograd knows of the change
     return dW
 
 
