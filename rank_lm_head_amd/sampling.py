@@ -120,6 +120,8 @@ def verify(logits: torch.Tensor, token: torch.Tensor, u: torch.Tensor, *, idx: t
         if idx.dim() != 3:
             raise ValueError(f"idx must be ({B}, {s}, k), not {tuple(idx.shape)}")
         k = idx.shape[2]
+        if k < 1:   # an empty tensor has no address, and the C call would take the lists as left out
+            raise ValueError("idx must have a column at least")
     for name, t, dtype, shape in (("token", token, torch.int32, (B, s)), ("u", u, torch.float32, (B, m)),
                                   ("idx", idx, torch.int32, (B, s, k)), ("probs", probs, torch.float32, (B, s, k)),
                                   ("length", length, torch.int32, (B,))):

@@ -89,3 +89,12 @@ def test_the_ends_of_the_acceptance_numbers(n, how, lists):
         assert got[1][5:].tolist() == [1, 1, 1] and np.array_equal(got[0][5:, 0].cpu().numpy(), token[5:, 0])
     for b in range(B):                                 # none passes the place that has no chance
         assert got[1][b] <= 2 + b % 3
+
+
+@pytest.mark.parametrize("s", [0, 3])
+def test_lists_without_a_column_are_refused(s):
+    """They are no lists left out: those make the drafted tokens ones of probability 1."""
+    x, u = torch.zeros(2, s + 1, 100, device=DEV), torch.zeros(2, s + 1, device=DEV)
+    none = torch.zeros(2, s, 0, device=DEV)
+    with pytest.raises(ValueError, match="column"):
+        lr.verify(x, torch.zeros(2, s, dtype=torch.int32, device=DEV), u, idx=none.int(), probs=none)
