@@ -563,6 +563,7 @@ struct Lds {
   int four[kList];                 // places of four columns to look at
   int ask[2 * kRowThreads];        // groups to read
   uint32_t set[2 * kRowThreads];   // maxima of strided sets of columns
+  uint32_t held[2 * kRowThreads];  // of a row of several windows of groups, the joint maxima
   Item items[kWave];
   uint64_t sum[kRowWaves];
   uint64_t win_before[kRowWaves];
@@ -862,7 +863,8 @@ struct RowCtx {
   // below the bound has its candidates in the chunk of its maximum; the others
   // are read, a wave on eight of them at a time. That gives the places of four
   // neighbouring columns with one that reaches the bound, or nearly only
-  // these, which are then looked at one by one.
+  // these, which are then looked at one by one. Of a row of several windows of
+  // groups, g holds the last one afterwards.
   __device__ __forceinline__ int gather(GroupMax& g, uint32_t bound) {
     constexpr int kAtOnce = 8, kOfLast = 1 << 30, EP = Elems<T>::n;
     static_assert(kGroup == 4 * kWave, "a lane has four columns of a group");
@@ -1347,6 +1349,10 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) g.v[e] = max(g.v[e], more.v[e]);
   }
+  if (groups > kHeldGroups && wave_id() == 0) {
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) s.held[e * kWave + lane] = g.v[e];
+  }
   const uint32_t top = g.most();
   const bool none = !top;
   const float m = none ? neg_inf() : __uint_as_float(order_key_inv(top));
@@ -1448,6 +1454,10 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
         }
         if (k >= kThirdK || flat) break;
         k = k == kFirstK && few ? kSecondK : kThirdK;
+        if (groups > kHeldGroups) {
+#pragma unroll
+          for (int e = 0; e < kHeld; ++e) g.v[e] = s.held[e * kWave + lane];
+        }
       }
       if (way == 3 && !(h.mass() && r.keep_row(all))) r.split_row(all);
     }
