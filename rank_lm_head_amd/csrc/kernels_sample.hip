@@ -1424,7 +1424,7 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS * kRowWaves / 4) sample_ro
         // (256 rows of 5000 columns, bf16, top_p 0.9: 31 -> 19 us; 64 of 1000, top_k 20: 19 -> 12;
         // 1024 of 32003, top_k 200: 256 -> 71). Of mostly empty groups a list
         // may hold all candidates, and is tried first.
-        const bool finer = (!bound || (held < 2 * k && k <= kWave)) && k < INT_MAX && a.n > kWave;
+        const bool finer = (!bound || (k <= kWave && held < 2 * k)) && k < INT_MAX && a.n > kWave;
         if (finer && full) bound = r.fine_bound(k, top, made);
         // all that can be kept is in a list that reaches down to top_k columns or to min_p
         bool enough = h.top_k || !bound || bound <= floor_key;
