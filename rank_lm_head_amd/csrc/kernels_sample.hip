@@ -25,8 +25,10 @@
 // What bounds a large call is the one read of the logits and, for rows that
 // need their mass, the 64-bit exponentials (half rate); a small one, the
 // chain of dependent steps in a row's block. 256 rows of 151936 columns, bf16,
-// tiles / rows in us: top_k 20 16 / 13, top_k 200 18 / 23, top_p 0.9 38 / 15,
-// no setting 32 / 7, a flat row's top_p 38 / 129.
+// tiles / rows in us: top_k 20 17 / 12, top_k 200 17 / 21, top_p 0.9 at T = 0.8
+// 39 / 15, no setting 32 / 7, top_p 0.9 of noise 40 / 110, of nearly equal
+// logits 39 / 395, top_k 2000 17 / 305. With the high logits side by side, of
+// which a group's maximum shows one, lists are longer: 17 / 18, 17 / 24, 39 / 20.
 #include <algorithm>
 #include <climits>
 
@@ -89,8 +91,8 @@ struct Exp2 {
 // addition of 1.5 2^47, and the rest formed by one fma without rounding; the
 // maximum's weight is 1, without an error, so that ties have equal masses
 // whatever their tile. Per column this takes 11 64-bit instructions instead of
-// 16, which bound rows that need their mass (256 x 151936 bf16: 39 us with the polynomial of
-// degree 9).
+// 16, which bound rows that need their mass (256 x 151936 bf16, no setting: 32.0
+// us, and 39.2 with the polynomial of degree 9).
 __constant__ const double kPow32[32] = {
     1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
     1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
